@@ -72,7 +72,8 @@ typedef enum tp_status {
   TP_ERR_WORKSPACE_TOO_SMALL = 9,   /* workspace NULL or below the query       */
   TP_ERR_BAD_ALIASING = 10,         /* partially overlapping in/out buffers    */
   TP_ERR_BAD_FLAGS = 11,            /* unknown a_flags value                   */
-  TP_ERR_HIP = 12                   /* a HIP runtime call or launch failed     */
+  TP_ERR_HIP = 12,                  /* a HIP runtime call or launch failed     */
+  TP_ERR_BAD_VALUE = 13             /* a scalar argument outside its range     */
 } tp_status;
 
 /* Element types of floating-point operands. */
@@ -451,6 +452,75 @@ tp_status tp_qgemm_w4a8_prequantized(const int8_t* qa, int64_t ldqa, const float
                                      int64_t m, int64_t n, int64_t k, void* c, tp_dtype c_dtype,
                                      int64_t ldc, void* workspace, size_t workspace_bytes,
                                      hipStream_t stream);
+
+/* out_kind of tp_rmsnorm_rotate. */
+#define TP_NORM_OUT_I8 0   /* int8 codes [m, k] and fp32 scales [m] */
+#define TP_NORM_OUT_BF16 1 /* bf16 rows [m, k]                      */
+
+/*
+ * tp_rmsnorm_rotate -- the input of a block's projections, fused: the residual
+ * addition, the RMS norm, the rotation and the quantization of whole rows in
+ * one pass (TensorFold pull request #948, first comment: RMSNorm and the
+ * residual among the row kernels around the projections; tensai docs,
+ * "画像生成", section "GPU": each product's activations are quantized on the
+ * device).
+ *
+ *   t[r, j]   residual given: fp32(x + residual) rounded once more (nearest
+ *             even) to s_dtype, which is what sum_out holds; else x itself.
+ *   h[r, j]   t[r, j] * gamma[j] / sqrt(mean_j(t[r, j]^2) + eps)
+ *   y         a_flags TP_A_ROTATE: h . blockdiag(Q); TP_A_PREROTATED: h.
+ *             TP_NORM_OUT_I8: int8 [m, k] (row pitch ldy bytes) and scales
+ *             fp32 [m], the codes and scales that tp_quantize_rows_int8 defines
+ *             for these rows, in fp64 throughout: h is not rounded before it is
+ *             rotated. TP_NORM_OUT_BF16: bf16 [m, k] (row pitch ldy elements),
+ *             fp32 arithmetic, rounded once; scales is not used (may be NULL).
+ *
+ *   x         [m, k], x_dtype, row pitch ldx.
+ *   residual  NULL, or [m, k], s_dtype, row pitch ldr; then sum_out [m, k],
+ *             s_dtype, row pitch ldsum, is required: the new residual stream.
+ *             sum_out may be residual or x itself (same pointer, type and
+ *             pitch); any other overlap is refused. With residual NULL,
+ *             sum_out must be NULL.
+ *   gamma     [k], g_dtype, contiguous, 16-byte aligned; NULL: all ones.
+ *   eps       positive and finite.
+ *   k at most 16384 (a row sits in the registers of one workgroup). A row of
+ *   zeros gives codes 0 and scale 0, or zeros.
+ */
+tp_status tp_rmsnorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, const void* residual, int64_t ldr,
+                            void* sum_out, int64_t ldsum, tp_dtype s_dtype, const void* gamma,
+                            tp_dtype g_dtype, double eps, int a_flags, int64_t m, int64_t k, int out_kind,
+                            void* y, int64_t ldy, float* scales, hipStream_t stream);
+
+/*
+ * tp_rmsnorm_rotate_backward -- the gradients of tp_rmsnorm_rotate, the
+ * quantization taken as the identity (straight through):
+ *
+ *   g         a_flags TP_A_ROTATE: dy . blockdiag(Q) (dy is the gradient of
+ *             the rotated rows, as a rotated projection's backward gives it;
+ *             the rotation is its own inverse); TP_A_PREROTATED: dy.
+ *   rr        1 / sqrt(mean_j(t[r, j]^2) + eps)
+ *   dx[r, j]  rr gamma[j] g[r, j] - t[r, j] rr^3 mean_j(gamma g t) + dsum[r, j]
+ *             (the gradient of x and of the residual alike)
+ *   dgamma[j] sum_r g[r, j] t[r, j] rr
+ *
+ *   dy        [m, k], dy_dtype, row pitch lddy.
+ *   t         [m, k], t_dtype, row pitch ldt: the forward's sum_out (or x).
+ *   gamma     as in the forward; NULL: all ones.
+ *   dsum      NULL, or [m, k], dx_dtype, row pitch ldds: the gradient that
+ *             reaches the residual stream from behind.
+ *   dx        [m, k], dx_dtype, row pitch lddx; may be dsum or dy itself (same
+ *             pointer, type and pitch); any other overlap is refused.
+ *   dgamma    fp32 [k], or NULL (not wanted). m == 0 gives zeros.
+ *   workspace tp_rmsnorm_backward_workspace_size(m, k) bytes, 16-byte aligned,
+ *             where dgamma is wanted; not used otherwise.
+ *   fp32 arithmetic and sums; dx rounded once. k at most 16384.
+ */
+size_t tp_rmsnorm_backward_workspace_size(int64_t m, int64_t k);
+tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t lddy, int a_flags, const void* t,
+                                     tp_dtype t_dtype, int64_t ldt, const void* gamma, tp_dtype g_dtype,
+                                     double eps, const void* dsum, int64_t ldds, int64_t m, int64_t k, void* dx,
+                                     tp_dtype dx_dtype, int64_t lddx, float* dgamma, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char* tp_status_string(tp_status status);

@@ -14,12 +14,19 @@ of the computation runs in the library's HIP kernels; there is no CPU path.
     tp_qgemm_w8a8(a, q, s, rotate, out_dtype, want_codes, want_acc)
                                                -> C (and qa, sa, acc on request)
     tp_qgemm_w8a8_prequantized(qa, sa, q, s)   -> C (codes from tp_quantize_rows_int8)
+
+The operators around the projections of a block (block_ops.py):
+
+    tp_rmsnorm_rotate(x, gamma, residual)      -> qa, sa (or rows), and the new stream
+    tp_rmsnorm_rotate_backward(dy, t, gamma)   -> dx, dgamma
 """
 
 import torch
 
 from . import _lib
 from ._lib import TPError, TP_A_PREROTATED, TP_A_ROTATE, TP_FFN_OUT_BF16, TP_FFN_OUT_I8  # noqa: F401
+from .block_ops import (  # noqa: F401
+    tp_rmsnorm_backward_workspace_size, tp_rmsnorm_rotate, tp_rmsnorm_rotate_backward)
 
 _DTYPE = {torch.float32: _lib.TP_F32, torch.bfloat16: _lib.TP_BF16}
 

@@ -25,17 +25,20 @@ STATUS_NAMES = {
     10: "TP_ERR_BAD_ALIASING",
     11: "TP_ERR_BAD_FLAGS",
     12: "TP_ERR_HIP",
+    13: "TP_ERR_BAD_VALUE",
 }
 TP_F32, TP_BF16 = 0, 1
 TP_A_PREROTATED, TP_A_ROTATE = 0, 1
 TP_OP_QGEMM_W8, TP_OP_QGEMM_W4, TP_OP_QGEMM_W8A8, TP_OP_QGEMM_W8A8_PREQUANTIZED = 1, 2, 3, 4
 TP_OP_QGEMM_W4A8, TP_OP_QGEMM_W4A8_PREQUANTIZED = 5, 6
 TP_FFN_OUT_I8, TP_FFN_OUT_BF16 = 0, 1
+TP_NORM_OUT_I8, TP_NORM_OUT_BF16 = 0, 1
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+_dbl = ctypes.c_double
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -64,6 +67,11 @@ SIGNATURES = {
                              _sz, _p]),
     "tp_qgemm_w4a8_prequantized": (_int, [_p, _i64, _p, _p, _i64, _p, _i64, _i64, _i64, _p, _int, _i64, _p, _sz,
                                           _p]),
+    "tp_rmsnorm_rotate": (_int, [_p, _int, _i64, _p, _i64, _p, _i64, _int, _p, _int, _dbl, _int, _i64, _i64, _int, _p,
+                                 _i64, _p, _p]),
+    "tp_rmsnorm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "tp_rmsnorm_rotate_backward": (_int, [_p, _int, _i64, _int, _p, _int, _i64, _p, _int, _dbl, _p, _i64, _i64, _i64,
+                                          _p, _int, _i64, _p, _p, _sz, _p]),
     "tp_status_string": (ctypes.c_char_p, [_int]),
     "tp_last_error_message": (ctypes.c_char_p, []),
     "tp_abi_version": (_int, []),

@@ -1,0 +1,180 @@
+"""Binding of the operators around the projections of a transformer block.
+
+    tp_rmsnorm_rotate(x, gamma, residual)         -> codes, scales (or rows), and the new stream
+    tp_rmsnorm_rotate_backward(dy, t, gamma)      -> dx, dgamma
+
+Like the rest of the package, each function has the name of the C entry point
+it calls, allocates what it is not given, and runs on the current stream of its
+tensors' device (or on `stream`, whose allocations it then uses). All tensors
+of a call sit on one device.
+"""
+
+import torch
+
+from . import _lib
+from ._lib import TP_A_PREROTATED, TP_A_ROTATE, TP_NORM_OUT_BF16, TP_NORM_OUT_I8
+
+_DTYPE = {torch.float32: _lib.TP_F32, torch.bfloat16: _lib.TP_BF16}
+_KIND = {"i8": (TP_NORM_OUT_I8, torch.int8), "bf16": (TP_NORM_OUT_BF16, torch.bfloat16)}
+
+
+def _dt(t, name):
+    try:
+        return _DTYPE[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)") from None
+
+
+def _device(first, **others):
+    """The one CUDA (HIP) device of a call's tensors (None: not given)."""
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("the operands must be CUDA (HIP) tensors")
+    for name, t in others.items():
+        if t is not None and (not isinstance(t, torch.Tensor) or t.device != first.device):
+            raise ValueError(f"{name} must be a tensor on {first.device}")
+    return first.device
+
+
+def _elsewhere(device, stream):
+    """The context a call has to move into: that of an explicit stream, or of
+    a device other than the current one; None where the call already is."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
+
+
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _mat(t, name, shape=None, dtype=None):
+    """Checks a 2-D row-major matrix; returns its row pitch in elements."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be {'2-D' if shape is None else shape}, got shape {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vec(t, name, count, dtype=None):
+    """Checks a contiguous vector."""
+    if t.dim() != 1 or t.shape[0] != count or (count > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {count} elements, got shape {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def _weight(t, name, count):
+    """Pointer and dtype code of an optional weight vector."""
+    if t is None:
+        return None, _lib.TP_F32
+    return _vec(t, name, count).data_ptr(), _dt(t, name)
+
+
+def _scratch(workspace, need, device):
+    """Pointer and size of the caller's scratch tensor, or of a new one (kept
+    alive by the third value until the launch)."""
+    if workspace is None:
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def tp_rmsnorm_rotate(x, gamma=None, eps=1e-6, residual=None, rotate=True, out_kind="i8", out=None, scales=None,
+                      sum_out=None, stream=None):
+    """t = x + residual (fp32, rounded to the residual's dtype) or x; the RMS
+    norm of t's rows times gamma, rotated per 256-group (unless rotate=False),
+    as int8 codes with one fp32 scale per row (out_kind "i8") or as bf16 rows
+    ("bf16"). Returns (codes, scales) or rows; with a residual also t, the new
+    stream: (codes, scales, t) or (rows, t). sum_out may be residual (or x)
+    itself."""
+    dev = _device(x, gamma=gamma, residual=residual, out=out, scales=scales, sum_out=sum_out)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return tp_rmsnorm_rotate(x, gamma, eps, residual, rotate, out_kind, out, scales, sum_out)
+    if out_kind not in _KIND:
+        raise ValueError("out_kind must be 'i8' or 'bf16'")
+    kind, y_dtype = _KIND[out_kind]
+    ldx = _mat(x, "x")
+    m, k = x.shape
+    g_ptr, g_dt = _weight(gamma, "gamma", k)
+    r_ptr = s_ptr = None
+    ldr = lds = s_dt = 0
+    if residual is not None:
+        ldr = _mat(residual, "residual", (m, k))
+        s_dt = _dt(residual, "residual")
+        if sum_out is None:
+            sum_out = torch.empty((m, k), dtype=residual.dtype, device=dev)
+        lds = _mat(sum_out, "sum_out", (m, k), residual.dtype)
+        r_ptr, s_ptr = residual.data_ptr(), sum_out.data_ptr()
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if out is None:
+        out = torch.empty((m, k), dtype=y_dtype, device=dev)
+    ldy = _mat(out, "out", (m, k), y_dtype)
+    sc_ptr = None
+    if kind == TP_NORM_OUT_I8:
+        if scales is None:
+            scales = torch.empty((m,), dtype=torch.float32, device=dev)
+        sc_ptr = _vec(scales, "scales", m, torch.float32).data_ptr()
+    elif scales is not None:
+        raise ValueError("scales belong to out_kind 'i8'")
+    _lib.check(_lib.load().tp_rmsnorm_rotate(
+        x.data_ptr(), _dt(x, "x"), ldx, r_ptr, ldr, s_ptr, lds, s_dt, g_ptr, g_dt, eps,
+        TP_A_ROTATE if rotate else TP_A_PREROTATED, m, k, kind, out.data_ptr(), ldy, sc_ptr, _raw_stream(dev)))
+    got = (out, scales) if kind == TP_NORM_OUT_I8 else (out,)
+    if residual is not None:
+        got += (sum_out,)
+    return got if len(got) > 1 else out
+
+
+def tp_rmsnorm_backward_workspace_size(m, k):
+    """Bytes of workspace tp_rmsnorm_rotate_backward needs for dgamma."""
+    return int(_lib.load().tp_rmsnorm_backward_workspace_size(m, k))
+
+
+def tp_rmsnorm_rotate_backward(dy, t, gamma=None, eps=1e-6, dsum=None, rotate=True, dx_dtype=None, want_dgamma=True,
+                               dx=None, dgamma=None, workspace=None, stream=None):
+    """Gradients of tp_rmsnorm_rotate (quantization straight through): dy is
+    the gradient of its rows (rotated ones unless rotate=False), t its sum (or
+    x), dsum the gradient that reaches the stream from behind. Returns
+    (dx, dgamma); dgamma is None where it is not wanted. dx (default dtype:
+    dsum's, else t's) may be dsum or dy itself."""
+    dev = _device(dy, t=t, gamma=gamma, dsum=dsum, dx=dx, dgamma=dgamma, workspace=workspace)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return tp_rmsnorm_rotate_backward(dy, t, gamma, eps, dsum, rotate, dx_dtype, want_dgamma, dx, dgamma,
+                                              workspace)
+    lddy = _mat(dy, "dy")
+    m, k = dy.shape
+    ldt = _mat(t, "t", (m, k))
+    g_ptr, g_dt = _weight(gamma, "gamma", k)
+    if dx is None:
+        dx = torch.empty((m, k), dtype=dx_dtype or (t if dsum is None else dsum).dtype, device=dev)
+    elif dx_dtype is not None and dx.dtype != dx_dtype:
+        raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
+    lddx = _mat(dx, "dx", (m, k))
+    ldds = 0 if dsum is None else _mat(dsum, "dsum", (m, k), dx.dtype)
+    want = want_dgamma or dgamma is not None
+    dg_ptr = ws_ptr = ws = None
+    ws_bytes = 0
+    if want:
+        if dgamma is None:
+            dgamma = torch.empty((k,), dtype=torch.float32, device=dev)
+        dg_ptr = _vec(dgamma, "dgamma", k, torch.float32).data_ptr()
+        ws_ptr, ws_bytes, ws = _scratch(workspace, tp_rmsnorm_backward_workspace_size(m, k), dev)
+    _lib.check(_lib.load().tp_rmsnorm_rotate_backward(
+        dy.data_ptr(), _dt(dy, "dy"), lddy, TP_A_ROTATE if rotate else TP_A_PREROTATED, t.data_ptr(), _dt(t, "t"),
+        ldt, g_ptr, g_dt, eps, None if dsum is None else dsum.data_ptr(), ldds, m, k, dx.data_ptr(), _dt(dx, "dx"),
+        lddx, dg_ptr, ws_ptr, ws_bytes, _raw_stream(dev)))
+    return dx, dgamma

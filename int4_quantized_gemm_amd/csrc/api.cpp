@@ -12,6 +12,7 @@
 #include <string.h>
 
 #include "../../include/tp.h"
+#include "block_ops.hpp"
 #include "kernels.hpp"
 
 namespace {
@@ -198,6 +199,7 @@ const char* tp_status_string(tp_status s) {
     case TP_ERR_BAD_ALIASING: return "TP_ERR_BAD_ALIASING";
     case TP_ERR_BAD_FLAGS: return "TP_ERR_BAD_FLAGS";
     case TP_ERR_HIP: return "TP_ERR_HIP";
+    case TP_ERR_BAD_VALUE: return "TP_ERR_BAD_VALUE";
   }
   return "TP_ERR_UNKNOWN";
 }
@@ -664,6 +666,166 @@ tp_status tp_qgemm_w4a8_prequantized(const int8_t* qa, int64_t ldqa, const float
                                      size_t workspace_bytes, hipStream_t stream) {
   return prequantized_product(tp::GEMM_W4A8, qa, ldqa, sa, q4, ldq_bytes, w_scales, m, n, k, c, c_dtype, ldc,
                               nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------ norm around the projections
+
+namespace {
+
+tp_status check_eps(double eps) {
+  if (!(eps > 0.0) || !(eps < 1e300)) return fail(TP_ERR_BAD_VALUE, "eps=%g is not positive and finite", eps);
+  return TP_OK;
+}
+
+// A weight vector: optional, contiguous, 16-byte aligned.
+tp_status check_weight(const char* name, const void* p, tp_dtype dtype, int64_t count, Extent* ext) {
+  *ext = Extent{};
+  if (!p) return TP_OK;
+  if (!dtype_ok(dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d is not TP_F32 or TP_BF16", name, (int)dtype);
+  return check_matrix(name, p, 1, count * dtype_size(dtype), count, dtype_size(dtype), ext);
+}
+
+tp_status check_norm_k(int64_t k) {
+  if (k / 256 > tp::NORM_MAX_GROUPS)
+    return fail(TP_ERR_BAD_SHAPE, "k=%lld: rows of at most %d columns", (long long)k, tp::NORM_MAX_GROUPS * 256);
+  return TP_OK;
+}
+
+// Whether out may be the very buffer of in.
+bool same_buffer(const void* out, tp_dtype od, int64_t ldo, const void* in, tp_dtype id, int64_t ldi) {
+  return out == in && od == id && ldo == ldi;
+}
+
+// The caller's scratch memory, where `need` bytes of it are used.
+tp_status check_scratch(const char* query, const void* ws, size_t ws_bytes, int64_t need, Extent* ew) {
+  *ew = Extent{};
+  if (need == 0) return TP_OK;
+  if (!ws || (uint64_t)ws_bytes < (uint64_t)need)
+    return fail(TP_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %lld needed (%s)", ws_bytes, (long long)need, query);
+  if (((uintptr_t)ws & 15u) != 0) return fail(TP_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+  ew->lo = (uintptr_t)ws;
+  ew->hi = ew->lo + (uintptr_t)need;
+  return TP_OK;
+}
+
+}  // namespace
+
+tp_status tp_rmsnorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, const void* residual, int64_t ldr,
+                            void* sum_out, int64_t ldsum, tp_dtype s_dtype, const void* gamma, tp_dtype g_dtype,
+                            double eps, int a_flags, int64_t m, int64_t k, int out_kind, void* y, int64_t ldy,
+                            float* scales, hipStream_t stream) {
+  if (!dtype_ok(x_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "x_dtype %d is not TP_F32 or TP_BF16", (int)x_dtype);
+  if (out_kind != TP_NORM_OUT_I8 && out_kind != TP_NORM_OUT_BF16) return fail(TP_ERR_BAD_FLAGS, "out_kind=%d", out_kind);
+  if (a_flags != TP_A_ROTATE && a_flags != TP_A_PREROTATED) return fail(TP_ERR_BAD_FLAGS, "a_flags=%d", a_flags);
+  TP_TRY(check_sizes(m, 0, k));
+  TP_TRY(check_norm_k(k));
+  TP_TRY(check_eps(eps));
+  const bool i8 = out_kind == TP_NORM_OUT_I8;
+  const int64_t xs = dtype_size(x_dtype);
+  Extent ex, er{}, esum{}, eg, ey, esc{};
+  TP_TRY(check_matrix("x", x, m, k * xs, ldx, xs, &ex));
+  if (residual || sum_out) {
+    if (!dtype_ok(s_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "s_dtype %d is not TP_F32 or TP_BF16", (int)s_dtype);
+    const int64_t ss = dtype_size(s_dtype);
+    if (!residual || !sum_out)
+      return fail(TP_ERR_NULL_POINTER, "residual and sum_out are given together or not at all");
+    TP_TRY(check_matrix("residual", residual, m, k * ss, ldr, ss, &er));
+    TP_TRY(check_matrix("sum_out", sum_out, m, k * ss, ldsum, ss, &esum));
+  }
+  TP_TRY(check_weight("gamma", gamma, g_dtype, k, &eg));
+  TP_TRY(check_matrix("y", y, m, k * (i8 ? 1 : 2), ldy, i8 ? 1 : 2, &ey));
+  if (i8) TP_TRY(check_vector("scales", scales, m, &esc));
+  const Extent* outs[] = {&ey, &esc};
+  for (const Extent* o : outs)
+    if (overlaps(*o, ex) || overlaps(*o, er) || overlaps(*o, esum) || overlaps(*o, eg))
+      return fail(TP_ERR_BAD_ALIASING, "y and scales must not overlap x, residual, sum_out or gamma");
+  if (overlaps(ey, esc)) return fail(TP_ERR_BAD_ALIASING, "y and scales overlap");
+  if (overlaps(esum, eg)) return fail(TP_ERR_BAD_ALIASING, "sum_out overlaps gamma");
+  if (overlaps(esum, er) && !same_buffer(sum_out, s_dtype, ldsum, residual, s_dtype, ldr))
+    return fail(TP_ERR_BAD_ALIASING, "sum_out overlaps residual without being the same buffer");
+  if (overlaps(esum, ex) && !same_buffer(sum_out, s_dtype, ldsum, x, x_dtype, ldx))
+    return fail(TP_ERR_BAD_ALIASING, "sum_out overlaps x without being the same buffer");
+  if (m == 0) return ok();
+  tp::NormArgs a{};
+  a.x = x;
+  a.x_bf16 = x_dtype == TP_BF16;
+  a.ldx = ldx;
+  a.res = residual;
+  a.ldr = ldr;
+  a.sum = sum_out;
+  a.ldsum = ldsum;
+  a.s_bf16 = residual && s_dtype == TP_BF16;
+  a.gamma = {gamma, gamma && g_dtype == TP_BF16};
+  a.eps = eps;
+  a.rotate = a_flags == TP_A_ROTATE;
+  a.m = m;
+  a.groups = (int)(k / 256);
+  a.out_i8 = i8;
+  a.y = y;
+  a.ldy = ldy;
+  a.scales = i8 ? scales : nullptr;
+  return hip_status(tp::launch_norm_rotate(a, stream), "norm launch");
+}
+
+size_t tp_rmsnorm_backward_workspace_size(int64_t m, int64_t k) {
+  if (m <= 0 || k <= 0 || k % 256 != 0 || m > INT_MAX || k / 256 > tp::NORM_MAX_GROUPS) return 0;
+  return (size_t)(tp::norm_bwd_partial_rows(m, (int)(k / 256)) * k * 4);
+}
+
+tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t lddy, int a_flags, const void* t,
+                                     tp_dtype t_dtype, int64_t ldt, const void* gamma, tp_dtype g_dtype, double eps,
+                                     const void* dsum, int64_t ldds, int64_t m, int64_t k, void* dx,
+                                     tp_dtype dx_dtype, int64_t lddx, float* dgamma, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream) {
+  if (!dtype_ok(dy_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "dy_dtype %d is not TP_F32 or TP_BF16", (int)dy_dtype);
+  if (!dtype_ok(t_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "t_dtype %d is not TP_F32 or TP_BF16", (int)t_dtype);
+  if (!dtype_ok(dx_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "dx_dtype %d is not TP_F32 or TP_BF16", (int)dx_dtype);
+  if (a_flags != TP_A_ROTATE && a_flags != TP_A_PREROTATED) return fail(TP_ERR_BAD_FLAGS, "a_flags=%d", a_flags);
+  TP_TRY(check_sizes(m, 0, k));
+  TP_TRY(check_norm_k(k));
+  TP_TRY(check_eps(eps));
+  const int64_t gs = dtype_size(dy_dtype), ts = dtype_size(t_dtype), xs = dtype_size(dx_dtype);
+  Extent edy, et, eg, eds{}, edx, edg{}, ew;
+  TP_TRY(check_matrix("dy", dy, m, k * gs, lddy, gs, &edy));
+  TP_TRY(check_matrix("t", t, m, k * ts, ldt, ts, &et));
+  TP_TRY(check_weight("gamma", gamma, g_dtype, k, &eg));
+  if (dsum) TP_TRY(check_matrix("dsum", dsum, m, k * xs, ldds, xs, &eds));
+  TP_TRY(check_matrix("dx", dx, m, k * xs, lddx, xs, &edx));
+  if (dgamma) TP_TRY(check_vector("dgamma", dgamma, k, &edg));
+  TP_TRY(check_scratch("tp_rmsnorm_backward_workspace_size", workspace, workspace_bytes,
+                       dgamma ? (int64_t)tp_rmsnorm_backward_workspace_size(m, k) : 0, &ew));
+  const Extent* ins[] = {&edy, &et, &eg, &eds};
+  for (const Extent* i : ins)
+    if (overlaps(edg, *i) || overlaps(ew, *i))
+      return fail(TP_ERR_BAD_ALIASING, "dgamma or the workspace overlaps an input");
+  if (overlaps(edx, edg) || overlaps(edx, ew) || overlaps(edg, ew))
+    return fail(TP_ERR_BAD_ALIASING, "dx, dgamma and the workspace must not overlap");
+  if (overlaps(edx, et) || overlaps(edx, eg)) return fail(TP_ERR_BAD_ALIASING, "dx overlaps t or gamma");
+  if (overlaps(edx, eds) && !same_buffer(dx, dx_dtype, lddx, dsum, dx_dtype, ldds))
+    return fail(TP_ERR_BAD_ALIASING, "dx overlaps dsum without being the same buffer");
+  if (overlaps(edx, edy) && !same_buffer(dx, dx_dtype, lddx, dy, dy_dtype, lddy))
+    return fail(TP_ERR_BAD_ALIASING, "dx overlaps dy without being the same buffer");
+  if (m == 0 && !dgamma) return ok();
+  tp::NormBwdArgs a{};
+  a.dy = dy;
+  a.dy_bf16 = dy_dtype == TP_BF16;
+  a.lddy = lddy;
+  a.rotate = a_flags == TP_A_ROTATE;
+  a.t = t;
+  a.t_bf16 = t_dtype == TP_BF16;
+  a.ldt = ldt;
+  a.gamma = {gamma, gamma && g_dtype == TP_BF16};
+  a.eps = eps;
+  a.dsum = dsum;
+  a.ldds = ldds;
+  a.m = m;
+  a.groups = (int)(k / 256);
+  a.dx = dx;
+  a.dx_bf16 = dx_dtype == TP_BF16;
+  a.lddx = lddx;
+  a.dgamma = dgamma;
+  a.part = (float*)workspace;
+  return hip_status(tp::launch_norm_bwd(a, stream), "norm backward launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,69 @@
+// Internal launchers of the operators around the projections of a transformer
+// block: norm.hip (RMS norm in front of them), side.hip (the adapter's side
+// path on 8-bit activations, and its gradients) and rope.hip (per-head norm and
+// rotary positions behind the qkv projection). Callers (api.cpp) validate every
+// argument first; the launchers return the launch's hipError_t.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace tp {
+
+// A vector of weights: fp32 or bf16, or none (p == nullptr).
+struct VecArg {
+  const void* p;
+  int bf16;
+};
+
+// ------------------------------------------------------------------ norm.hip
+constexpr int NORM_MAX_GROUPS = 64;  // one 16-lane set per 256-group, 1024 threads a row at most
+
+struct NormArgs {
+  const void* x;
+  int x_bf16;
+  int64_t ldx;
+  const void* res;  // nullptr: no residual (and no sum)
+  int64_t ldr;
+  void* sum;
+  int64_t ldsum;
+  int s_bf16;
+  VecArg gamma;
+  double eps;
+  int rotate;
+  int64_t m;
+  int groups;
+  int out_i8;
+  void* y;
+  int64_t ldy;
+  float* scales;
+};
+hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream);
+
+struct NormBwdArgs {
+  const void* dy;
+  int dy_bf16;
+  int64_t lddy;
+  int rotate;
+  const void* t;
+  int t_bf16;
+  int64_t ldt;
+  VecArg gamma;
+  double eps;
+  const void* dsum;  // nullptr: none
+  int64_t ldds;
+  int64_t m;
+  int groups;
+  void* dx;
+  int dx_bf16;
+  int64_t lddx;
+  float* dgamma;  // nullptr: not wanted
+  float* part;    // norm_bwd_partial_rows(m, groups) rows of groups * 256 floats
+};
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
+int64_t norm_bwd_partial_rows(int64_t m, int groups);
+
+// out[c] = sum over the rows p of part[p][c], added in a fixed order.
+hipError_t launch_colsum(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t stream);
+
+}  // namespace tp

@@ -78,6 +78,7 @@ from .products import qgemm_w8, qgemm_w4, qgemm_w8a8, qgemm_w4a8, int_accumulate
 from .ffn import silu_mul, swiglu_bf16, ffn_middle_int8, ffn_middle_rotated
 from .loader import dequantize, dequantize_unrotate, requantize
 from .lora import lora_delta, lora_add
+from .norm import stream_sum, rmsnorm, rmsnorm_backward
 
 __all__ = [
     "GROUP",
@@ -91,6 +92,9 @@ __all__ = [
     "unpack_int4",
     "dequantize_int8",
     "dequantize_int4",
+    "stream_sum",
+    "rmsnorm",
+    "rmsnorm_backward",
     "lora_delta",
     "lora_add",
     "dequantize",

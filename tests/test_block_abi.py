@@ -1,0 +1,96 @@
+"""Refusals of the operators around the projections, without a GPU: every
+invalid call is named before any HIP call (made-up device addresses; nothing is
+dereferenced or launched), and the binding refuses what the C boundary cannot
+see."""
+
+import os
+
+import pytest
+import torch
+
+import int4_quantized_gemm_amd as tp
+from int4_quantized_gemm_amd import _lib
+
+A, B, C, D, E, F, G = (0x10000000 * i for i in range(1, 8))  # disjoint fake addresses
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        import __graft_entry__
+        __graft_entry__.build()
+    return _lib.load()
+
+
+def _err(lib):
+    return lib.tp_last_error_message().decode()
+
+
+# ----------------------------------------------------------------- RMS norm
+def nr(lib, x=A, xdt=0, ldx=512, res=B, ldr=512, sm=C, lds=512, sdt=0, g=D, gdt=0, eps=1e-6, fl=1, m=64, k=512,
+       kind=0, y=E, ldy=512, sc=F):
+    return lib.tp_rmsnorm_rotate(x, xdt, ldx, res, ldr, sm, lds, sdt, g, gdt, eps, fl, m, k, kind, y, ldy, sc, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=300), 3), (dict(k=0), 2), (dict(m=-1), 2), (dict(m=2 ** 31), 2),
+    (dict(k=16640, ldx=16640, ldr=16640, lds=16640, ldy=16640), 2),
+    (dict(x=0), 1), (dict(y=0), 1), (dict(sc=0), 1), (dict(res=0), 1), (dict(sm=0), 1),
+    (dict(ldx=500), 4), (dict(ldr=511), 4), (dict(lds=0), 4), (dict(ldy=511), 4), (dict(kind=1, ldy=500), 4),
+    (dict(x=A + 8), 5), (dict(res=B + 4), 5), (dict(sm=C + 8), 5), (dict(g=D + 8), 5), (dict(y=E + 1), 5),
+    (dict(sc=F + 2), 5), (dict(ldx=513), 5),
+    (dict(xdt=2), 6), (dict(sdt=5), 6), (dict(gdt=-1), 6),
+    (dict(kind=2), 11), (dict(fl=2), 11),
+    (dict(eps=0.0), 13), (dict(eps=-1e-6), 13), (dict(eps=float("nan")), 13), (dict(eps=float("inf")), 13),
+    (dict(ldx=2 ** 62), 8),
+    (dict(y=A + 4096), 10), (dict(y=B), 10), (dict(y=C), 10), (dict(y=D), 10), (dict(sc=E + 64), 10),
+    (dict(sc=A), 10), (dict(sm=D), 10), (dict(sm=B + 16), 10), (dict(sm=B, lds=516), 10), (dict(sm=A, sdt=1), 10),
+    (dict(sm=A + 2048), 10),
+])
+def test_norm_refusals(lib, kw, status):
+    assert nr(lib, **kw) == status, _err(lib)
+    assert _err(lib)
+
+
+def test_norm_empty_and_optional(lib):
+    assert nr(lib, m=0) == 0
+    assert nr(lib, m=0, x=0, y=0, sc=0) == 0
+    assert nr(lib, m=0, res=0, sm=0, g=0, sdt=9) == 0       # no residual, no weight
+    assert nr(lib, m=0, kind=1, sc=0) == 0
+
+
+def nb(lib, dy=A, ydt=0, lddy=512, fl=1, t=B, tdt=0, ldt=512, g=C, gdt=0, eps=1e-6, ds=D, ldds=512, m=64, k=512,
+       dx=E, xdt=0, lddx=512, dg=F, ws=G, wsb=1 << 24):
+    return lib.tp_rmsnorm_rotate_backward(dy, ydt, lddy, fl, t, tdt, ldt, g, gdt, eps, ds, ldds, m, k, dx, xdt, lddx,
+                                          dg, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=300), 3), (dict(k=-256), 2), (dict(m=-1), 2), (dict(k=16640), 2),
+    (dict(dy=0), 1), (dict(t=0), 1), (dict(dx=0), 1),
+    (dict(lddy=500), 4), (dict(ldt=500), 4), (dict(ldds=500), 4), (dict(lddx=500), 4),
+    (dict(dy=A + 8), 5), (dict(t=B + 2), 5), (dict(g=C + 4), 5), (dict(ds=D + 8), 5), (dict(dx=E + 8), 5),
+    (dict(dg=F + 1), 5), (dict(ws=G + 8), 5),
+    (dict(ydt=2), 6), (dict(tdt=2), 6), (dict(xdt=2), 6), (dict(gdt=2), 6),
+    (dict(fl=3), 11), (dict(eps=0.0), 13), (dict(ldt=2 ** 62), 8),
+    (dict(ws=0), 9), (dict(wsb=100), 9),
+    (dict(dx=B), 10), (dict(dx=C), 10), (dict(dx=A, ydt=1), 10), (dict(dx=A + 16), 10), (dict(dx=D, lddx=516), 10),
+    (dict(dg=E), 10), (dict(dg=A), 10), (dict(ws=A), 10), (dict(ws=E), 10), (dict(ws=F), 10),
+])
+def test_norm_backward_refusals(lib, kw, status):
+    assert nb(lib, **kw) == status, _err(lib)
+    assert _err(lib)
+
+
+def test_norm_backward_empty_and_workspace(lib):
+    assert nb(lib, m=0, dg=0, ws=0) == 0
+    assert lib.tp_rmsnorm_backward_workspace_size(64, 512) > 0
+    for m, k in ((0, 512), (-1, 512), (4, 300), (4, 0), (4, 16640), (2 ** 31, 256)):
+        assert lib.tp_rmsnorm_backward_workspace_size(m, k) == 0
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.zeros((4, 256))
+    for call in (lambda: tp.tp_rmsnorm_rotate(x), lambda: tp.tp_rmsnorm_rotate_backward(x, x)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()

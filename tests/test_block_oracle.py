@@ -1,0 +1,59 @@
+"""Pins of the oracle's operators around the projections: closed forms, plain
+loops and gradients against central differences (fp64, CPU)."""
+
+import numpy as np
+import pytest
+
+import oracle
+
+
+def _differences(f, x, step=1e-6):
+    """d f / d x for a scalar f, by central differences."""
+    g = np.zeros_like(x)
+    it = np.nditer(x, flags=["multi_index"])
+    for _ in it:
+        i = it.multi_index
+        keep = x[i]
+        x[i] = keep + step
+        hi = f(x)
+        x[i] = keep - step
+        lo = f(x)
+        x[i] = keep
+        g[i] = (hi - lo) / (2 * step)
+    return g
+
+
+def test_norm_closed_forms():
+    t = np.full((1, 256), 3.0)
+    assert np.allclose(oracle.rmsnorm(t, None, 1e-300), 1.0, rtol=1e-15)
+    t = np.zeros((1, 256))
+    t[0, 5] = -2.0  # mean square 4 / 256: h = -16 at 5
+    assert np.allclose(oracle.rmsnorm(t, np.arange(256.0), 1e-300)[0, 5], -16.0 * 5.0, rtol=1e-15)
+    assert np.all(oracle.rmsnorm(np.zeros((2, 256)), None, 1e-6) == 0.0)
+    # eps = 3 mean(t^2) halves the result
+    t = np.array([[1.0, -1.0] * 128])
+    assert np.allclose(oracle.rmsnorm(t, None, 3.0), t / 2.0, rtol=1e-15)
+
+
+def test_stream_sum_rounds_to_its_type():
+    x = np.float32([1.0, 1.0, 2.0 ** 24])
+    res = np.float32([2.0 ** -8, 3 * 2.0 ** -8, 1.0])
+    # bf16 steps of 2^-7 above 1: the first is a tie to even (1.0), the second a tie to 1 + 2^-6
+    assert oracle.stream_sum(x, res, True).tolist() == [1.0, 1.0 + 2.0 ** -6, 2.0 ** 24]
+    assert oracle.stream_sum(x, res, False).tolist() == [1.0 + 2.0 ** -8, 1.0 + 3 * 2.0 ** -8, 2.0 ** 24]
+
+
+@pytest.mark.parametrize("rotate", [False, True])
+def test_norm_gradient_against_differences(rotate):
+    rng = np.random.default_rng(3)
+    t = rng.standard_normal((2, 256)) * 2.0
+    gamma = 1.0 + 0.2 * rng.standard_normal(256)
+    dy, ds = rng.standard_normal((2, 256)), rng.standard_normal((2, 256))
+
+    def loss(t, gamma):
+        h = oracle.rmsnorm(t, gamma, 1e-3)
+        return np.sum(dy * (oracle.rotate_groups(h) if rotate else h)) + np.sum(ds * t)
+
+    dx, dgamma = oracle.rmsnorm_backward(dy, t, gamma, 1e-3, dsum=ds, rotate=rotate)
+    assert np.allclose(dx, _differences(lambda v: loss(v, gamma), t.copy()), rtol=1e-6, atol=1e-6)
+    assert np.allclose(dgamma, _differences(lambda v: loss(t, v), gamma.copy()), rtol=1e-6, atol=1e-6)
