@@ -522,6 +522,60 @@ tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t 
                                      tp_dtype dx_dtype, int64_t lddx, float* dgamma, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * tp_lora_down_prequantized -- tp_lora_down on activations that are held as
+ * int8 codes and scales (tp_quantize_rows_int8, tp_rmsnorm_rotate or
+ * tp_swiglu_rotate), without a copy of the activations in a wider type:
+ *
+ *   T[i, t] = sa[i] * sum_q qa[i, q] * lora_a[t, q]   (fp32)
+ *
+ *   qa       int8 [m, k], row pitch ldqa bytes; sa fp32 [m].
+ *   lora_a   [r, k] (a_dtype) in the codes' domain (rotated by
+ *            tp_hadamard_rotate_rows where they are), row pitch lda; 16-byte
+ *            aligned rows; 1 <= r <= 64; k a multiple of 256.
+ *   t        as in tp_lora_down.
+ *   Products are exact, summed in fp32 in a fixed order, then scaled.
+ */
+tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float* sa, const void* lora_a,
+                                    tp_dtype a_dtype, int64_t lda, int64_t m, int64_t k, int64_t r, float* t,
+                                    size_t t_bytes, hipStream_t stream);
+
+/*
+ * tp_lora_grad_prequantized -- the gradients of a LoRA side path
+ * Y += alpha * T . lora_b^T, T = x . lora_a^T, from the activations' int8 codes
+ * x = sa qa: the checkpoint of the forward pass is what the quantized product
+ * read, one byte an element (kvad-gpu internals, section "Pictures, which are
+ * not tokens": the loaded, quantized weights stay as they are; only the side
+ * path changes).
+ *
+ *   dt[i, j] = alpha * sum_c dy[i, c] lora_b[c, j]
+ *   db[c, j] = alpha * sum_i dy[i, c] t[i, j]
+ *   da[j, q] = sum_i dt[i, j] sa[i] qa[i, q]     a_flags TP_A_PREROTATED: as
+ *              it is (lora_a is trained in the codes' domain); TP_A_ROTATE:
+ *              da . blockdiag(Q), the gradient of the un-rotated lora_a.
+ *
+ *   dy       [m, n] (dy_dtype), row pitch lddy, 16-byte aligned rows.
+ *   qa, sa   as in tp_lora_down_prequantized; t: its (or tp_lora_down's)
+ *            result, fp32 rows of 64.
+ *   lora_b   [n, r] (b_dtype), row pitch ldb; 16-byte aligned rows.
+ *   dt       fp32 [m, 64], rows of 64 (zeros past r), 16-byte aligned: dx's part
+ *            of the side path is dt . lora_a.
+ *   da       fp32 [r, k], row pitch ldda, 16-byte aligned rows.
+ *   db       fp32 [n, r], row pitch lddb, aligned to the element.
+ *   workspace  tp_lora_grad_workspace_size(m, n, k, r) bytes, 16-byte aligned
+ *            (partial sums; nothing is kept between calls).
+ *   dt, da, db and the workspace must not overlap any other operand. m == 0 or
+ *   n == 0 gives zeros for the sums over nothing. m and n below 2^28.
+ *   fp32 accuracy: operands that are not bf16 are split exactly into three bf16
+ *   parts, the products are summed in fp32 in a fixed order.
+ */
+size_t tp_lora_grad_workspace_size(int64_t m, int64_t n, int64_t k, int64_t r);
+tp_status tp_lora_grad_prequantized(const void* dy, tp_dtype dy_dtype, int64_t lddy, const int8_t* qa, int64_t ldqa,
+                                    const float* sa, const float* t, const void* lora_b, tp_dtype b_dtype,
+                                    int64_t ldb, float alpha, int a_flags, int64_t m, int64_t n, int64_t k,
+                                    int64_t r, float* dt, float* da, int64_t ldda, float* db, int64_t lddb,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* tp_status_string(tp_status status);
 

@@ -19,6 +19,9 @@ The operators around the projections of a block (block_ops.py):
 
     tp_rmsnorm_rotate(x, gamma, residual)      -> qa, sa (or rows), and the new stream
     tp_rmsnorm_rotate_backward(dy, t, gamma)   -> dx, dgamma
+    tp_lora_down_prequantized(qa, sa, lora_a)  -> T (the side path's first half on 8-bit activations)
+    tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha)
+                                               -> dA, dB, dT (from the 8-bit activations)
 """
 
 import torch
@@ -26,6 +29,7 @@ import torch
 from . import _lib
 from ._lib import TPError, TP_A_PREROTATED, TP_A_ROTATE, TP_FFN_OUT_BF16, TP_FFN_OUT_I8  # noqa: F401
 from .block_ops import (  # noqa: F401
+    tp_lora_down_prequantized, tp_lora_grad_prequantized, tp_lora_grad_workspace_size,
     tp_rmsnorm_backward_workspace_size, tp_rmsnorm_rotate, tp_rmsnorm_rotate_backward)
 
 _DTYPE = {torch.float32: _lib.TP_F32, torch.bfloat16: _lib.TP_BF16}

@@ -2,6 +2,9 @@
 
     tp_rmsnorm_rotate(x, gamma, residual)         -> codes, scales (or rows), and the new stream
     tp_rmsnorm_rotate_backward(dy, t, gamma)      -> dx, dgamma
+    tp_lora_down_prequantized(qa, sa, lora_a)     -> T
+    tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha)
+                                                  -> dA, dB, dT
 
 Like the rest of the package, each function has the name of the C entry point
 it calls, allocates what it is not given, and runs on the current stream of its
@@ -52,14 +55,18 @@ def _raw_stream(device):
 
 
 def _mat(t, name, shape=None, dtype=None):
-    """Checks a 2-D row-major matrix; returns its row pitch in elements."""
+    """Checks a 2-D row-major matrix; returns its row pitch in elements (any
+    pitch describes a single row: the shortest that the C boundary takes)."""
     if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
         raise ValueError(f"{name} must be {'2-D' if shape is None else shape}, got shape {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.shape[0] > 1:
+        return t.stride(0)
+    per = 16 // t.element_size()
+    return -(-t.shape[1] // per) * per
 
 
 def _vec(t, name, count, dtype=None):
@@ -178,3 +185,84 @@ def tp_rmsnorm_rotate_backward(dy, t, gamma=None, eps=1e-6, dsum=None, rotate=Tr
         ldt, g_ptr, g_dt, eps, None if dsum is None else dsum.data_ptr(), ldds, m, k, dx.data_ptr(), _dt(dx, "dx"),
         lddx, dg_ptr, ws_ptr, ws_bytes, _raw_stream(dev)))
     return dx, dgamma
+
+
+_T = 64  # floats of a row of T and dT
+
+
+def tp_lora_down_prequantized(qa, sa, lora_a, t=None, stream=None):
+    """T = sa (qa . lora_a^T) in fp32 rows of 64 (zeros past r): the first half
+    of the side path on activations held as int8 codes and scales; lora_a
+    [r, k] in the codes' domain. Returns T [m, 64], as tp_lora_down does."""
+    dev = _device(qa, sa=sa, lora_a=lora_a, t=t)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return tp_lora_down_prequantized(qa, sa, lora_a, t)
+    ldqa = _mat(qa, "qa", dtype=torch.int8)
+    m, k = qa.shape
+    _vec(sa, "sa", m, torch.float32)
+    lda = _mat(lora_a, "lora_a")
+    r = lora_a.shape[0]
+    if lora_a.shape[1] != k:
+        raise ValueError(f"lora_a must be [r, {k}], got shape {tuple(lora_a.shape)}")
+    t = _t_rows(t, "t", m, dev)
+    _lib.check(_lib.load().tp_lora_down_prequantized(qa.data_ptr(), ldqa, sa.data_ptr(), lora_a.data_ptr(),
+                                                     _dt(lora_a, "lora_a"), lda, m, k, r, t.data_ptr(),
+                                                     m * _T * 4, _raw_stream(dev)))
+    return t
+
+
+def _t_rows(t, name, m, device):
+    """fp32 [m, 64] contiguous, allocated where it is not given."""
+    if t is None:
+        return torch.empty((m, _T), dtype=torch.float32, device=device)
+    if _mat(t, name, (m, _T), torch.float32) != _T:
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def tp_lora_grad_workspace_size(m, n, k, r):
+    """Bytes of workspace tp_lora_grad_prequantized needs."""
+    return int(_lib.load().tp_lora_grad_workspace_size(m, n, k, r))
+
+
+def tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha, rotate=False, da=None, db=None, dt=None, workspace=None,
+                              stream=None):
+    """Gradients of the side path alpha * T . lora_b^T, T = x . lora_a^T, with
+    the activations x = sa qa held in 8 bits: (dA, dB, dT) = (dT^T x, alpha
+    dy^T T, alpha dy . lora_b), fp32. dA is in the codes' domain, or with
+    rotate=True rotated back (the gradient of an un-rotated lora_a); dT [m, 64]
+    gives dx = dT . lora_a."""
+    dev = _device(dy, qa=qa, sa=sa, t=t, lora_b=lora_b, da=da, db=db, dt=dt, workspace=workspace)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha, rotate, da, db, dt, workspace)
+    lddy = _mat(dy, "dy")
+    m, n = dy.shape
+    ldqa = _mat(qa, "qa", dtype=torch.int8)
+    k = qa.shape[1]
+    if qa.shape[0] != m:
+        raise ValueError(f"qa must have {m} rows, got shape {tuple(qa.shape)}")
+    _vec(sa, "sa", m, torch.float32)
+    if t is None:
+        raise ValueError("t (the forward's T) is needed")
+    t = _t_rows(t, "t", m, dev)
+    ldb = _mat(lora_b, "lora_b")
+    r = lora_b.shape[1]
+    if lora_b.shape[0] != n:
+        raise ValueError(f"lora_b must be [{n}, r], got shape {tuple(lora_b.shape)}")
+    dt = _t_rows(dt, "dt", m, dev)
+    if da is None:
+        da = torch.empty((r, k), dtype=torch.float32, device=dev)
+    ldda = _mat(da, "da", (r, k), torch.float32)
+    if db is None:
+        db = torch.empty((n, r), dtype=torch.float32, device=dev)
+    lddb = _mat(db, "db", (n, r), torch.float32)
+    ws_ptr, ws_bytes, ws = _scratch(workspace, tp_lora_grad_workspace_size(m, n, k, r), dev)
+    _lib.check(_lib.load().tp_lora_grad_prequantized(
+        dy.data_ptr(), _dt(dy, "dy"), lddy, qa.data_ptr(), ldqa, sa.data_ptr(), t.data_ptr(), lora_b.data_ptr(),
+        _dt(lora_b, "lora_b"), ldb, float(alpha), TP_A_ROTATE if rotate else TP_A_PREROTATED, m, n, k, r,
+        dt.data_ptr(), da.data_ptr(), ldda, db.data_ptr(), lddb, ws_ptr, ws_bytes, _raw_stream(dev)))
+    return da, db, dt

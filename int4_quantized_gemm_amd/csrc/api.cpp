@@ -828,5 +828,103 @@ tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t 
   return hip_status(tp::launch_norm_bwd(a, stream), "norm backward launch");
 }
 
+// ------------------------------------------- side path on 8-bit activations
+
+namespace {
+
+constexpr int64_t SIDE_MAX = (int64_t)1 << 28;  // rows and columns: a launch counts its threads in 32 bits
+
+tp_status check_rank(int64_t r) {
+  if (r < 1 || r > 64) return fail(TP_ERR_BAD_SHAPE, "rank r=%lld outside [1, 64]", (long long)r);
+  return TP_OK;
+}
+
+}  // namespace
+
+tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float* sa, const void* lora_a,
+                                    tp_dtype a_dtype, int64_t lda, int64_t m, int64_t k, int64_t r, float* t,
+                                    size_t t_bytes, hipStream_t stream) {
+  if (!dtype_ok(a_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "a_dtype %d is not TP_F32 or TP_BF16", (int)a_dtype);
+  TP_TRY(check_sizes(m, 0, k));
+  TP_TRY(check_rank(r));
+  const int64_t as = dtype_size(a_dtype);
+  Extent eq, es, ea, et;
+  TP_TRY(check_matrix("qa", qa, m, k, ldqa, 1, &eq));
+  TP_TRY(check_vector("sa", sa, m, &es));
+  TP_TRY(check_matrix("lora_a", lora_a, r, k * as, lda, as, &ea));
+  if (m > 0 && (uint64_t)t_bytes < (uint64_t)(m * 64 * 4))
+    return fail(TP_ERR_WORKSPACE_TOO_SMALL, "t of %zu bytes, %lld needed (m rows of 64 floats)", t_bytes,
+                (long long)(m * 64 * 4));
+  TP_TRY(check_matrix("t", t, m, 64 * 4, 64, 4, &et));
+  if (overlaps(et, eq) || overlaps(et, es) || overlaps(et, ea)) return fail(TP_ERR_BAD_ALIASING, "t overlaps an input");
+  if (m == 0) return ok();
+  return hip_status(tp::launch_side_down(qa, ldqa, sa, lora_a, a_dtype == TP_BF16, lda, m, k, (int)r, t, stream),
+                    "side path launch");
+}
+
+size_t tp_lora_grad_workspace_size(int64_t m, int64_t n, int64_t k, int64_t r) {
+  if (m < 0 || n < 0 || m >= SIDE_MAX || n >= SIDE_MAX || k <= 0 || k % 256 != 0 || k > INT_MAX || r < 1 || r > 64)
+    return 0;
+  return (size_t)(tp::side_grad_workspace_floats(m, n, k, r) * 4);
+}
+
+tp_status tp_lora_grad_prequantized(const void* dy, tp_dtype dy_dtype, int64_t lddy, const int8_t* qa, int64_t ldqa,
+                                    const float* sa, const float* t, const void* lora_b, tp_dtype b_dtype,
+                                    int64_t ldb, float alpha, int a_flags, int64_t m, int64_t n, int64_t k, int64_t r,
+                                    float* dt, float* da, int64_t ldda, float* db, int64_t lddb, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream) {
+  if (!dtype_ok(dy_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "dy_dtype %d is not TP_F32 or TP_BF16", (int)dy_dtype);
+  if (!dtype_ok(b_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "b_dtype %d is not TP_F32 or TP_BF16", (int)b_dtype);
+  if (a_flags != TP_A_ROTATE && a_flags != TP_A_PREROTATED) return fail(TP_ERR_BAD_FLAGS, "a_flags=%d", a_flags);
+  TP_TRY(check_sizes(m, n, k));
+  TP_TRY(check_rank(r));
+  if (m >= SIDE_MAX || n >= SIDE_MAX)
+    return fail(TP_ERR_BAD_SHAPE, "m=%lld, n=%lld: below 2^28 each", (long long)m, (long long)n);
+  const int64_t ys = dtype_size(dy_dtype), bs = dtype_size(b_dtype);
+  Extent edy, eq, es, et, eb, edt, eda, edb, ew;
+  TP_TRY(check_matrix("dy", dy, m, n * ys, lddy, ys, &edy));
+  TP_TRY(check_matrix("qa", qa, m, k, ldqa, 1, &eq));
+  TP_TRY(check_vector("sa", sa, m, &es));
+  TP_TRY(check_matrix("t", t, m, 64 * 4, 64, 4, &et));
+  TP_TRY(check_matrix("lora_b", lora_b, n, r * bs, ldb, bs, &eb));
+  TP_TRY(check_matrix("dt", dt, m, 64 * 4, 64, 4, &edt));
+  TP_TRY(check_matrix("da", da, r, k * 4, ldda, 4, &eda));
+  TP_TRY(check_matrix("db", db, n, r * 4, lddb, 4, &edb, 4));
+  TP_TRY(check_scratch("tp_lora_grad_workspace_size", workspace, workspace_bytes,
+                       (int64_t)tp_lora_grad_workspace_size(m, n, k, r), &ew));
+  const Extent* ins[] = {&edy, &eq, &es, &et, &eb};
+  const Extent* outs[] = {&edt, &eda, &edb, &ew};
+  for (int o = 0; o < 4; ++o) {
+    for (const Extent* i : ins)
+      if (overlaps(*outs[o], *i)) return fail(TP_ERR_BAD_ALIASING, "an output or the workspace overlaps an input");
+    for (int p = 0; p < o; ++p)
+      if (overlaps(*outs[o], *outs[p])) return fail(TP_ERR_BAD_ALIASING, "dt, da, db and the workspace must not overlap");
+  }
+  tp::SideGradArgs a{};
+  a.dy = dy;
+  a.dy_bf16 = dy_dtype == TP_BF16;
+  a.lddy = lddy;
+  a.qa = qa;
+  a.ldqa = ldqa;
+  a.sa = sa;
+  a.t = t;
+  a.b = lora_b;
+  a.b_bf16 = b_dtype == TP_BF16;
+  a.ldb = ldb;
+  a.alpha = alpha;
+  a.rotate = a_flags == TP_A_ROTATE;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  a.r = (int)r;
+  a.dt = dt;
+  a.da = da;
+  a.ldda = ldda;
+  a.db = db;
+  a.lddb = lddb;
+  a.ws = (float*)workspace;
+  return hip_status(tp::launch_side_grad(a, stream), "side path gradient launch");
+}
+
 }  // extern "C"
 

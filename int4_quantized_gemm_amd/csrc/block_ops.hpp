@@ -66,4 +66,34 @@ int64_t norm_bwd_partial_rows(int64_t m, int groups);
 // out[c] = sum over the rows p of part[p][c], added in a fixed order.
 hipError_t launch_colsum(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t stream);
 
+// ------------------------------------------------------------------ side.hip
+// T = sa (qa . a^T), fp32 [m, 64] (zeros past r), a [r, k].
+hipError_t launch_side_down(const int8_t* qa, int64_t ldqa, const float* sa, const void* a, bool a_bf16, int64_t lda,
+                            int64_t m, int64_t k, int r, float* t, hipStream_t stream);
+
+struct SideGradArgs {
+  const void* dy;  // [m, n]
+  int dy_bf16;
+  int64_t lddy;
+  const int8_t* qa;  // [m, k]
+  int64_t ldqa;
+  const float* sa;
+  const float* t;  // [m, 64]
+  const void* b;   // [n, r]
+  int b_bf16;
+  int64_t ldb;
+  float alpha;
+  int rotate;
+  int64_t m, n, k;
+  int r;
+  float* dt;  // [m, 64]
+  float* da;  // [r, k]
+  int64_t ldda;
+  float* db;  // [n, r]
+  int64_t lddb;
+  float* ws;  // side_grad_workspace_floats(m, n, k, r) floats
+};
+hipError_t launch_side_grad(const SideGradArgs& a, hipStream_t stream);
+int64_t side_grad_workspace_floats(int64_t m, int64_t n, int64_t k, int64_t r);
+
 }  // namespace tp

@@ -77,7 +77,7 @@ from .quantize import (
 from .products import qgemm_w8, qgemm_w4, qgemm_w8a8, qgemm_w4a8, int_accumulate, group_accumulate
 from .ffn import silu_mul, swiglu_bf16, ffn_middle_int8, ffn_middle_rotated
 from .loader import dequantize, dequantize_unrotate, requantize
-from .lora import lora_delta, lora_add
+from .lora import lora_delta, lora_add, lora_down_codes, lora_grad_codes
 from .norm import stream_sum, rmsnorm, rmsnorm_backward
 
 __all__ = [
@@ -95,6 +95,8 @@ __all__ = [
     "stream_sum",
     "rmsnorm",
     "rmsnorm_backward",
+    "lora_down_codes",
+    "lora_grad_codes",
     "lora_delta",
     "lora_add",
     "dequantize",

@@ -19,6 +19,8 @@ Reading (also in the design notes):
 
 import numpy as np
 
+from .hadamard import rotate_groups
+
 
 def lora_delta(x, a, b, alpha):
     """alpha * (x . a^T) . b^T in fp64 ([M, N])."""
@@ -31,3 +33,20 @@ def lora_delta(x, a, b, alpha):
 def lora_add(c, x, a, b, alpha):
     """c + alpha * (x . a^T) . b^T in fp64 (R21)."""
     return np.asarray(c, dtype=np.float64) + lora_delta(x, a, b, alpha)
+
+
+def lora_down_codes(qa, sa, a):
+    """T = (sa qa) . A^T in fp64: the side path's first half on int8 codes."""
+    return (np.asarray(qa, dtype=np.float64) * np.asarray(sa, dtype=np.float64)[:, None]) @ \
+        np.asarray(a, dtype=np.float64).T
+
+
+def lora_grad_codes(dy, qa, sa, t, b, alpha, rotate=False):
+    """(dA, dB, dT) of alpha (x . A^T) . B^T with x = sa qa and T = x . A^T:
+    dT = alpha dY . B, dB = alpha dY^T . T, dA = dT^T . x, rotated back per
+    256-group on request (the rotation is its own inverse)."""
+    dy, b = np.asarray(dy, dtype=np.float64), np.asarray(b, dtype=np.float64)
+    x = np.asarray(qa, dtype=np.float64) * np.asarray(sa, dtype=np.float64)[:, None]
+    dt = alpha * (dy @ b)
+    da = dt.T @ x
+    return (rotate_groups(da) if rotate else da), alpha * (dy.T @ np.asarray(t, dtype=np.float64)), dt

@@ -61,3 +61,14 @@ def assert_close(got, want, bound, bf16, what):
     bad = ~(off <= room)
     assert not np.any(bad), (f"{what}: {int(bad.sum())} of {bad.size} values out of bounds, worst "
                              f"{float(np.max(off[bad] / room[bad])):.2f} times the bound")
+
+
+def assert_sum(got, want, magnitudes, terms, what):
+    """A sum of exact products in fp32, in any order: element by element at
+    most (terms + 4) U times the sum of magnitudes (4: the factors and the
+    store)."""
+    room = 1.01 * (terms + 4) * U * magnitudes + TINY
+    off = np.abs(got - want)
+    bad = ~(off <= room)
+    assert not np.any(bad), (f"{what}: {int(bad.sum())} of {bad.size} values out of bounds, worst "
+                             f"{float(np.max(off[bad] / room[bad])):.2f} times the bound")

@@ -94,3 +94,63 @@ def test_binding_refuses_host_tensors():
     for call in (lambda: tp.tp_rmsnorm_rotate(x), lambda: tp.tp_rmsnorm_rotate_backward(x, x)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+# ------------------------------------------------- side path on 8-bit activations
+def dn(lib, q=A, ldq=512, s=B, a=C, adt=0, lda=512, m=64, k=512, r=16, t=D, tb=1 << 20):
+    return lib.tp_lora_down_prequantized(q, ldq, s, a, adt, lda, m, k, r, t, tb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=300), 3), (dict(k=0), 2), (dict(m=-1), 2), (dict(r=0), 2), (dict(r=65), 2),
+    (dict(q=0), 1), (dict(s=0), 1), (dict(a=0), 1), (dict(t=0), 1),
+    (dict(ldq=511), 4), (dict(lda=500), 4), (dict(q=A + 8), 5), (dict(ldq=520), 5), (dict(a=C + 8), 5),
+    (dict(s=B + 1), 5), (dict(t=D + 4), 5), (dict(adt=4), 6), (dict(tb=64 * 256 - 1), 9),
+    (dict(lda=2 ** 62), 8), (dict(t=A + 1024), 10), (dict(t=B), 10), (dict(t=C), 10),
+])
+def test_down_refusals(lib, kw, status):
+    assert dn(lib, **kw) == status, _err(lib)
+    assert _err(lib)
+
+
+H, I, J = (0x10000000 * i for i in range(8, 11))
+
+
+def gr(lib, dy=A, ydt=0, lddy=512, q=B, ldq=512, s=C, t=D, b=E, bdt=0, ldb=16, alpha=1.0, fl=0, m=64, n=512, k=512,
+       r=16, dt=F, da=G, ldda=512, db=H, lddb=16, ws=I, wsb=1 << 26):
+    return lib.tp_lora_grad_prequantized(dy, ydt, lddy, q, ldq, s, t, b, bdt, ldb, alpha, fl, m, n, k, r, dt, da, ldda,
+                                         db, lddb, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=300), 3), (dict(k=0), 2), (dict(m=-1), 2), (dict(n=-1), 2), (dict(r=0), 2), (dict(r=65, ldb=68), 2),
+    (dict(m=2 ** 28), 2), (dict(n=2 ** 28, lddy=2 ** 28), 2),
+    (dict(dy=0), 1), (dict(q=0), 1), (dict(s=0), 1), (dict(t=0), 1), (dict(b=0), 1), (dict(dt=0), 1),
+    (dict(da=0), 1), (dict(db=0), 1),
+    (dict(lddy=511), 4), (dict(ldq=500), 4), (dict(ldb=15), 4), (dict(ldda=511), 4), (dict(lddb=15), 4),
+    (dict(dy=A + 8), 5), (dict(q=B + 4), 5), (dict(b=E + 4), 5), (dict(dt=F + 4), 5), (dict(da=G + 4), 5),
+    (dict(db=H + 2), 5), (dict(ws=I + 8), 5), (dict(ldb=17), 5), (dict(ldda=513), 5),
+    (dict(ydt=2), 6), (dict(bdt=2), 6), (dict(fl=2), 11), (dict(ws=0), 9), (dict(wsb=16), 9),
+    (dict(lddy=2 ** 62), 8),
+    (dict(dt=A), 10), (dict(da=B), 10), (dict(db=C), 10), (dict(ws=D), 10), (dict(ws=E), 10), (dict(dt=D), 10),
+    (dict(da=F), 10), (dict(db=G), 10), (dict(ws=F), 10), (dict(ws=G), 10), (dict(ws=H), 10),
+])
+def test_grad_refusals(lib, kw, status):
+    assert gr(lib, **kw) == status, _err(lib)
+    assert _err(lib)
+
+
+def test_grad_workspace_query(lib):
+    assert lib.tp_lora_grad_workspace_size(64, 512, 512, 16) > 0
+    for args in ((-1, 8, 256, 4), (8, -1, 256, 4), (8, 8, 300, 4), (8, 8, 0, 4), (8, 8, 256, 0), (8, 8, 256, 65),
+                 (2 ** 28, 8, 256, 4), (8, 2 ** 28, 256, 4)):
+        assert lib.tp_lora_grad_workspace_size(*args) == 0
+    assert lib.tp_lora_grad_workspace_size(0, 8, 256, 4) == 0  # sums over nothing
+
+
+def test_side_binding_refuses_host_tensors():
+    q, s, t = torch.zeros((4, 256), dtype=torch.int8), torch.zeros(4), torch.zeros((4, 64))
+    with pytest.raises(ValueError, match="CUDA"):
+        tp.tp_lora_down_prequantized(q, s, torch.zeros((8, 256)))
+    with pytest.raises(ValueError, match="CUDA"):
+        tp.tp_lora_grad_prequantized(torch.zeros((4, 16)), q, s, t, torch.zeros((16, 8)), 1.0)

@@ -57,3 +57,31 @@ def test_norm_gradient_against_differences(rotate):
     dx, dgamma = oracle.rmsnorm_backward(dy, t, gamma, 1e-3, dsum=ds, rotate=rotate)
     assert np.allclose(dx, _differences(lambda v: loss(v, gamma), t.copy()), rtol=1e-6, atol=1e-6)
     assert np.allclose(dgamma, _differences(lambda v: loss(t, v), gamma.copy()), rtol=1e-6, atol=1e-6)
+
+
+def test_side_path_gradients_by_loops_and_differences():
+    rng = np.random.default_rng(5)
+    m, n, k, r, alpha = 3, 5, 256, 2, 1.5
+    qa = rng.integers(-127, 128, size=(m, k)).astype(np.int8)
+    sa = rng.uniform(0.5, 2.0, size=m).astype(np.float32)
+    a, b = rng.standard_normal((r, k)) / 100, rng.standard_normal((n, r))
+    dy = rng.standard_normal((m, n))
+    t = oracle.lora_down_codes(qa, sa, a)
+    for i in range(m):
+        for j in range(r):
+            assert np.isclose(t[i, j], sum(float(sa[i]) * int(qa[i, q]) * a[j, q] for q in range(k)), rtol=1e-12)
+    da, db, dt = oracle.lora_grad_codes(dy, qa, sa, t, b, alpha)
+
+    def loss(a, b):
+        return np.sum(dy * alpha * (oracle.lora_down_codes(qa, sa, a) @ b.T))
+
+    assert np.allclose(da, _differences(lambda v: loss(v, b), a.copy(), 1e-4), rtol=1e-7, atol=1e-6)
+    assert np.allclose(db, _differences(lambda v: loss(a, v), b.copy(), 1e-4), rtol=1e-7, atol=1e-6)
+    assert np.allclose(dt, alpha * dy @ b, rtol=1e-14)
+    # trained un-rotated: T = x . (A Q)^T, so the gradient is the codes' domain's times Q
+    back, _, _ = oracle.lora_grad_codes(dy, qa, sa, t, b, alpha, rotate=True)
+
+    def loss_rot(a):
+        return np.sum(dy * alpha * (oracle.lora_down_codes(qa, sa, oracle.rotate_groups(a)) @ b.T))
+
+    assert np.allclose(back, _differences(loss_rot, a.copy(), 1e-4), rtol=1e-7, atol=1e-6)
