@@ -576,6 +576,80 @@ tp_status tp_lora_grad_prequantized(const void* dy, tp_dtype dy_dtype, int64_t l
                                     int64_t r, float* dt, float* da, int64_t ldda, float* db, int64_t lddb,
                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* layout of tp_qk_norm_rope: where the two members of a rotated pair sit. */
+#define TP_ROPE_INTERLEAVED 0 /* pair p: columns 2 p and 2 p + 1 of a head  */
+#define TP_ROPE_HALVES 1      /* pair p: columns p and pairs + p of a head  */
+
+/*
+ * tp_qk_norm_rope -- the RMS norm of each head of q and k, and rotary positions
+ * with one to four axes (time, height, width), in one pass behind the qkv
+ * projection (TensorFold pull request #948, first comment: q/k norm and rotary
+ * among the row kernels around the projections).
+ *
+ *   x, per head of head_dim columns:
+ *   n        x[i] * gamma[i] / sqrt(mean(x^2) + eps); x itself where the tensor's
+ *            gamma is NULL.
+ *   theta_p  (double)positions[row, pair_axis[p]] * (double)inv_freq[p], in fp64
+ *            for positions of any size, negative ones included.
+ *   out      pair (a, b) of n -> (a cos theta - b sin theta,
+ *            a sin theta + b cos theta); columns past the 2 * pairs rotated ones
+ *            are n's.
+ *
+ *   q, k     [m, heads * head_dim], x_dtype, row pitches ldq and ldk: column
+ *            views of one qkv output, or buffers of their own; heads_q and
+ *            heads_k may differ (shared key heads) and may be 0 (pointers then
+ *            NULL). head_dim a multiple of 8, at most 256; heads_q + heads_k at
+ *            most 4096.
+ *   q_gamma, k_gamma  [head_dim], g_dtype, contiguous, 16-byte aligned, or NULL
+ *            (that tensor is not normed). eps positive and finite.
+ *   positions  int32 [m, axes], row pitch ldpos elements, 4-byte aligned; axes
+ *            1..4. inv_freq fp32 [pairs].
+ *   pair_axis  HOST array of `pairs` axis numbers below axes, read during the
+ *            call. pairs a multiple of 4, 0 .. head_dim / 2; with pairs == 0
+ *            positions, inv_freq and pair_axis may be NULL.
+ *   q_out, k_out  [m, heads * head_dim], out_dtype, row pitches ldqo and ldko;
+ *            each may be its input itself (same pointer, type and pitch), and
+ *            both may be column views of one buffer. Any other overlap with an
+ *            input or each other is refused.
+ *   fp32 arithmetic (angles apart), one rounding; the squares of a head have to
+ *   add up within fp32's range. All matrices have 16-byte aligned rows.
+ */
+tp_status tp_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, tp_dtype x_dtype, int64_t m,
+                          int64_t heads_q, int64_t heads_k, int64_t head_dim, const void* q_gamma,
+                          const void* k_gamma, tp_dtype g_dtype, double eps, const int32_t* positions,
+                          int64_t ldpos, int axes, const float* inv_freq, const uint8_t* pair_axis, int64_t pairs,
+                          int layout, void* q_out, int64_t ldqo, void* k_out, int64_t ldko, tp_dtype out_dtype,
+                          hipStream_t stream);
+
+/*
+ * tp_qk_norm_rope_backward -- the gradients of tp_qk_norm_rope: g is dq_out
+ * (dk_out) with every pair turned back by theta; then, per head,
+ *
+ *   dx[i]      rr gamma[i] g[i] - x[i] rr^3 mean(gamma g x)   (g where the tensor
+ *              is not normed), rr = 1 / sqrt(mean(x^2) + eps)
+ *   dgamma[i]  sum over rows and heads of g[i] x[i] rr
+ *
+ *   dq_out, dk_out  [m, heads * head_dim], dy_dtype, row pitches lddqo, lddko.
+ *   q, k     the forward's inputs, x_dtype; used (and required) only for a tensor
+ *            that is normed.
+ *   dq, dk   dx_dtype, row pitches lddq and lddk; each may be its dq_out (dk_out)
+ *            or its q (k) itself, and both may be column views of one buffer.
+ *   dq_gamma, dk_gamma  fp32 [head_dim], or NULL (not wanted); only for a tensor
+ *            that is normed.
+ *   workspace  tp_qk_norm_rope_workspace_size(m, heads_q, heads_k, head_dim)
+ *            bytes, 16-byte aligned, where a dgamma is wanted.
+ *   Other arguments as in tp_qk_norm_rope. fp32 sums in a fixed order.
+ */
+size_t tp_qk_norm_rope_workspace_size(int64_t m, int64_t heads_q, int64_t heads_k, int64_t head_dim);
+tp_status tp_qk_norm_rope_backward(const void* dq_out, int64_t lddqo, const void* dk_out, int64_t lddko,
+                                   tp_dtype dy_dtype, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                   tp_dtype x_dtype, int64_t m, int64_t heads_q, int64_t heads_k, int64_t head_dim,
+                                   const void* q_gamma, const void* k_gamma, tp_dtype g_dtype, double eps,
+                                   const int32_t* positions, int64_t ldpos, int axes, const float* inv_freq,
+                                   const uint8_t* pair_axis, int64_t pairs, int layout, void* dq, int64_t lddq,
+                                   void* dk, int64_t lddk, tp_dtype dx_dtype, float* dq_gamma, float* dk_gamma,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* tp_status_string(tp_status status);
 

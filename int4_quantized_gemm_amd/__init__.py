@@ -22,6 +22,10 @@ The operators around the projections of a block (block_ops.py):
     tp_lora_down_prequantized(qa, sa, lora_a)  -> T (the side path's first half on 8-bit activations)
     tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha)
                                                -> dA, dB, dT (from the 8-bit activations)
+    tp_qk_norm_rope(q, k, head_dim, positions, inv_freq)
+                                               -> q, k normed per head and turned to their positions
+    tp_qk_norm_rope_backward(dq_out, dk_out, q, k, ...)
+                                               -> dq, dk, dq_gamma, dk_gamma
 """
 
 import torch
@@ -30,7 +34,8 @@ from . import _lib
 from ._lib import TPError, TP_A_PREROTATED, TP_A_ROTATE, TP_FFN_OUT_BF16, TP_FFN_OUT_I8  # noqa: F401
 from .block_ops import (  # noqa: F401
     tp_lora_down_prequantized, tp_lora_grad_prequantized, tp_lora_grad_workspace_size,
-    tp_rmsnorm_backward_workspace_size, tp_rmsnorm_rotate, tp_rmsnorm_rotate_backward)
+    tp_qk_norm_rope, tp_qk_norm_rope_backward, tp_qk_norm_rope_workspace_size, tp_rmsnorm_backward_workspace_size,
+    tp_rmsnorm_rotate, tp_rmsnorm_rotate_backward)
 
 _DTYPE = {torch.float32: _lib.TP_F32, torch.bfloat16: _lib.TP_BF16}
 

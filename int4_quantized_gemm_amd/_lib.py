@@ -33,6 +33,7 @@ TP_OP_QGEMM_W8, TP_OP_QGEMM_W4, TP_OP_QGEMM_W8A8, TP_OP_QGEMM_W8A8_PREQUANTIZED 
 TP_OP_QGEMM_W4A8, TP_OP_QGEMM_W4A8_PREQUANTIZED = 5, 6
 TP_FFN_OUT_I8, TP_FFN_OUT_BF16 = 0, 1
 TP_NORM_OUT_I8, TP_NORM_OUT_BF16 = 0, 1
+TP_ROPE_INTERLEAVED, TP_ROPE_HALVES = 0, 1
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -76,6 +77,12 @@ SIGNATURES = {
     "tp_lora_grad_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
     "tp_lora_grad_prequantized": (_int, [_p, _int, _i64, _p, _i64, _p, _p, _p, _int, _i64, ctypes.c_float, _int, _i64,
                                          _i64, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _sz, _p]),
+    "tp_qk_norm_rope": (_int, [_p, _i64, _p, _i64, _int, _i64, _i64, _i64, _i64, _p, _p, _int, _dbl, _p, _i64, _int, _p,
+                               _p, _i64, _int, _p, _i64, _p, _i64, _int, _p]),
+    "tp_qk_norm_rope_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
+    "tp_qk_norm_rope_backward": (_int, [_p, _i64, _p, _i64, _int, _p, _i64, _p, _i64, _int, _i64, _i64, _i64, _i64, _p,
+                                        _p, _int, _dbl, _p, _i64, _int, _p, _p, _i64, _int, _p, _i64, _p, _i64, _int,
+                                        _p, _p, _p, _sz, _p]),
     "tp_status_string": (ctypes.c_char_p, [_int]),
     "tp_last_error_message": (ctypes.c_char_p, []),
     "tp_abi_version": (_int, []),

@@ -5,6 +5,8 @@
     tp_lora_down_prequantized(qa, sa, lora_a)     -> T
     tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha)
                                                   -> dA, dB, dT
+    tp_qk_norm_rope(q, k, head_dim, positions, inv_freq)          -> q, k turned to their positions
+    tp_qk_norm_rope_backward(dq_out, dk_out, q, k, head_dim, ...) -> dq, dk, dq_gamma, dk_gamma
 
 Like the rest of the package, each function has the name of the C entry point
 it calls, allocates what it is not given, and runs on the current stream of its
@@ -15,7 +17,8 @@ of a call sit on one device.
 import torch
 
 from . import _lib
-from ._lib import TP_A_PREROTATED, TP_A_ROTATE, TP_NORM_OUT_BF16, TP_NORM_OUT_I8
+from ._lib import (TP_A_PREROTATED, TP_A_ROTATE, TP_NORM_OUT_BF16, TP_NORM_OUT_I8, TP_ROPE_HALVES,
+                   TP_ROPE_INTERLEAVED)
 
 _DTYPE = {torch.float32: _lib.TP_F32, torch.bfloat16: _lib.TP_BF16}
 _KIND = {"i8": (TP_NORM_OUT_I8, torch.int8), "bf16": (TP_NORM_OUT_BF16, torch.bfloat16)}
@@ -266,3 +269,139 @@ def tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha, rotate=False, da=Non
         _dt(lora_b, "lora_b"), ldb, float(alpha), TP_A_ROTATE if rotate else TP_A_PREROTATED, m, n, k, r,
         dt.data_ptr(), da.data_ptr(), ldda, db.data_ptr(), lddb, ws_ptr, ws_bytes, _raw_stream(dev)))
     return da, db, dt
+
+
+_LAYOUT = {"interleaved": TP_ROPE_INTERLEAVED, "halves": TP_ROPE_HALVES}
+
+
+def _heads(t, name, m, head_dim, dtype=None):
+    """Row pitch and head count of a [m, heads * head_dim] matrix."""
+    ld = _mat(t, name, dtype=dtype)
+    if t.shape[0] != m or t.shape[1] % head_dim != 0:
+        raise ValueError(f"{name} must be [{m}, heads * {head_dim}], got shape {tuple(t.shape)}")
+    return ld, t.shape[1] // head_dim
+
+
+def _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps):
+    """The arguments that forward and backward share, in the C order."""
+    if layout not in _LAYOUT:
+        raise ValueError("layout must be 'interleaved' or 'halves'")
+    qg, g_dt = _weight(q_gamma, "q_gamma", head_dim)
+    kg, k_dt = _weight(k_gamma, "k_gamma", head_dim)
+    if q_gamma is not None and k_gamma is not None and g_dt != k_dt:
+        raise TypeError("q_gamma and k_gamma must have one dtype")
+    if q_gamma is None:
+        g_dt = k_dt
+    pairs = 0 if inv_freq is None else inv_freq.shape[0]
+    axes, ldpos, pos_ptr, freq_ptr, axis = 1, 0, None, None, None
+    if pairs:
+        if positions is None:
+            raise ValueError("positions are needed")
+        if positions.dim() == 1:
+            positions = positions[:, None]
+        ldpos = _mat(positions, "positions", dtype=torch.int32)
+        if positions.shape[0] != m:
+            raise ValueError(f"positions must have {m} rows, got shape {tuple(positions.shape)}")
+        axes = positions.shape[1]
+        pos_ptr = positions.data_ptr()
+        freq_ptr = _vec(inv_freq, "inv_freq", pairs, torch.float32).data_ptr()
+        axis = bytes(pairs) if pair_axis is None else bytes(pair_axis)
+        if len(axis) != pairs:
+            raise ValueError(f"pair_axis must have {pairs} entries, got {len(axis)}")
+    return (qg, kg, g_dt, eps, pos_ptr, ldpos, axes, freq_ptr, axis, pairs, _LAYOUT[layout])
+
+
+def tp_qk_norm_rope(q, k, head_dim, positions=None, inv_freq=None, pair_axis=None, layout="interleaved", q_gamma=None,
+                    k_gamma=None, eps=1e-6, out_dtype=None, q_out=None, k_out=None, stream=None):
+    """The RMS norm of each head of q and k (where its gamma is given), then
+    rotary positions. q, k [m, heads * head_dim] (views of one qkv output, of
+    different head counts); positions int32 [m, axes] (or [m]); inv_freq fp32
+    [pairs]; pair_axis the axis of each pair (host integers, default all 0);
+    layout "interleaved" (pairs of neighbours) or "halves". Columns past the
+    rotated ones are passed on. Returns (q_out, k_out), which may be the inputs
+    themselves; default dtype: the inputs'."""
+    dev = _device(q, k=k, positions=positions, inv_freq=inv_freq, q_gamma=q_gamma, k_gamma=k_gamma, q_out=q_out,
+                  k_out=k_out)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return tp_qk_norm_rope(q, k, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps,
+                                   out_dtype, q_out, k_out)
+    m = q.shape[0]
+    ldq, hq = _heads(q, "q", m, head_dim)
+    ldk, hk = _heads(k, "k", m, head_dim, q.dtype)
+    shared = _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps)
+    if out_dtype is None:
+        out_dtype = q.dtype if q_out is None else q_out.dtype
+    if q_out is None:
+        q_out = torch.empty((m, hq * head_dim), dtype=out_dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty((m, hk * head_dim), dtype=out_dtype, device=dev)
+    ldqo = _mat(q_out, "q_out", tuple(q.shape), out_dtype)
+    ldko = _mat(k_out, "k_out", tuple(k.shape), out_dtype)
+    _lib.check(_lib.load().tp_qk_norm_rope(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, _dt(q, "q"), m, hq, hk, head_dim, *shared, q_out.data_ptr(), ldqo,
+        k_out.data_ptr(), ldko, _dt(q_out, "q_out"), _raw_stream(dev)))
+    return q_out, k_out
+
+
+def tp_qk_norm_rope_workspace_size(m, heads_q, heads_k, head_dim):
+    """Bytes of workspace tp_qk_norm_rope_backward needs for the weights' gradients."""
+    return int(_lib.load().tp_qk_norm_rope_workspace_size(m, heads_q, heads_k, head_dim))
+
+
+def tp_qk_norm_rope_backward(dq_out, dk_out, q, k, head_dim, positions=None, inv_freq=None, pair_axis=None,
+                             layout="interleaved", q_gamma=None, k_gamma=None, eps=1e-6, dx_dtype=None,
+                             want_dgamma=True, dq=None, dk=None, dq_gamma=None, dk_gamma=None, workspace=None,
+                             stream=None):
+    """Gradients of tp_qk_norm_rope: (dq, dk, dq_gamma, dk_gamma), the latter
+    None for a tensor without a norm or where want_dgamma is False. q and k (the
+    forward's inputs) may be None for a tensor without a norm. Default dtype of
+    dq and dk: dq_out's."""
+    dev = _device(dq_out, dk_out=dk_out, q=q, k=k, positions=positions, inv_freq=inv_freq, q_gamma=q_gamma,
+                  k_gamma=k_gamma, dq=dq, dk=dk, dq_gamma=dq_gamma, dk_gamma=dk_gamma, workspace=workspace)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return tp_qk_norm_rope_backward(dq_out, dk_out, q, k, head_dim, positions, inv_freq, pair_axis, layout,
+                                            q_gamma, k_gamma, eps, dx_dtype, want_dgamma, dq, dk, dq_gamma, dk_gamma,
+                                            workspace)
+    m = dq_out.shape[0]
+    lddqo, hq = _heads(dq_out, "dq_out", m, head_dim)
+    lddko, hk = _heads(dk_out, "dk_out", m, head_dim, dq_out.dtype)
+    shared = _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps)
+    x_ptr, x_ld, x_dt = [None, None], [0, 0], None
+    for i, (x, gamma, like, name) in enumerate(((q, q_gamma, dq_out, "q"), (k, k_gamma, dk_out, "k"))):
+        if gamma is None:
+            continue
+        if x is None:
+            raise ValueError(f"{name} is needed for the gradient of its norm")
+        x_ld[i] = _mat(x, name, tuple(like.shape))
+        if x_dt is not None and _dt(x, name) != x_dt:
+            raise TypeError("q and k must have one dtype")
+        x_ptr[i], x_dt = x.data_ptr(), _dt(x, name)
+    if dx_dtype is None:
+        dx_dtype = dq_out.dtype if dq is None else dq.dtype
+    if dq is None:
+        dq = torch.empty(tuple(dq_out.shape), dtype=dx_dtype, device=dev)
+    if dk is None:
+        dk = torch.empty(tuple(dk_out.shape), dtype=dx_dtype, device=dev)
+    lddq = _mat(dq, "dq", tuple(dq_out.shape), dx_dtype)
+    lddk = _mat(dk, "dk", tuple(dk_out.shape), dx_dtype)
+    if q_gamma is None and dq_gamma is not None or k_gamma is None and dk_gamma is not None:
+        raise ValueError("the gradient of a weight that is not given")
+    if want_dgamma and q_gamma is not None and dq_gamma is None:
+        dq_gamma = torch.empty((head_dim,), dtype=torch.float32, device=dev)
+    if want_dgamma and k_gamma is not None and dk_gamma is None:
+        dk_gamma = torch.empty((head_dim,), dtype=torch.float32, device=dev)
+    dg_ptr = [None if t is None else _vec(t, n, head_dim, torch.float32).data_ptr()
+              for t, n in ((dq_gamma, "dq_gamma"), (dk_gamma, "dk_gamma"))]
+    ws_ptr = ws = None
+    ws_bytes = 0
+    if dq_gamma is not None or dk_gamma is not None:
+        ws_ptr, ws_bytes, ws = _scratch(workspace, tp_qk_norm_rope_workspace_size(m, hq, hk, head_dim), dev)
+    _lib.check(_lib.load().tp_qk_norm_rope_backward(
+        dq_out.data_ptr(), lddqo, dk_out.data_ptr(), lddko, _dt(dq_out, "dq_out"), x_ptr[0], x_ld[0], x_ptr[1],
+        x_ld[1], _lib.TP_F32 if x_dt is None else x_dt, m, hq, hk, head_dim, *shared, dq.data_ptr(), lddq,
+        dk.data_ptr(), lddk, _dt(dq, "dq"), dg_ptr[0], dg_ptr[1], ws_ptr, ws_bytes, _raw_stream(dev)))
+    return dq, dk, dq_gamma, dk_gamma

@@ -926,5 +926,209 @@ tp_status tp_lora_grad_prequantized(const void* dy, tp_dtype dy_dtype, int64_t l
   return hip_status(tp::launch_side_grad(a, stream), "side path gradient launch");
 }
 
+// ----------------------------------------------- norm and positions of q and k
+
+namespace {
+
+// A checked matrix: where its rows are.
+struct MatRef {
+  const void* p = nullptr;
+  int dtype = 0;
+  int64_t ld = 0;
+  int64_t pitch = 0, row = 0;  // bytes
+  Extent e;
+};
+
+tp_status check_ref(const char* name, const void* p, tp_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                    MatRef* r) {
+  const int64_t es = dtype_size(dtype);
+  TP_TRY(check_matrix(name, p, rows, cols * es, ld, es, &r->e));
+  r->p = p;
+  r->dtype = dtype;
+  r->ld = ld;
+  r->pitch = ld * es;
+  r->row = cols * es;
+  return TP_OK;
+}
+
+// Whether two matrices share bytes; column views of one buffer (equal pitches)
+// do only where their columns do.
+bool share(const MatRef& a, const MatRef& b) {
+  if (!overlaps(a.e, b.e)) return false;
+  if (a.pitch != b.pitch || a.pitch == 0) return true;
+  const MatRef &lo = a.e.lo <= b.e.lo ? a : b, &hi = a.e.lo <= b.e.lo ? b : a;
+  const int64_t delta = (int64_t)((hi.e.lo - lo.e.lo) % (uintptr_t)lo.pitch);
+  return !(delta >= lo.row && delta + hi.row <= lo.pitch);
+}
+
+bool same_ref(const MatRef& a, const MatRef& b) { return a.p == b.p && a.dtype == b.dtype && a.ld == b.ld; }
+
+// What forward and backward have in common.
+tp_status check_rope(int64_t m, int64_t heads_q, int64_t heads_k, int64_t head_dim, const void* q_gamma,
+                     const void* k_gamma, tp_dtype g_dtype, double eps, const int32_t* positions, int64_t ldpos,
+                     int axes, const float* inv_freq, const uint8_t* pair_axis, int64_t pairs, int layout,
+                     tp::RopeArgs* a, Extent* small /* [4] */) {
+  if (m < 0 || m > INT_MAX) return fail(TP_ERR_BAD_SHAPE, "m=%lld", (long long)m);
+  if (heads_q < 0 || heads_k < 0 || heads_q > tp::ROPE_MAX_HEADS || heads_k > tp::ROPE_MAX_HEADS ||
+      heads_q + heads_k > tp::ROPE_MAX_HEADS)
+    return fail(TP_ERR_BAD_SHAPE, "heads_q=%lld, heads_k=%lld: 0..%d together", (long long)heads_q, (long long)heads_k,
+                tp::ROPE_MAX_HEADS);
+  if (head_dim < 8 || head_dim % 8 != 0 || head_dim > tp::ROPE_MAX_DIM)
+    return fail(TP_ERR_BAD_SHAPE, "head_dim=%lld: a multiple of 8 up to %d", (long long)head_dim, tp::ROPE_MAX_DIM);
+  if (pairs < 0 || pairs % 4 != 0 || 2 * pairs > head_dim)
+    return fail(TP_ERR_BAD_SHAPE, "pairs=%lld: a multiple of 4 up to head_dim / 2", (long long)pairs);
+  if (layout != TP_ROPE_INTERLEAVED && layout != TP_ROPE_HALVES) return fail(TP_ERR_BAD_FLAGS, "layout=%d", layout);
+  TP_TRY(check_eps(eps));
+  TP_TRY(check_weight("q_gamma", q_gamma, g_dtype, head_dim, &small[0]));
+  TP_TRY(check_weight("k_gamma", k_gamma, g_dtype, head_dim, &small[1]));
+  small[2] = small[3] = Extent{};
+  if (pairs > 0) {
+    if (axes < 1 || axes > 4) return fail(TP_ERR_BAD_SHAPE, "axes=%d outside [1, 4]", axes);
+    if (!pair_axis) return fail(TP_ERR_NULL_POINTER, "pair_axis is NULL");
+    for (int64_t p = 0; p < pairs; ++p) {
+      if (pair_axis[p] >= axes)
+        return fail(TP_ERR_BAD_VALUE, "pair_axis[%lld]=%d, axes=%d", (long long)p, (int)pair_axis[p], axes);
+      a->axis[p] = pair_axis[p];
+    }
+    TP_TRY(check_matrix("positions", positions, m, (int64_t)axes * 4, ldpos, 4, &small[2], 4));
+    TP_TRY(check_vector("inv_freq", inv_freq, pairs, &small[3]));
+  }
+  a->m = m;
+  a->heads_q = (int)heads_q;
+  a->heads_k = (int)heads_k;
+  a->head_dim = (int)head_dim;
+  a->q_gamma = {q_gamma, q_gamma && g_dtype == TP_BF16};
+  a->k_gamma = {k_gamma, k_gamma && g_dtype == TP_BF16};
+  a->eps = eps;
+  a->positions = positions;
+  a->ldpos = ldpos;
+  a->inv_freq = inv_freq;
+  a->pairs = (int)pairs;
+  a->halves = layout == TP_ROPE_HALVES;
+  return TP_OK;
+}
+
+}  // namespace
+
+tp_status tp_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, tp_dtype x_dtype, int64_t m,
+                          int64_t heads_q, int64_t heads_k, int64_t head_dim, const void* q_gamma,
+                          const void* k_gamma, tp_dtype g_dtype, double eps, const int32_t* positions, int64_t ldpos,
+                          int axes, const float* inv_freq, const uint8_t* pair_axis, int64_t pairs, int layout,
+                          void* q_out, int64_t ldqo, void* k_out, int64_t ldko, tp_dtype out_dtype,
+                          hipStream_t stream) {
+  if (!dtype_ok(x_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "x_dtype %d is not TP_F32 or TP_BF16", (int)x_dtype);
+  if (!dtype_ok(out_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "out_dtype %d is not TP_F32 or TP_BF16", (int)out_dtype);
+  tp::RopeArgs a{};
+  Extent small[4];
+  TP_TRY(check_rope(m, heads_q, heads_k, head_dim, q_gamma, k_gamma, g_dtype, eps, positions, ldpos, axes, inv_freq,
+                    pair_axis, pairs, layout, &a, small));
+  MatRef in[2], out[2];
+  TP_TRY(check_ref("q", q, x_dtype, m, heads_q * head_dim, ldq, &in[0]));
+  TP_TRY(check_ref("k", k, x_dtype, m, heads_k * head_dim, ldk, &in[1]));
+  TP_TRY(check_ref("q_out", q_out, out_dtype, m, heads_q * head_dim, ldqo, &out[0]));
+  TP_TRY(check_ref("k_out", k_out, out_dtype, m, heads_k * head_dim, ldko, &out[1]));
+  for (int o = 0; o < 2; ++o) {
+    for (int i = 0; i < 2; ++i)
+      if (share(out[o], in[i]) && !(o == i && same_ref(out[o], in[i])))
+        return fail(TP_ERR_BAD_ALIASING, "%s overlaps an input without being its own", o ? "k_out" : "q_out");
+    for (const Extent& e : small)
+      if (overlaps(out[o].e, e)) return fail(TP_ERR_BAD_ALIASING, "an output overlaps a weight, positions or inv_freq");
+  }
+  if (share(out[0], out[1])) return fail(TP_ERR_BAD_ALIASING, "q_out and k_out overlap");
+  if (m == 0 || heads_q + heads_k == 0) return ok();
+  a.q = q;
+  a.ldq = ldq;
+  a.k = k;
+  a.ldk = ldk;
+  a.x_bf16 = x_dtype == TP_BF16;
+  a.q_out = q_out;
+  a.ldqo = ldqo;
+  a.k_out = k_out;
+  a.ldko = ldko;
+  a.out_bf16 = out_dtype == TP_BF16;
+  return hip_status(tp::launch_rope(a, stream), "rope launch");
+}
+
+size_t tp_qk_norm_rope_workspace_size(int64_t m, int64_t heads_q, int64_t heads_k, int64_t head_dim) {
+  if (m <= 0 || m > INT_MAX || heads_q < 0 || heads_k < 0 || heads_q > tp::ROPE_MAX_HEADS ||
+      heads_k > tp::ROPE_MAX_HEADS || heads_q + heads_k > tp::ROPE_MAX_HEADS || head_dim < 8 || head_dim % 8 != 0 ||
+      head_dim > tp::ROPE_MAX_DIM)
+    return 0;
+  return (size_t)(tp::rope_partial_rows(m, (int)(heads_q + heads_k), (int)head_dim) * 2 * head_dim * 4);
+}
+
+tp_status tp_qk_norm_rope_backward(const void* dq_out, int64_t lddqo, const void* dk_out, int64_t lddko,
+                                   tp_dtype dy_dtype, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                   tp_dtype x_dtype, int64_t m, int64_t heads_q, int64_t heads_k, int64_t head_dim,
+                                   const void* q_gamma, const void* k_gamma, tp_dtype g_dtype, double eps,
+                                   const int32_t* positions, int64_t ldpos, int axes, const float* inv_freq,
+                                   const uint8_t* pair_axis, int64_t pairs, int layout, void* dq, int64_t lddq,
+                                   void* dk, int64_t lddk, tp_dtype dx_dtype, float* dq_gamma, float* dk_gamma,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!dtype_ok(dy_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "dy_dtype %d is not TP_F32 or TP_BF16", (int)dy_dtype);
+  if (!dtype_ok(dx_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "dx_dtype %d is not TP_F32 or TP_BF16", (int)dx_dtype);
+  if ((q_gamma || k_gamma) && !dtype_ok(x_dtype))
+    return fail(TP_ERR_UNSUPPORTED_DTYPE, "x_dtype %d is not TP_F32 or TP_BF16", (int)x_dtype);
+  tp::RopeArgs a{};
+  Extent small[4];
+  TP_TRY(check_rope(m, heads_q, heads_k, head_dim, q_gamma, k_gamma, g_dtype, eps, positions, ldpos, axes, inv_freq,
+                    pair_axis, pairs, layout, &a, small));
+  if ((dq_gamma && !q_gamma) || (dk_gamma && !k_gamma))
+    return fail(TP_ERR_NULL_POINTER, "the gradient of a weight that is NULL");
+  MatRef dy[2], in[2], out[2];
+  TP_TRY(check_ref("dq_out", dq_out, dy_dtype, m, heads_q * head_dim, lddqo, &dy[0]));
+  TP_TRY(check_ref("dk_out", dk_out, dy_dtype, m, heads_k * head_dim, lddko, &dy[1]));
+  if (q_gamma) TP_TRY(check_ref("q", q, x_dtype, m, heads_q * head_dim, ldq, &in[0]));
+  if (k_gamma) TP_TRY(check_ref("k", k, x_dtype, m, heads_k * head_dim, ldk, &in[1]));
+  TP_TRY(check_ref("dq", dq, dx_dtype, m, heads_q * head_dim, lddq, &out[0]));
+  TP_TRY(check_ref("dk", dk, dx_dtype, m, heads_k * head_dim, lddk, &out[1]));
+  Extent edg[2] = {}, ew;
+  if (dq_gamma) TP_TRY(check_vector("dq_gamma", dq_gamma, head_dim, &edg[0]));
+  if (dk_gamma) TP_TRY(check_vector("dk_gamma", dk_gamma, head_dim, &edg[1]));
+  const bool want = dq_gamma || dk_gamma;
+  TP_TRY(check_scratch("tp_qk_norm_rope_workspace_size", workspace, workspace_bytes,
+                       want ? (int64_t)tp_qk_norm_rope_workspace_size(m, heads_q, heads_k, head_dim) : 0, &ew));
+  for (int o = 0; o < 2; ++o) {
+    for (int i = 0; i < 2; ++i) {
+      if (share(out[o], dy[i]) && !(o == i && same_ref(out[o], dy[i])))
+        return fail(TP_ERR_BAD_ALIASING, "%s overlaps an output gradient without being its own", o ? "dk" : "dq");
+      if (share(out[o], in[i]) && !(o == i && same_ref(out[o], in[i])))
+        return fail(TP_ERR_BAD_ALIASING, "%s overlaps q or k without being its own", o ? "dk" : "dq");
+    }
+    for (const Extent& e : small)
+      if (overlaps(out[o].e, e) || overlaps(edg[o], e) || overlaps(ew, e))
+        return fail(TP_ERR_BAD_ALIASING, "an output or the workspace overlaps a weight, positions or inv_freq");
+  }
+  if (share(out[0], out[1])) return fail(TP_ERR_BAD_ALIASING, "dq and dk overlap");
+  const Extent* mats[] = {&dy[0].e, &dy[1].e, &in[0].e, &in[1].e, &out[0].e, &out[1].e};
+  for (const Extent* e : mats)
+    if (overlaps(*e, edg[0]) || overlaps(*e, edg[1]) || overlaps(*e, ew))
+      return fail(TP_ERR_BAD_ALIASING, "a weight's gradient or the workspace overlaps another operand");
+  if (overlaps(edg[0], edg[1]) || overlaps(edg[0], ew) || overlaps(edg[1], ew))
+    return fail(TP_ERR_BAD_ALIASING, "the weights' gradients and the workspace must not overlap");
+  if ((m == 0 || heads_q + heads_k == 0) && !want) return ok();
+  a.q = q;
+  a.ldq = ldq;
+  a.k = k;
+  a.ldk = ldk;
+  a.x_bf16 = (q_gamma || k_gamma) && x_dtype == TP_BF16;
+  a.q_out = dq;
+  a.ldqo = lddq;
+  a.k_out = dk;
+  a.ldko = lddk;
+  a.out_bf16 = dx_dtype == TP_BF16;
+  a.backward = 1;
+  a.dq_out = dq_out;
+  a.lddqo = lddqo;
+  a.dk_out = dk_out;
+  a.lddko = lddko;
+  a.dy_bf16 = dy_dtype == TP_BF16;
+  a.dq_gamma = dq_gamma;
+  a.dk_gamma = dk_gamma;
+  a.want_dgamma = want;
+  a.part = (float*)workspace;
+  return hip_status(tp::launch_rope(a, stream), "rope backward launch");
+}
+
 }  // extern "C"
 

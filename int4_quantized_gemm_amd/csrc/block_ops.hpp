@@ -63,8 +63,10 @@ struct NormBwdArgs {
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
 int64_t norm_bwd_partial_rows(int64_t m, int groups);
 
-// out[c] = sum over the rows p of part[p][c], added in a fixed order.
-hipError_t launch_colsum(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t stream);
+// Sums over the rows of part [rows, cols], added in a fixed order: the first
+// `first` columns to out, the others to out2 (null: not wanted).
+hipError_t launch_colsum(const float* part, int64_t rows, int64_t cols, float* out, int64_t first, float* out2,
+                         hipStream_t stream);
 
 // ------------------------------------------------------------------ side.hip
 // T = sa (qa . a^T), fp32 [m, 64] (zeros past r), a [r, k].
@@ -95,5 +97,35 @@ struct SideGradArgs {
 };
 hipError_t launch_side_grad(const SideGradArgs& a, hipStream_t stream);
 int64_t side_grad_workspace_floats(int64_t m, int64_t n, int64_t k, int64_t r);
+
+// ------------------------------------------------------------------ rope.hip
+constexpr int ROPE_MAX_DIM = 256, ROPE_MAX_PAIRS = ROPE_MAX_DIM / 2, ROPE_MAX_HEADS = 4096;
+
+struct RopeArgs {
+  const void *q, *k;  // [m, heads * head_dim]; the backward's only where there is a norm
+  int64_t ldq, ldk;
+  int x_bf16;
+  int64_t m;
+  int heads_q, heads_k, head_dim;
+  VecArg q_gamma, k_gamma;  // none: no norm
+  double eps;
+  const int32_t* positions;  // [m, axes]
+  int64_t ldpos;
+  const float* inv_freq;  // [pairs]
+  int pairs, halves;
+  void *q_out, *k_out;  // the rotated heads, or their inputs' gradients
+  int64_t ldqo, ldko;
+  int out_bf16;
+  int backward;
+  const void *dq_out, *dk_out;
+  int64_t lddqo, lddko;
+  int dy_bf16;
+  float *dq_gamma, *dk_gamma;  // null: not wanted
+  int want_dgamma;             // either of them is
+  float* part;                 // rope_partial_rows() rows of 2 head_dim floats, where want_dgamma
+  uint8_t axis[ROPE_MAX_PAIRS];
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
+int64_t rope_partial_rows(int64_t m, int heads, int d);
 
 }  // namespace tp

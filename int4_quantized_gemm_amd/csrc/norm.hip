@@ -386,9 +386,10 @@ __global__ __launch_bounds__(NT) void k_norm_bwd(NormBwdArgs a, int rows_per_blo
 }
 
 // Column sums of part [rows, cols]: 64 columns a block, 16 slices of the rows,
-// the slices joined in order.
+// the slices joined in order. The first columns go to out, the others to out2
+// (either may be null).
 __global__ __launch_bounds__(1024) void k_colsum(const float* __restrict__ part, int64_t rows, int64_t cols,
-                                                 float* __restrict__ out) {
+                                                 float* __restrict__ out, int64_t first, float* __restrict__ out2) {
   __shared__ float red[16][64];
   const int c = threadIdx.x & 63, sl = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * 64 + c;
@@ -404,7 +405,11 @@ __global__ __launch_bounds__(1024) void k_colsum(const float* __restrict__ part,
     s = red[0][c];
 #pragma unroll
     for (int w = 1; w < 16; ++w) s += red[w][c];
-    out[col] = s;
+    if (col < first) {
+      if (out != nullptr) out[col] = s;
+    } else if (out2 != nullptr) {
+      out2[col - first] = s;
+    }
   }
 }
 
@@ -485,8 +490,10 @@ int64_t norm_bwd_partial_rows(int64_t m, int groups) {
   return s.blocks * s.rows;
 }
 
-hipError_t launch_colsum(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t stream) {
-  hipLaunchKernelGGL(k_colsum, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, stream, part, rows, cols, out);
+hipError_t launch_colsum(const float* part, int64_t rows, int64_t cols, float* out, int64_t first, float* out2,
+                         hipStream_t stream) {
+  hipLaunchKernelGGL(k_colsum, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, stream, part, rows, cols, out,
+                     first, out2);
   return hipGetLastError();
 }
 
@@ -501,8 +508,8 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
   }
   if (a.dgamma == nullptr) return hipSuccess;
   // m == 0: no partial rows, so the sum is zero
-  return launch_colsum(a.part, a.m > 0 ? norm_bwd_partial_rows(a.m, a.groups) : 0, (int64_t)a.groups * 256, a.dgamma,
-                       stream);
+  const int64_t k = (int64_t)a.groups * 256;
+  return launch_colsum(a.part, a.m > 0 ? norm_bwd_partial_rows(a.m, a.groups) : 0, k, a.dgamma, k, nullptr, stream);
 }
 
 }  // namespace tp

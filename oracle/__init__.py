@@ -79,6 +79,7 @@ from .ffn import silu_mul, swiglu_bf16, ffn_middle_int8, ffn_middle_rotated
 from .loader import dequantize, dequantize_unrotate, requantize
 from .lora import lora_delta, lora_add, lora_down_codes, lora_grad_codes
 from .norm import stream_sum, rmsnorm, rmsnorm_backward
+from .rope import norm_rope, norm_rope_backward
 
 __all__ = [
     "GROUP",
@@ -95,6 +96,8 @@ __all__ = [
     "stream_sum",
     "rmsnorm",
     "rmsnorm_backward",
+    "norm_rope",
+    "norm_rope_backward",
     "lora_down_codes",
     "lora_grad_codes",
     "lora_delta",

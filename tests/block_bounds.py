@@ -72,3 +72,43 @@ def assert_sum(got, want, magnitudes, terms, what):
     bad = ~(off <= room)
     assert not np.any(bad), (f"{what}: {int(bad.sum())} of {bad.size} values out of bounds, worst "
                              f"{float(np.max(off[bad] / room[bad])):.2f} times the bound")
+
+
+def _partner(x, pairs, halves):
+    """Magnitude of each element's pair, |a| + |b|; of the element alone past
+    the rotated ones. x [m, heads, head_dim]."""
+    s = np.abs(x).copy()
+    p = np.arange(pairs)
+    first, second = (p, pairs + p) if halves else (2 * p, 2 * p + 1)
+    s[..., first] = s[..., second] = np.abs(x[..., first]) + np.abs(x[..., second])
+    return s
+
+
+def rope_forward(x, head_dim, positions, inv_freq, pair_axis, halves, gamma, eps):
+    """Before the last rounding. Cosines and sines are off by 8 U at most (the
+    fraction of a turn in fp32: pi U; sincospif: 4 U); the row factor by 10 U
+    (13 steps of a fp32 sum, so 6.5 of the root, and three roundings); a normed
+    element by 12 U, and a turned one by three roundings more."""
+    y = oracle.norm_rope(x, head_dim, positions, inv_freq, pair_axis, halves, gamma, eps)
+    h = x.reshape(x.shape[0], -1, head_dim)
+    n = h if gamma is None else oracle.rmsnorm(h, gamma, eps)
+    return y, 1.01 * (23 * U * _partner(n, len(pair_axis), halves)).reshape(x.shape)
+
+
+def rope_backward(dy, x, head_dim, positions, inv_freq, pair_axis, halves, gamma, eps, adds):
+    """(dx, bound, dgamma, bound); g is off by 11 U of its pair, the rest as in
+    norm_backward. adds: terms that a column of dgamma goes through in a row."""
+    dx, dgamma = oracle.norm_rope_backward(dy, x, head_dim, positions, inv_freq, pair_axis, halves, gamma, eps)
+    g, _ = oracle.norm_rope_backward(dy, None, head_dim, positions, inv_freq, pair_axis, halves, None, eps)
+    shape = (dy.shape[0], -1, head_dim)
+    eg = 11 * U * _partner(dy.reshape(shape), len(pair_axis), halves)
+    if gamma is None:
+        return dx, 1.01 * eg.reshape(dy.shape), None, None
+    g, x = g.reshape(shape), x.reshape(shape)
+    r = inv_rms(x, eps)
+    w = np.abs(gamma * g)
+    es = (np.abs(gamma * x) * eg).sum(axis=-1, keepdims=True) + 20 * U * (w * np.abs(x)).sum(axis=-1, keepdims=True)
+    s = np.abs((gamma * g * x).sum(axis=-1, keepdims=True))
+    bound = r * np.abs(gamma) * eg + 14 * U * r * w + np.abs(x) * r ** 3 / head_dim * (es + 40 * U * s)
+    bdg = (np.abs(x) * r * eg).sum(axis=(0, 1)) + (14 + adds) * U * (np.abs(g * x) * r).sum(axis=(0, 1))
+    return dx, 1.01 * bound.reshape(dy.shape), dgamma, 1.01 * bdg

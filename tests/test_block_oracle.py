@@ -85,3 +85,47 @@ def test_side_path_gradients_by_loops_and_differences():
         return np.sum(dy * alpha * (oracle.lora_down_codes(qa, sa, oracle.rotate_groups(a)) @ b.T))
 
     assert np.allclose(back, _differences(loss_rot, a.copy(), 1e-4), rtol=1e-7, atol=1e-6)
+
+
+def test_rope_closed_forms():
+    x = np.zeros((3, 2 * 8))
+    x[:, [0, 8]] = 1.0  # the first member of the first pair of both heads
+    pos = np.array([[0, 9], [1, 9], [-2, 9]])
+    freq = np.array([np.pi / 2, 1.0, 1.0, 1.0])
+    # interleaved: the pair is (0, 1); halves: (0, 4); quarter turns of axis 0
+    for halves, other in ((False, 1), (True, 4)):
+        y = oracle.norm_rope(x, 8, pos, freq, [0, 1, 1, 1], halves, None, 1e-6).reshape(3, 2, 8)
+        for row, (c, s) in enumerate([(1, 0), (0, 1), (-1, 0)]):
+            for head in range(2):
+                assert np.allclose(y[row, head, 0], c, atol=1e-15) and np.allclose(y[row, head, other], s, atol=1e-15)
+                assert np.count_nonzero(np.abs(np.delete(y[row, head], [0, other])) > 0) == 0
+    # a turn keeps each pair's length, and only positions' differences move q . k
+    rng = np.random.default_rng(1)
+    q, k = rng.standard_normal((2, 1, 8))
+    freq = np.array([1.0, 0.3, 0.1, 0.01])
+
+    def dot(i, j):
+        at = lambda x, p: oracle.norm_rope(x, 8, [[p]], freq, [0] * 4, True, None, 1e-6)  # noqa: E731
+        return float((at(q, i) * at(k, j)).sum())
+
+    assert np.isclose(dot(5, 3), dot(105, 103), rtol=1e-10) and np.isclose(dot(0, 0), float((q * k).sum()))
+    # past the rotated pairs a head is passed on, normed
+    y = oracle.norm_rope(np.full((1, 16), 2.0), 16, [[7]], [1.0] * 4, [0] * 4, True, np.arange(16.0), 1e-300)
+    assert np.allclose(y[0, 8:], np.arange(8.0, 16.0), rtol=1e-15)
+
+
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("normed", [False, True])
+def test_rope_gradient_against_differences(halves, normed):
+    rng = np.random.default_rng(2)
+    x, dy = rng.standard_normal((2, 2, 32))
+    gamma = 1.0 + 0.2 * rng.standard_normal(16) if normed else None
+    pos, freq, axis = rng.integers(-50, 50, size=(2, 2)), rng.uniform(0.01, 1.0, 4), [0, 0, 1, 1]
+
+    def loss(x, gamma):
+        return np.sum(dy * oracle.norm_rope(x, 16, pos, freq, axis, halves, gamma, 1e-3))
+
+    dx, dgamma = oracle.norm_rope_backward(dy, x, 16, pos, freq, axis, halves, gamma, 1e-3)
+    assert np.allclose(dx, _differences(lambda v: loss(v, gamma), x.copy()), rtol=1e-6, atol=1e-7)
+    if normed:
+        assert np.allclose(dgamma, _differences(lambda v: loss(x, v), gamma.copy()), rtol=1e-6, atol=1e-7)
