@@ -534,11 +534,16 @@ tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t 
  *            tp_hadamard_rotate_rows where they are), row pitch lda; 16-byte
  *            aligned rows; 1 <= r <= 64; k a multiple of 256.
  *   t        as in tp_lora_down.
- *   Products are exact, summed in fp32 in a fixed order, then scaled.
+ *   workspace  tp_lora_down_prequantized_workspace_size(m, k, r) bytes, 16-byte
+ *            aligned (partial sums over k; nothing is kept between calls).
+ *   Products are exact, summed in fp32 in a fixed order, then scaled. m below
+ *   2^28.
  */
+size_t tp_lora_down_prequantized_workspace_size(int64_t m, int64_t k, int64_t r);
 tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float* sa, const void* lora_a,
                                     tp_dtype a_dtype, int64_t lda, int64_t m, int64_t k, int64_t r, float* t,
-                                    size_t t_bytes, hipStream_t stream);
+                                    size_t t_bytes, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
 
 /*
  * tp_lora_grad_prequantized -- the gradients of a LoRA side path

@@ -33,7 +33,8 @@ import torch
 from . import _lib
 from ._lib import TPError, TP_A_PREROTATED, TP_A_ROTATE, TP_FFN_OUT_BF16, TP_FFN_OUT_I8  # noqa: F401
 from .block_ops import (  # noqa: F401
-    tp_lora_down_prequantized, tp_lora_grad_prequantized, tp_lora_grad_workspace_size,
+    tp_lora_down_prequantized, tp_lora_down_prequantized_workspace_size, tp_lora_grad_prequantized,
+    tp_lora_grad_workspace_size,
     tp_qk_norm_rope, tp_qk_norm_rope_backward, tp_qk_norm_rope_workspace_size, tp_rmsnorm_backward_workspace_size,
     tp_rmsnorm_rotate, tp_rmsnorm_rotate_backward)
 

@@ -73,7 +73,8 @@ SIGNATURES = {
     "tp_rmsnorm_backward_workspace_size": (_sz, [_i64, _i64]),
     "tp_rmsnorm_rotate_backward": (_int, [_p, _int, _i64, _int, _p, _int, _i64, _p, _int, _dbl, _p, _i64, _i64, _i64,
                                           _p, _int, _i64, _p, _p, _sz, _p]),
-    "tp_lora_down_prequantized": (_int, [_p, _i64, _p, _p, _int, _i64, _i64, _i64, _i64, _p, _sz, _p]),
+    "tp_lora_down_prequantized_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "tp_lora_down_prequantized": (_int, [_p, _i64, _p, _p, _int, _i64, _i64, _i64, _i64, _p, _sz, _p, _sz, _p]),
     "tp_lora_grad_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
     "tp_lora_grad_prequantized": (_int, [_p, _int, _i64, _p, _i64, _p, _p, _p, _int, _i64, ctypes.c_float, _int, _i64,
                                          _i64, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _sz, _p]),

@@ -193,15 +193,20 @@ def tp_rmsnorm_rotate_backward(dy, t, gamma=None, eps=1e-6, dsum=None, rotate=Tr
 _T = 64  # floats of a row of T and dT
 
 
-def tp_lora_down_prequantized(qa, sa, lora_a, t=None, stream=None):
+def tp_lora_down_prequantized_workspace_size(m, k, r):
+    """Bytes of workspace tp_lora_down_prequantized needs."""
+    return int(_lib.load().tp_lora_down_prequantized_workspace_size(m, k, r))
+
+
+def tp_lora_down_prequantized(qa, sa, lora_a, t=None, workspace=None, stream=None):
     """T = sa (qa . lora_a^T) in fp32 rows of 64 (zeros past r): the first half
     of the side path on activations held as int8 codes and scales; lora_a
     [r, k] in the codes' domain. Returns T [m, 64], as tp_lora_down does."""
-    dev = _device(qa, sa=sa, lora_a=lora_a, t=t)
+    dev = _device(qa, sa=sa, lora_a=lora_a, t=t, workspace=workspace)
     scope = _elsewhere(dev, stream)
     if scope is not None:
         with scope:
-            return tp_lora_down_prequantized(qa, sa, lora_a, t)
+            return tp_lora_down_prequantized(qa, sa, lora_a, t, workspace)
     ldqa = _mat(qa, "qa", dtype=torch.int8)
     m, k = qa.shape
     _vec(sa, "sa", m, torch.float32)
@@ -210,9 +215,10 @@ def tp_lora_down_prequantized(qa, sa, lora_a, t=None, stream=None):
     if lora_a.shape[1] != k:
         raise ValueError(f"lora_a must be [r, {k}], got shape {tuple(lora_a.shape)}")
     t = _t_rows(t, "t", m, dev)
+    ws_ptr, ws_bytes, ws = _scratch(workspace, tp_lora_down_prequantized_workspace_size(m, k, r), dev)
     _lib.check(_lib.load().tp_lora_down_prequantized(qa.data_ptr(), ldqa, sa.data_ptr(), lora_a.data_ptr(),
                                                      _dt(lora_a, "lora_a"), lda, m, k, r, t.data_ptr(),
-                                                     m * _T * 4, _raw_stream(dev)))
+                                                     m * _T * 4, ws_ptr, ws_bytes, _raw_stream(dev)))
     return t
 
 

@@ -841,14 +841,20 @@ tp_status check_rank(int64_t r) {
 
 }  // namespace
 
+size_t tp_lora_down_prequantized_workspace_size(int64_t m, int64_t k, int64_t r) {
+  if (m < 0 || m >= SIDE_MAX || k <= 0 || k % 256 != 0 || k > INT_MAX || r < 1 || r > 64) return 0;
+  return (size_t)(tp::side_down_workspace_floats(m, k, r) * 4);
+}
+
 tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float* sa, const void* lora_a,
                                     tp_dtype a_dtype, int64_t lda, int64_t m, int64_t k, int64_t r, float* t,
-                                    size_t t_bytes, hipStream_t stream) {
+                                    size_t t_bytes, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (!dtype_ok(a_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "a_dtype %d is not TP_F32 or TP_BF16", (int)a_dtype);
   TP_TRY(check_sizes(m, 0, k));
   TP_TRY(check_rank(r));
+  if (m >= SIDE_MAX) return fail(TP_ERR_BAD_SHAPE, "m=%lld: below 2^28", (long long)m);
   const int64_t as = dtype_size(a_dtype);
-  Extent eq, es, ea, et;
+  Extent eq, es, ea, et, ew;
   TP_TRY(check_matrix("qa", qa, m, k, ldqa, 1, &eq));
   TP_TRY(check_vector("sa", sa, m, &es));
   TP_TRY(check_matrix("lora_a", lora_a, r, k * as, lda, as, &ea));
@@ -856,10 +862,26 @@ tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float*
     return fail(TP_ERR_WORKSPACE_TOO_SMALL, "t of %zu bytes, %lld needed (m rows of 64 floats)", t_bytes,
                 (long long)(m * 64 * 4));
   TP_TRY(check_matrix("t", t, m, 64 * 4, 64, 4, &et));
-  if (overlaps(et, eq) || overlaps(et, es) || overlaps(et, ea)) return fail(TP_ERR_BAD_ALIASING, "t overlaps an input");
+  TP_TRY(check_scratch("tp_lora_down_prequantized_workspace_size", workspace, workspace_bytes,
+                       (int64_t)tp_lora_down_prequantized_workspace_size(m, k, r), &ew));
+  const Extent* ins[] = {&eq, &es, &ea};
+  for (const Extent* i : ins)
+    if (overlaps(et, *i) || overlaps(ew, *i)) return fail(TP_ERR_BAD_ALIASING, "t or the workspace overlaps an input");
+  if (overlaps(et, ew)) return fail(TP_ERR_BAD_ALIASING, "t and the workspace overlap");
   if (m == 0) return ok();
-  return hip_status(tp::launch_side_down(qa, ldqa, sa, lora_a, a_dtype == TP_BF16, lda, m, k, (int)r, t, stream),
-                    "side path launch");
+  tp::SideDownArgs a{};
+  a.qa = qa;
+  a.ldqa = ldqa;
+  a.sa = sa;
+  a.a = lora_a;
+  a.a_bf16 = a_dtype == TP_BF16;
+  a.lda = lda;
+  a.m = m;
+  a.k = k;
+  a.r = (int)r;
+  a.t = t;
+  a.ws = (float*)workspace;
+  return hip_status(tp::launch_side_down(a, stream), "side path launch");
 }
 
 size_t tp_lora_grad_workspace_size(int64_t m, int64_t n, int64_t k, int64_t r) {

@@ -69,9 +69,19 @@ hipError_t launch_colsum(const float* part, int64_t rows, int64_t cols, float* o
                          hipStream_t stream);
 
 // ------------------------------------------------------------------ side.hip
-// T = sa (qa . a^T), fp32 [m, 64] (zeros past r), a [r, k].
-hipError_t launch_side_down(const int8_t* qa, int64_t ldqa, const float* sa, const void* a, bool a_bf16, int64_t lda,
-                            int64_t m, int64_t k, int r, float* t, hipStream_t stream);
+struct SideDownArgs {  // T = sa (qa . a^T)
+  const int8_t* qa;    // [m, k]
+  int64_t ldqa;
+  const float* sa;
+  const void* a;  // [r, k]
+  int a_bf16;
+  int64_t lda, m, k;
+  int r;
+  float* t;   // [m, 64] (zeros past r)
+  float* ws;  // side_down_workspace_floats(m, k, r) floats
+};
+hipError_t launch_side_down(const SideDownArgs& a, hipStream_t stream);
+int64_t side_down_workspace_floats(int64_t m, int64_t k, int64_t r);
 
 struct SideGradArgs {
   const void* dy;  // [m, n]

@@ -18,6 +18,7 @@
 
 #include "block_ops.hpp"
 #include "device_common.hpp"
+#include "group16.hpp"
 
 namespace tp {
 
@@ -84,70 +85,145 @@ __device__ __forceinline__ void load_parts(const float* p, int valid, bf16x8_t (
   split3_bf16(v, o[0], o[1], o[2]);
 }
 
-// --------------------------------------------------------------------- down
-// A block owns 16 rows; its 16 waves share the K / 64 steps and add their
-// sums in LDS in wave order. Lane l feeds row l % 16 with the 16 codes
-// 16 (l / 16) of each step, and the same 16 columns of lora_a row l % 16.
-constexpr int SD_WAVES = 16;
+// 8 consecutive elements as loaded, and as an operand.
+template <typename T> struct RawOp;
 
-template <typename TA, int R>
-__global__ __launch_bounds__(64 * SD_WAVES) void k_side_down(const int8_t* __restrict__ qa, int64_t ldqa,
-                                                             const float* __restrict__ sa, const TA* __restrict__ a,
-                                                             int64_t lda, int64_t M, int K, int r,
-                                                             float* __restrict__ t) {
+template <> struct RawOp<uint16_t> {
+  u32x4_t w;
+  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const u32x4_t*>(p); }
+  __device__ __forceinline__ void load(const uint16_t* p, int valid) {
+    bf16x8_t o[1];
+    load_parts(p, valid, o);
+    w = __builtin_bit_cast(u32x4_t, o[0]);
+  }
+  __device__ __forceinline__ void parts(bf16x8_t (&o)[1]) const { o[0] = as_bf16(w); }
+};
+
+template <> struct RawOp<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void load(const float* p, int valid) { load_f32x8(p, valid, v); }
+  __device__ __forceinline__ void parts(bf16x8_t (&o)[3]) const { split3_bf16(v, o[0], o[1], o[2]); }
+};
+
+// --------------------------------------------------------------------- down
+// Partial sums of qa . A^T: a block owns 16 WR FM rows and a run of 256-column
+// chunks of A, which its waves share through LDS (A read by every 16 rows from
+// memory made one compute unit's loads the bound: 24 us for a single row of
+// 12288 columns at rank 32). Lane l feeds row l % 16 with the 16 codes
+// 16 (l / 16) of each 64; A's columns are stored in the order in which the two
+// products of a step take them. With few rows (WR 1) the waves share a chunk.
+constexpr int SD_KC = 256;           // columns per chunk
+constexpr int SD_PITCH = SD_KC + 8;  // bf16 per LDS row: rows 4 banks apart
+
+struct DownArgs {
+  const int8_t* qa;
+  int64_t ldqa;
+  const void* a;
+  int64_t lda, m;
+  int r, splits, chunks_per_split, chunks;
+  float* part;  // [splits * 4 / WR, m, R]
+};
+
+template <typename TA, int R, int WR, int FM>
+__global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64) ? 1 : 2) void k_side_down(DownArgs d) {
   constexpr int NF = R / 16;
   constexpr int PA = std::is_same<TA, float>::value ? 3 : 1;
-  __shared__ __align__(16) float part[SD_WAVES][16][R];
+  constexpr int WN = 4 / WR;
+  constexpr int STEPS = SD_KC / 64 / WN;       // 64-column steps of a wave and chunk
+  constexpr int PLANE = R * SD_PITCH;
+  constexpr int UNITS = R * (SD_KC / 8) / 256;  // runs of 8 columns that a thread stages
+  __shared__ __align__(16) uint16_t at[PA * PLANE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int nk = K / 64, s0 = wave * nk / SD_WAVES, s1 = (wave + 1) * nk / SD_WAVES;
-  const TA* arow[NF];
-  int aval[NF];
+  const int rg = wave % WR, ns = wave / WR;
+  const int split = (int)(blockIdx.x % (unsigned)d.splits);
+  const int64_t m0 = ((int64_t)(blockIdx.x / (unsigned)d.splits) * WR + rg) * (16 * FM);
+  const int c0 = split * d.chunks_per_split, c1 = min(c0 + d.chunks_per_split, d.chunks);
+  // Rows past the last one and ranks past r read the last row or rank instead:
+  // what comes of them is not written.
+  const int8_t* xrow[FM];
 #pragma unroll
-  for (int f = 0; f < NF; ++f) {
-    const int j = f * 16 + l16;
-    aval[f] = j < r ? 8 : 0;
-    arow[f] = a + (int64_t)min(j, r - 1) * lda + 16 * g4;
+  for (int i = 0; i < FM; ++i)
+    xrow[i] = d.qa + min(m0 + 16 * i + l16, d.m - 1) * d.ldqa + ns * (64 * STEPS) + 16 * g4;
+  const int ar = threadIdx.x >> 5, ak = threadIdx.x & 31;  // rank (of 8 at a time) and run of 8 columns staged
+  u32x4_t x[FM][STEPS];
+  RawOp<TA> av[UNITS];
+  auto load_x = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+        x[i][s] = *reinterpret_cast<const u32x4_t*>(xrow[i] + (int64_t)c * SD_KC + 64 * s);
+  };
+  auto load_a = [&](int c) {
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+      av[u].load((const TA*)d.a + (int64_t)min(ar + 8 * u, d.r - 1) * d.lda + (int64_t)c * SD_KC + 8 * ak);
+  };
+  f32x4_t acc[FM][NF];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) acc[i][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (c0 < c1) {
+    load_a(c0);
+    load_x(c0);
   }
-  for (int64_t m0 = (int64_t)blockIdx.x * 16; m0 < M; m0 += (int64_t)gridDim.x * 16) {
-    const bool rowok = m0 + l16 < M;
-    const int8_t* xrow = qa + min(m0 + l16, M - 1) * ldqa + 16 * g4;
-    f32x4_t acc[NF];
+  // columns 64 s + 16 g + 8 h of a chunk sit at 64 s + 32 h + 8 g
+  const int pos = (ak >> 3) * 64 + (ak & 1) * 32 + ((ak >> 1) & 3) * 8;
+  for (int c = c0; c < c1; ++c) {
+    __syncthreads();
 #pragma unroll
-    for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int s = s0; s < s1; ++s) {
-      u32x4_t w = {0u, 0u, 0u, 0u};
-      if (rowok) w = *reinterpret_cast<const u32x4_t*>(xrow + 64 * s);
-      const bf16x8_t x0[1] = {widen8(w.x, w.y)}, x1[1] = {widen8(w.z, w.w)};
+    for (int u = 0; u < UNITS; ++u) {
+      bf16x8_t o[PA];
+      av[u].parts(o);
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        bf16x8_t a0[PA], a1[PA];
-        load_parts(arow[f] + 64 * s, aval[f], a0);
-        load_parts(arow[f] + 64 * s + 8, aval[f], a1);
-        acc[f] = mfma_parts(x0, a0, acc[f]);
-        acc[f] = mfma_parts(x1, a1, acc[f]);
+      for (int p = 0; p < PA; ++p)
+        *reinterpret_cast<bf16x8_t*>(at + p * PLANE + (ar + 8 * u) * SD_PITCH + pos) = o[p];
+    }
+    __syncthreads();
+    u32x4_t now[FM][STEPS];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) now[i][s] = x[i][s];
+    if (c + 1 < c1) {
+      load_a(c + 1);
+      load_x(c + 1);
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bf16x8_t xp[FM][1];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          xp[i][0] = h ? widen8(now[i][s].z, now[i][s].w) : widen8(now[i][s].x, now[i][s].y);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          bf16x8_t ap[PA];
+#pragma unroll
+          for (int p = 0; p < PA; ++p)
+            ap[p] = *reinterpret_cast<const bf16x8_t*>(at + p * PLANE + (16 * f + l16) * SD_PITCH +
+                                                       64 * (ns * STEPS + s) + 32 * h + 8 * g4);
+#pragma unroll
+          for (int i = 0; i < FM; ++i) acc[i][f] = mfma_parts(xp[i], ap, acc[i][f]);
+        }
+      }
+  }
+  // lane l holds rows 4 (l / 16) + v, column 16 f + l % 16
+  float* out = d.part + (int64_t)(split * WN + ns) * d.m * R;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t row = m0 + 16 * i + 4 * g4 + v;
+      if (row < d.m) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) out[row * R + 16 * f + l16] = acc[i][f][v];
       }
     }
-    // lane l holds rows 4 (l / 16) + v, column 16 f + l % 16
-#pragma unroll
-    for (int f = 0; f < NF; ++f)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) part[wave][4 * g4 + v][f * 16 + l16] = acc[f][v];
-    __syncthreads();
-    for (int e = threadIdx.x; e < 16 * SIDE_T; e += 64 * SD_WAVES) {
-      const int i = e / SIDE_T, j = e % SIDE_T;
-      if (m0 + i >= M) continue;
-      float sum = 0.f;
-      if (j < R && j < r) {
-        sum = part[0][i][j];
-#pragma unroll
-        for (int w = 1; w < SD_WAVES; ++w) sum += part[w][i][j];
-        sum *= sa[m0 + i];
-      }
-      t[(m0 + i) * SIDE_T + j] = sum;
-    }
-    __syncthreads();
-  }
 }
 
 // ----------------------------------------------------------------------- dt
@@ -163,122 +239,14 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t first, uint32_t second, int
   return __builtin_amdgcn_perm(second, first, odd ? 0x07060302u : 0x05040100u);
 }
 
-// An 8 x 8 block of B (rows n, columns j) into the planes bt[part][j][n].
-__device__ __forceinline__ void stage_b8(const uint16_t* b, int64_t ldb, int rows, int cols, uint16_t* bt, int,
-                                         int pitch) {
-  u32x4_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bf16x8_t o[1];
-    load_parts(b + (int64_t)min(i, max(rows - 1, 0)) * ldb, i < rows ? cols : 0, o);
-    w[i] = __builtin_bit_cast(u32x4_t, o[0]);
-  }
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    u32x4_t o;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) o[p] = pair_of(w[2 * p][c >> 1], w[2 * p + 1][c >> 1], c & 1);
-    *reinterpret_cast<u32x4_t*>(bt + c * pitch) = o;
-  }
-}
-
-__device__ __forceinline__ void stage_b8(const float* b, int64_t ldb, int rows, int cols, uint16_t* bt, int plane,
-                                         int pitch) {
-  float w[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    load_f32x8(b + (int64_t)min(i, max(rows - 1, 0)) * ldb, i < rows ? cols : 0, w[i]);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = w[i][c];
-    bf16x8_t h, m, l;
-    split3_bf16(v, h, m, l);
-    *reinterpret_cast<bf16x8_t*>(bt + c * pitch) = h;
-    *reinterpret_cast<bf16x8_t*>(bt + plane + c * pitch) = m;
-    *reinterpret_cast<bf16x8_t*>(bt + 2 * plane + c * pitch) = l;
-  }
-}
-
-template <typename SRC, typename TB, int R, int WR>
-__global__ __launch_bounds__(256) void k_side_dt(const typename SRC::elem* __restrict__ dy, int64_t lddy,
-                                                 const TB* __restrict__ b, int64_t ldb, int64_t M, int64_t N, int r,
-                                                 int splits, int chunks_per_split, float* __restrict__ part) {
-  constexpr int NF = R / 16;
-  constexpr int PY = SRC::PARTS, PB = std::is_same<TB, float>::value ? 3 : 1;
-  constexpr int WN = 4 / WR;                // waves that share a chunk
-  constexpr int STEPS = DT_NC / 32 / WN;    // 32-column steps of a wave and chunk
-  constexpr int PLANE = R * DT_PITCH;
-  __shared__ __align__(16) uint16_t bt[PB * PLANE];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int l16 = lane & 15, g4 = lane >> 4;
-  const int rg = wave % WR, ns = wave / WR;
-  const int split = (int)(blockIdx.x % (unsigned)splits);
-  const int64_t m0 = (int64_t)(blockIdx.x / (unsigned)splits) * (16 * WR) + 16 * rg;
-  const bool rowok = m0 + l16 < M;
-  const typename SRC::elem* row = dy + min(m0 + l16, M - 1) * lddy;
-  const int64_t nchunks = (N + DT_NC - 1) / DT_NC;
-  const int64_t c0 = (int64_t)split * chunks_per_split, c1 = min(c0 + chunks_per_split, nchunks);
-  f32x4_t acc[NF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int64_t c = c0; c < c1; ++c) {
-    const int64_t n0 = c * DT_NC;
-    __syncthreads();
-    for (int u = threadIdx.x; u < (DT_NC / 8) * (R / 8); u += 256) {
-      const int nb = u / (R / 8), jb = u % (R / 8);
-      const int64_t n = n0 + 8 * nb;
-      const int rows = (int)max((int64_t)0, min((int64_t)8, N - n)), cols = max(0, min(8, r - 8 * jb));
-      stage_b8(b + min(n, N - 1) * ldb + (cols > 0 ? 8 * jb : 0), ldb, rows, cols,
-               bt + 8 * jb * DT_PITCH + 8 * nb, PLANE, DT_PITCH);
-    }
-    __syncthreads();
-    const int64_t nw = n0 + ns * (32 * STEPS);
-    bf16x8_t y[STEPS][PY];
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int64_t n = nw + 32 * s + 8 * g4;
-      const int valid = rowok ? (int)max((int64_t)0, min((int64_t)8, N - n)) : 0;
-      load_parts(row + (valid > 0 ? n : 0), valid, y[s]);
-    }
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        bf16x8_t bp[PB];
-#pragma unroll
-        for (int p = 0; p < PB; ++p)
-          bp[p] = *reinterpret_cast<const bf16x8_t*>(bt + p * PLANE + (16 * f + l16) * DT_PITCH + ns * (32 * STEPS) +
-                                                     32 * s + 8 * g4);
-        acc[f] = mfma_parts(y[s], bp, acc[f]);
-      }
-  }
-  float* out = part + ((int64_t)(split * WN + ns) * M + m0) * R;
-#pragma unroll
-  for (int v = 0; v < 4; ++v)
-    if (m0 + 4 * g4 + v < M) {
-#pragma unroll
-      for (int f = 0; f < NF; ++f) out[(int64_t)(4 * g4 + v) * R + 16 * f + l16] = acc[f][v];
-    }
-}
-
-// -------------------------------------------------------------------- outer
-// Partial sums over rows of small^T . big: small [rows, r] fp32 (T, or dT sa)
-// split into three bf16 planes in LDS, big [rows, width] streamed from memory.
-// The sum runs over the rows, so a lane loads an 8 x 8 block (8 rows, 8
-// columns) and pairs up rows with byte permutes: its column c is then an
-// operand of 8 consecutive rows, and 16 lanes cover 128 columns, every eighth
-// at a time. A block's four waves own 128 columns each and a run of 64-row
-// chunks.
-constexpr int OU_MC = 64;            // rows per chunk
-constexpr int OU_PITCH = OU_MC + 8;  // bf16 per LDS row
-constexpr int OU_COLS = 512;         // columns of a block
-
-template <typename SRC> struct Block8;  // 8 x 8 elements of a lane, and column c as an operand
+// 8 x 8 elements of a lane (row i, column c), and column c as an operand of
+// the 8 rows: 16-bit halves are paired by byte permutes, fp32 columns split.
+template <typename SRC> struct Block8;
 
 template <> struct Block8<SrcBf16> {
   u32x4_t w[8];
+  __device__ __forceinline__ void zero(int i) { w[i] = u32x4_t{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(int i, const uint16_t* p) { w[i] = *reinterpret_cast<const u32x4_t*>(p); }
   __device__ __forceinline__ void load(int i, const uint16_t* p, int valid) {
     bf16x8_t o[1];
     load_parts(p, valid, o);
@@ -294,6 +262,11 @@ template <> struct Block8<SrcBf16> {
 
 template <> struct Block8<SrcF32> {
   float w[8][8];
+  __device__ __forceinline__ void zero(int i) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) w[i][c] = 0.f;
+  }
+  __device__ __forceinline__ void load(int i, const float* p) { load8(p, w[i]); }
   __device__ __forceinline__ void load(int i, const float* p, int valid) { load_f32x8(p, valid, w[i]); }
   __device__ __forceinline__ void column(int c, bf16x8_t (&o)[3]) const {
     float v[8];
@@ -305,8 +278,13 @@ template <> struct Block8<SrcF32> {
 
 template <> struct Block8<SrcI8> {
   uint2 w[8];
-  __device__ __forceinline__ void load(int i, const int8_t* p, int valid) {  // whole 8s: k is a multiple of 256
-    w[i] = valid > 0 ? *reinterpret_cast<const uint2*>(p) : uint2{0u, 0u};
+  __device__ __forceinline__ void zero(int i) { w[i] = uint2{0u, 0u}; }
+  __device__ __forceinline__ void load(int i, const int8_t* p) { w[i] = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void load(int i, const int8_t* p, int valid) {  // k is a multiple of 256: all 8 or none
+    if (valid > 0)
+      load(i, p);
+    else
+      zero(i);
   }
   __device__ __forceinline__ void column(int c, bf16x8_t (&o)[1]) const {
     u32x4_t v;
@@ -319,161 +297,371 @@ template <> struct Block8<SrcI8> {
   }
 };
 
-struct OuterArgs {
-  const void* big;
-  int64_t ldbig, width;   // [m, width]
-  const float* small;     // T [m, 64] (dB), or the dt partial sums [np, m, R] (dA)
-  int np;                 // partial sums to join; 0 with T
-  float alpha;            // dA: factor of the joined sums
-  const float* sa;        // dA: row scales
-  float* dt;              // dA: dT [m, 64] to write
-  int64_t m;
+struct DtArgs {
+  const void* dy;
+  int64_t lddy;
+  const void* b;
+  int64_t ldb, m, n;
   int r, splits, chunks_per_split;
-  int64_t nmc;            // 64-row chunks
-  float* part;            // dB: [splits, width, R]; dA: [splits, R, width]
+  float* part;  // [splits * 4 / WR, m, R]
 };
 
-template <typename SRC, int R, bool DA>
-__global__ __launch_bounds__(256) void k_side_outer(OuterArgs a) {
-  constexpr int NF = R / 16, PS = SRC::PARTS;
-  constexpr int PLANE = R * OU_PITCH;
-  __shared__ __align__(16) uint16_t st[3 * PLANE];
+// The next chunk's dY and B are in flight while a chunk is multiplied (only B
+// where dY is fp32: its registers do not allow more).
+template <typename SRC, typename TB, int R, int WR>
+__device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t* bt) {
+  typedef typename SRC::elem TY;
+  typedef typename std::conditional<std::is_same<TB, float>::value, SrcF32, SrcBf16>::type BSRC;
+  constexpr int NF = R / 16;
+  constexpr int PY = SRC::PARTS, PB = BSRC::PARTS;
+  constexpr int WN = 4 / WR;                // waves that share a chunk
+  constexpr int STEPS = DT_NC / 32 / WN;    // 32-column steps of a wave and chunk
+  constexpr int PLANE = R * DT_PITCH;
+  constexpr bool AHEAD = PY == 1;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int split = (int)(blockIdx.x % (unsigned)a.splits);
-  const int64_t cblk = blockIdx.x / (unsigned)a.splits;
-  const int64_t col = cblk * OU_COLS + wave * 128 + 8 * l16;
-  const int valid_cols = (int)max((int64_t)0, min((int64_t)8, a.width - col));
-  const typename SRC::elem* big = (const typename SRC::elem*)a.big + (valid_cols > 0 ? col : 0);
+  const int rg = wave % WR, ns = wave / WR;
+  const int split = (int)(blk % (unsigned)a.splits);
+  const int64_t m0 = (int64_t)(blk / (unsigned)a.splits) * (16 * WR) + 16 * rg;
+  // rows past the last one read that one: what comes of them is not written
+  const TY* row = (const TY*)a.dy + min(m0 + l16, a.m - 1) * a.lddy + ns * (32 * STEPS) + 8 * g4;
+  const int64_t nchunks = (a.n + DT_NC - 1) / DT_NC;
+  const int64_t c0 = (int64_t)split * a.chunks_per_split, c1 = min(c0 + a.chunks_per_split, nchunks);
+  // this thread's 8 x 8 block of a chunk of B
+  const int nb = threadIdx.x / (R / 8), jb = threadIdx.x % (R / 8);
+  const bool stages = nb < DT_NC / 8;
+  const int cols = max(0, min(8, a.r - 8 * jb));
+  const TB* bcol = (const TB*)a.b + (cols > 0 ? 8 * jb : 0);
+
+  RawOp<TY> y[STEPS];
+  Block8<BSRC> bb;
+  auto load_y = [&](int64_t c) {
+    const int64_t n0 = c * DT_NC;
+    if (n0 + DT_NC <= a.n) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) y[s].load(row + n0 + 32 * s);
+    } else {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const int64_t left = a.n - (n0 + ns * (32 * STEPS) + 32 * s + 8 * g4);
+        y[s].load(left > 0 ? row + n0 + 32 * s : row, (int)max((int64_t)0, min((int64_t)8, left)));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  auto load_b = [&](int64_t c) {
+    if (!stages) return;
+    const int64_t n = c * DT_NC + 8 * nb;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (n + i < a.n)
+        bb.load(i, bcol + (n + i) * a.ldb, cols);
+      else
+        bb.zero(i);
+    }
+  };
+  f32x4_t acc[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (c0 < c1) {
+    load_b(c0);
+    if (AHEAD) load_y(c0);
+  }
+  for (int64_t c = c0; c < c1; ++c) {
+    if (!AHEAD) load_y(c);
+    __syncthreads();
+    if (stages) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        bf16x8_t o[PB];
+        bb.column(e, o);
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+          *reinterpret_cast<bf16x8_t*>(bt + p * PLANE + (8 * jb + e) * DT_PITCH + 8 * nb) = o[p];
+      }
+    }
+    __syncthreads();
+    RawOp<TY> now[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) now[s] = y[s];
+    if (c + 1 < c1) {
+      load_b(c + 1);
+      if (AHEAD) load_y(c + 1);
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      bf16x8_t yp[PY];
+      now[s].parts(yp);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        bf16x8_t bp[PB];
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+          bp[p] = *reinterpret_cast<const bf16x8_t*>(bt + p * PLANE + (16 * f + l16) * DT_PITCH + ns * (32 * STEPS) +
+                                                     32 * s + 8 * g4);
+        acc[f] = mfma_parts(yp, bp, acc[f]);
+      }
+    }
+  }
+  float* out = a.part + ((int64_t)(split * WN + ns) * a.m + m0) * R;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (m0 + 4 * g4 + v < a.m) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) out[(int64_t)(4 * g4 + v) * R + 16 * f + l16] = acc[f][v];
+    }
+}
+
+// -------------------------------------------------------------------- outer
+// Partial sums over rows of small^T . big: small [rows, r] fp32 (T, or dT sa)
+// split into three bf16 parts, big [rows, width] streamed from memory. The sum
+// runs over the rows, so a lane loads an 8 x 8 block (8 rows, 8 columns): its
+// column c is an operand of 8 consecutive rows, and 16 lanes cover 128 columns,
+// every eighth at a time. A block owns 128 columns, up to 32 ranks and a run of
+// 32-row chunks, which its four waves take in turn, each with LDS of its own
+// for the small operand; their sums are added in LDS in wave order. The next
+// chunk is in flight while one is multiplied.
+constexpr int OU_MC = 32;            // rows per chunk
+constexpr int OU_PITCH = OU_MC + 8;  // bf16 per LDS row: 16 rows cover the 64 banks
+constexpr int OU_COLS = 128;         // columns of a block
+constexpr int OU_RB = 32;            // ranks of a block, at most
+
+struct OuterArgs {
+  const void* big;
+  int64_t ldbig, width;  // [m, width]
+  const float* small;    // T, or dT sa: [m, 64]
+  int64_t m;
+  int r, splits, chunks_per_split;
+  int64_t nmc;           // 32-row chunks
+  float* part;           // [splits, width, R]; of codes: [splits, R, width]
+};
+
+template <int R> struct OuterShape {
+  static constexpr int RB = R < OU_RB ? R : OU_RB;  // ranks of a block
+  static constexpr int HALVES = R / RB;
+  static constexpr int LDS = 4 * 3 * RB * OU_PITCH;  // 16-bit words
+};
+
+template <typename SRC, int R, bool BY_RANK>
+__device__ __forceinline__ void outer_block(const OuterArgs& a, unsigned blk, uint16_t* lds) {
+  typedef typename SRC::elem TY;
+  constexpr int RB = OuterShape<R>::RB, HALVES = OuterShape<R>::HALVES;
+  constexpr int NF = RB / 16, PS = SRC::PARTS;
+  constexpr int PLANE = RB * OU_PITCH;
+  constexpr bool AHEAD = PS == 1;  // fp32 columns leave no registers for a second block
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, g4 = lane >> 4;
+  uint16_t* st = lds + wave * 3 * PLANE;
+  const int j0 = (int)(blk % HALVES) * RB;
+  const int split = (int)(blk / HALVES % (unsigned)a.splits);
+  const int64_t col0 = (int64_t)(blk / HALVES / (unsigned)a.splits) * OU_COLS, col = col0 + 8 * l16;
+  const int valid = (int)max((int64_t)0, min((int64_t)8, a.width - col));
+  const bool inside = col0 + OU_COLS <= a.width;
+  const TY* big = (const TY*)a.big + (valid > 0 ? col : 0);
   const int64_t c0 = (int64_t)split * a.chunks_per_split, c1 = min(c0 + a.chunks_per_split, a.nmc);
   f32x4_t acc[8][NF];
 #pragma unroll
   for (int c = 0; c < 8; ++c)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[c][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int64_t ch = c0; ch < c1; ++ch) {
-    const int64_t mb = ch * OU_MC;
-    __syncthreads();
-    for (int u = threadIdx.x; u < R * (OU_MC / 8); u += 256) {
-      const int j = u % R, oct = u / R;
-      float v[8];
+
+  float sv[NF][8];
+  auto load_small = [&](int64_t ch) {
+#pragma unroll
+    for (int q = 0; q < NF; ++q) {
+      const int u = lane + 64 * q, j = u % RB, oct = u / RB;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)  // in range always; zeroed where it does not count when it is staged
+        sv[q][i] = a.small[min(ch * OU_MC + 8 * oct + i, a.m - 1) * SIDE_T + j0 + j];
+    }
+  };
+  auto load_big = [&](int64_t ch, Block8<SRC>& b) {
+    const int64_t r0 = ch * OU_MC;
+    if (inside && r0 + OU_MC <= a.m) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b.load(i, big + (r0 + 8 * g4 + i) * a.ldbig);
+    } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int64_t row = mb + 8 * oct + i;
-        v[i] = 0.f;
-        if (row < a.m) {
-          if constexpr (DA) {
-            float s = 0.f;
-            for (int p = 0; p < a.np; ++p) s += a.small[((int64_t)p * a.m + row) * R + j];
-            s *= a.alpha;
-            if (j >= a.r) s = 0.f;
-            if (cblk == 0) a.dt[row * SIDE_T + j] = s;
-            v[i] = s * a.sa[row];
-          } else {
-            if (j < a.r) v[i] = a.small[row * SIDE_T + j];
-          }
-        }
+        const int64_t row = r0 + 8 * g4 + i;
+        if (row < a.m)
+          b.load(i, big + row * a.ldbig, valid);
+        else
+          b.zero(i);
+        __builtin_amdgcn_sched_barrier(0);  // one row's elements at a time: the edges need no more registers
       }
+    }
+  };
+  Block8<SRC> next;
+  int64_t ch = c0 + wave;
+  if (ch < c1) {
+    load_small(ch);
+    if (AHEAD) load_big(ch, next);
+  }
+  for (; ch < c1; ch += 4) {
+    if (!AHEAD) load_big(ch, next);
+    wave_lds_sync();
+#pragma unroll
+    for (int q = 0; q < NF; ++q) {
+      const int u = lane + 64 * q, j = u % RB, oct = u / RB;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sv[q][i] = ch * OU_MC + 8 * oct + i < a.m && j0 + j < a.r ? sv[q][i] : 0.f;
       bf16x8_t h, md, l;
-      split3_bf16(v, h, md, l);
+      split3_bf16(sv[q], h, md, l);
       uint16_t* to = st + j * OU_PITCH + 8 * oct;
       *reinterpret_cast<bf16x8_t*>(to) = h;
       *reinterpret_cast<bf16x8_t*>(to + PLANE) = md;
       *reinterpret_cast<bf16x8_t*>(to + 2 * PLANE) = l;
     }
-    if (DA && R < SIDE_T && cblk == 0) {  // dT is zero past the columns computed here
-      constexpr int REST = SIDE_T - R;
-      for (int u = threadIdx.x; u < OU_MC * REST; u += 256) {
-        const int64_t row = mb + u / REST;
-        if (row < a.m) a.dt[row * SIDE_T + R + u % REST] = 0.f;
-      }
+    wave_lds_sync();
+    const Block8<SRC> now = next;
+    if (ch + 4 < c1) {
+      load_small(ch + 4);
+      if (AHEAD) load_big(ch + 4, next);
     }
-    __syncthreads();
+    bf16x8_t sm[NF][3];
 #pragma unroll
-    for (int sub = 0; sub < OU_MC / 32; ++sub) {
-      Block8<SRC> blk;
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t row = mb + 32 * sub + 8 * g4 + i;
-        blk.load(i, big + min(row, a.m - 1) * a.ldbig, row < a.m ? valid_cols : 0);
-      }
-      bf16x8_t sm[NF][3];
+      for (int p = 0; p < 3; ++p)
+        sm[f][p] = *reinterpret_cast<const bf16x8_t*>(st + p * PLANE + (16 * f + l16) * OU_PITCH + 8 * g4);
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
+    for (int c = 0; c < 8; ++c) {
+      bf16x8_t bc[PS];
+      now.column(c, bc);
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-          sm[f][p] = *reinterpret_cast<const bf16x8_t*>(st + p * PLANE + (16 * f + l16) * OU_PITCH + 32 * sub + 8 * g4);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        bf16x8_t big_c[PS];
-        blk.column(c, big_c);
-#pragma unroll
-        for (int f = 0; f < NF; ++f) acc[c][f] = mfma_parts(sm[f], big_c, acc[c][f]);
-      }
+      for (int f = 0; f < NF; ++f) acc[c][f] = mfma_parts(sm[f], bc, acc[c][f]);
+      if (c & 1) __builtin_amdgcn_sched_barrier(0);  // two columns' operands at a time
     }
   }
-  // lane l holds, for column col + c, the ranks 16 f + 4 (l / 16) + v
-  if constexpr (DA) {
-    if (valid_cols > 0) {
+  // lane l holds, for column col + c, the ranks j0 + 16 f + 4 (l / 16) + v. Two
+  // columns' sums at a time (c and c + 4) go through LDS, where a thread adds
+  // the waves' sums of one: four columns in a row after the four rounds.
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);  // [wave][column][f][lane]
+  static_assert(4 * 2 * NF * 64 * 16 <= OuterShape<R>::LDS * 2, "the sums fit in the staging area");
+  const int half = (int)threadIdx.x / (64 * NF), f = (int)threadIdx.x / 64 % NF;
+  f32x4_t sum[4];
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
+  for (int c = 0; c < 4; ++c) {
+    __syncthreads();
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          float o[8];
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < 8; ++c) o[c] = acc[c][f][v];
-          store8(a.part + ((int64_t)split * R + 16 * f + 4 * g4 + v) * a.width + col, o);
-        }
+      for (int g = 0; g < NF; ++g) red[((wave * 2 + h) * NF + g) * 64 + lane] = acc[c + 4 * h][g];
+    __syncthreads();
+    if (half < 2) {
+      sum[c] = red[(half * NF + f) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) sum[c] += red[((w * 2 + half) * NF + f) * 64 + lane];
     }
-  } else {
+  }
+  if (half >= 2) return;
+  const int j = j0 + 16 * f + 4 * g4;
+  if constexpr (BY_RANK) {  // [splits, R, width]; the width is a multiple of 256
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (c < valid_cols) {
+    for (int v = 0; v < 4; ++v)
+      *reinterpret_cast<f32x4_t*>(a.part + ((int64_t)split * R + j + v) * a.width + col + 4 * half) =
+          f32x4_t{sum[0][v], sum[1][v], sum[2][v], sum[3][v]};
+  } else {  // [splits, width, R]
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
-          *reinterpret_cast<f32x4_t*>(a.part + ((int64_t)split * a.width + col + c) * R + 16 * f + 4 * g4) = acc[c][f];
-      }
+    for (int c = 0; c < 4; ++c)
+      if (4 * half + c < valid)
+        *reinterpret_cast<f32x4_t*>(a.part + ((int64_t)split * a.width + col + 4 * half + c) * R + j) = sum[c];
   }
 }
 
+template <typename SRC, typename TB, int R, int WR>
+__global__ __launch_bounds__(256) void k_side_dt(DtArgs t) {
+  constexpr int PB = std::is_same<TB, float>::value ? 3 : 1;
+  __shared__ __align__(16) uint16_t lds[PB * R * DT_PITCH];
+  dt_block<SRC, TB, R, WR>(t, blockIdx.x, lds);
+}
+
+template <typename SRC, int R>
+__global__ __launch_bounds__(256) void k_side_outer(OuterArgs o) {
+  __shared__ __align__(16) uint16_t lds[OuterShape<R>::LDS];
+  outer_block<SRC, R, std::is_same<SRC, SrcI8>::value>(o, blockIdx.x, lds);
+}
+
 // --------------------------------------------------------------------- join
-// The splits of dB and dA added in order. The first nb_db blocks take dB, four
-// ranks a thread; the others dA, a 256-group of one rank per half wave, which
-// rotates it back on request.
+// The splits of T or dT (the first nb_t blocks) and of dB added in order, four
+// ranks a thread, times alpha. T's and dT's rows are 64 long, zeros past the
+// rank; `scaled` gets them times the rows' factors, t without (either may be
+// null).
 template <int R>
-__global__ __launch_bounds__(256) void k_side_join(const float* __restrict__ pb, int sb, int64_t N, float alpha,
-                                                   float* __restrict__ db, int64_t lddb,
-                                                   const float* __restrict__ pa, int sa_splits, int K,
-                                                   float* __restrict__ da, int64_t ldda, int rotate, int r,
-                                                   int64_t nb_db) {
-  if ((int64_t)blockIdx.x < nb_db) {
-    constexpr int Q = R / 4;
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t n = e / Q;
-    const int j = (int)(e % Q) * 4;
-    if (n >= N || j >= r) return;
-    f32x4_t s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = 0; p < sb; ++p) s += *reinterpret_cast<const f32x4_t*>(pb + ((int64_t)p * N + n) * R + j);
-    float* to = db + n * lddb + j;
+__global__ __launch_bounds__(256) void k_side_join(const float* __restrict__ pt, int st, int64_t M,
+                                                   const float* __restrict__ rowscale, float* __restrict__ t,
+                                                   float* __restrict__ scaled,
+                                                   const float* __restrict__ pb, int sb, int64_t N,
+                                                   float* __restrict__ db, int64_t lddb, float alpha, int r,
+                                                   unsigned nb_t) {
+  const bool is_t = blockIdx.x < nb_t;
+  const int64_t e = (int64_t)(is_t ? blockIdx.x : blockIdx.x - nb_t) * 256 + threadIdx.x;
+  const int64_t row = e / (is_t ? SIDE_T / 4 : R / 4), rows = is_t ? M : N;
+  const int j = (int)(e % (is_t ? SIDE_T / 4 : R / 4)) * 4;
+  if (row >= rows) return;
+  const float* p = is_t ? pt : pb;
+  const int splits = is_t ? st : sb;
+  f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+  if (j < r) {
+    for (int q0 = 0; q0 < splits; q0 += 8) {  // eight loads in flight, the last ones clamped
+      f32x4_t w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        w[q] = *reinterpret_cast<const f32x4_t*>(p + ((int64_t)min(q0 + q, splits - 1) * rows + row) * R + j);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q0 + q < splits) s += w[q];
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) s[v] = j + v < r ? s[v] * alpha : 0.f;
+  }
+  if (is_t) {
+    if (t != nullptr) *reinterpret_cast<f32x4_t*>(t + row * SIDE_T + j) = s;
+    *reinterpret_cast<f32x4_t*>(scaled + row * SIDE_T + j) = s * rowscale[row];
+  } else {
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-      if (j + v < r) to[v] = s[v] * alpha;
-    return;
+      if (j + v < r) db[row * lddb + j + v] = s[v];
   }
-  const int lane32 = threadIdx.x & 31;
-  const int groups = K / 256;
-  const int64_t unit = ((int64_t)blockIdx.x - nb_db) * 8 + (threadIdx.x >> 5);
-  if (unit >= (int64_t)r * groups) return;  // uniform over the half wave that owns the unit
-  const int64_t j = unit / groups;
-  const int64_t c = (unit % groups) * 256 + lane32 * 8;
+}
+
+// The splits of dA [splits, R, K] added: a half wave takes every fourth split of
+// a 256-group of one rank, eight of these units a block; the four sums are
+// joined in LDS, and the first half wave of a unit rotates the group back on
+// request.
+template <int R>
+__global__ __launch_bounds__(1024) void k_side_join_da(const float* __restrict__ pa, int splits, int K,
+                                                       float* __restrict__ da, int64_t ldda, int rotate, int r) {
+  __shared__ __align__(16) float sums[4][8][256];
+  const int lane32 = threadIdx.x & 31, i = (threadIdx.x >> 5) & 7, part = threadIdx.x >> 8;
+  const int groups = K / 256, units = r * groups;
+  const int unit = (int)blockIdx.x * 8 + i;
+  const int j = unit / groups, c = (unit - j * groups) * 256 + lane32 * 8;
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < sa_splits; ++p) {
+  if (unit < units) {
+    for (int q0 = part; q0 < splits; q0 += 16) {  // four splits in flight, the last ones clamped
+      float w[4][8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) load8(pa + ((int64_t)min(q0 + 4 * q, splits - 1) * R + j) * K + c, w[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q0 + 4 * q < splits) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += w[q][e];
+        }
+    }
+  }
+  store8(&sums[part][i][8 * lane32], v);
+  __syncthreads();
+  if (part != 0 || unit >= units) return;  // uniform over the half wave that owns the unit
+#pragma unroll
+  for (int q = 1; q < 4; ++q) {
     float w[8];
-    load8(pa + ((int64_t)p * R + j) * K + c, w);
+    load8(&sums[q][i][8 * lane32], w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += w[e];
   }
@@ -482,7 +670,7 @@ __global__ __launch_bounds__(256) void k_side_join(const float* __restrict__ pb,
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= 0.0625f;
   }
-  store8(da + j * ldda + c, v);
+  store8(da + (int64_t)j * ldda + c, v);
 }
 
 // ---------------------------------------------------------------- launchers
@@ -491,14 +679,16 @@ namespace {
 // How the sums are split: enough blocks for the chip, as few partial sums as
 // that allows.
 struct SidePlan {
-  int R, wr;                     // padded rank; row groups of a dt block
+  int wr, wn;                    // row groups of a dt block, partial sums per split
   int64_t rb, nchunks;           // row blocks, 256-column chunks (dt)
-  int s1, cps1, wn;              // splits of the columns, chunks of a split, partial sums per split
-  int64_t nmc;                   // 64-row chunks (outer)
+  int s1, cps1;                  // splits of the columns, chunks of a split
+  int64_t nmc;                   // 32-row chunks (outer)
   int64_t cb2, cb3;              // column blocks of dB and dA
   int s2, cps2, s3, cps3;
-  int64_t off2, off3, total;     // floats: the dB and dA partial sums, and all
+  int64_t off2, off3, off4, total;  // floats: the dB and dA partial sums, dT sa, and all
 };
+
+int padded_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
 
 void split_of(int64_t chunks, int64_t want, int* splits, int* per) {
   if (chunks == 0) {
@@ -506,7 +696,7 @@ void split_of(int64_t chunks, int64_t want, int* splits, int* per) {
     *per = 0;
     return;
   }
-  int64_t s = want < 1 ? 1 : (want > chunks ? chunks : want);
+  const int64_t s = want < 1 ? 1 : (want > chunks ? chunks : want);
   const int64_t p = (chunks + s - 1) / s;
   *per = (int)p;
   *splits = (int)((chunks + p - 1) / p);
@@ -514,32 +704,58 @@ void split_of(int64_t chunks, int64_t want, int* splits, int* per) {
 
 SidePlan side_plan(int64_t m, int64_t n, int64_t k, int64_t r) {
   SidePlan p;
-  p.R = r <= 16 ? 16 : r <= 32 ? 32 : 64;
+  const int R = padded_rank(r);
   p.wr = m > 16 ? 4 : 1;
   p.wn = 4 / p.wr;
   p.rb = (m + 16 * p.wr - 1) / (16 * p.wr);
   p.nchunks = (n + DT_NC - 1) / DT_NC;
-  split_of(m > 0 ? p.nchunks : 0, p.rb > 0 ? 512 / p.rb : 0, &p.s1, &p.cps1);
+  split_of(m > 0 ? p.nchunks : 0, p.rb > 0 ? 768 / p.rb : 0, &p.s1, &p.cps1);
   p.nmc = (m + OU_MC - 1) / OU_MC;
   p.cb2 = (n + OU_COLS - 1) / OU_COLS;
   p.cb3 = (k + OU_COLS - 1) / OU_COLS;
-  split_of(n > 0 ? p.nmc : 0, p.cb2 > 0 ? 256 / p.cb2 : 0, &p.s2, &p.cps2);
-  split_of(p.nmc, 256 / p.cb3 < 16 ? 256 / p.cb3 : 16, &p.s3, &p.cps3);
-  p.off2 = (int64_t)p.s1 * p.wn * m * p.R;
-  p.off3 = p.off2 + (int64_t)p.s2 * n * p.R;
-  p.total = p.off3 + (int64_t)p.s3 * k * p.R;
+  // (a split is at least a chunk for each of the four waves)
+  split_of(n > 0 ? (p.nmc + 3) / 4 : 0, p.cb2 > 0 ? 512 / p.cb2 : 0, &p.s2, &p.cps2);
+  split_of((p.nmc + 3) / 4, 512 / p.cb3, &p.s3, &p.cps3);
+  p.cps2 *= 4;
+  p.cps3 *= 4;
+  p.off2 = (int64_t)p.s1 * p.wn * m * R;
+  p.off3 = p.off2 + (int64_t)p.s2 * n * R;
+  p.off4 = p.off3 + (int64_t)p.s3 * k * R;
+  p.total = p.off4 + m * SIDE_T;
+  return p;
+}
+
+struct DownPlan {
+  int wr, fm;
+  int64_t rb;
+  int s, cps, wn;
+  int64_t total;  // floats
+};
+
+DownPlan down_plan(int64_t m, int64_t k, int64_t r) {
+  DownPlan p;
+  p.wr = m > 16 ? 4 : 1;
+  p.fm = m > 64 ? 2 : 1;
+  p.wn = 4 / p.wr;
+  const int64_t rows = 16 * p.wr * p.fm;
+  p.rb = (m + rows - 1) / rows;
+  split_of(m > 0 ? k / SD_KC : 0, p.rb > 0 ? 512 / p.rb : 0, &p.s, &p.cps);
+  p.total = (int64_t)p.s * p.wn * m * padded_rank(r);
   return p;
 }
 
 template <typename SRC, typename TB, int R>
-hipError_t dt_launch(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) {
+hipError_t dy_launch(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) {
+  DtArgs t{a.dy, a.lddy, a.b, a.ldb, a.m, a.n, a.r, p.s1, p.cps1, a.ws};
+  OuterArgs o{a.dy, a.lddy, a.n, a.t, a.m, a.r, p.s2, p.cps2, p.nmc, a.ws + p.off2};
   const dim3 grid((unsigned)(p.rb * p.s1)), block(256);
   if (p.wr == 4)
-    hipLaunchKernelGGL((k_side_dt<SRC, TB, R, 4>), grid, block, 0, stream, (const typename SRC::elem*)a.dy, a.lddy,
-                       (const TB*)a.b, a.ldb, a.m, a.n, a.r, p.s1, p.cps1, a.ws);
+    hipLaunchKernelGGL((k_side_dt<SRC, TB, R, 4>), grid, block, 0, stream, t);
   else
-    hipLaunchKernelGGL((k_side_dt<SRC, TB, R, 1>), grid, block, 0, stream, (const typename SRC::elem*)a.dy, a.lddy,
-                       (const TB*)a.b, a.ldb, a.m, a.n, a.r, p.s1, p.cps1, a.ws);
+    hipLaunchKernelGGL((k_side_dt<SRC, TB, R, 1>), grid, block, 0, stream, t);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_side_outer<SRC, R>), dim3((unsigned)(p.cb2 * p.s2 * OuterShape<R>::HALVES)), block, 0, stream, o);
   return hipGetLastError();
 }
 
@@ -547,85 +763,70 @@ template <int R>
 hipError_t grad_r(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) {
   hipError_t e = hipSuccess;
   const dim3 block(256);
-  if (p.s1 > 0) {
+  if (a.m > 0 && a.n > 0) {
     if (a.dy_bf16)
-      e = a.b_bf16 ? dt_launch<SrcBf16, uint16_t, R>(a, p, stream) : dt_launch<SrcBf16, float, R>(a, p, stream);
+      e = a.b_bf16 ? dy_launch<SrcBf16, uint16_t, R>(a, p, stream) : dy_launch<SrcBf16, float, R>(a, p, stream);
     else
-      e = a.b_bf16 ? dt_launch<SrcF32, uint16_t, R>(a, p, stream) : dt_launch<SrcF32, float, R>(a, p, stream);
+      e = a.b_bf16 ? dy_launch<SrcF32, uint16_t, R>(a, p, stream) : dy_launch<SrcF32, float, R>(a, p, stream);
     if (e != hipSuccess) return e;
   }
-  OuterArgs o{};
-  o.m = a.m;
-  o.r = a.r;
-  o.nmc = p.nmc;
-  if (p.s2 > 0) {
-    o.big = a.dy;
-    o.ldbig = a.lddy;
-    o.width = a.n;
-    o.small = a.t;
-    o.splits = p.s2;
-    o.chunks_per_split = p.cps2;
-    o.part = a.ws + p.off2;
-    const dim3 grid((unsigned)(p.cb2 * p.s2));
-    if (a.dy_bf16)
-      hipLaunchKernelGGL((k_side_outer<SrcBf16, R, false>), grid, block, 0, stream, o);
-    else
-      hipLaunchKernelGGL((k_side_outer<SrcF32, R, false>), grid, block, 0, stream, o);
+  const int64_t nb_dt = (a.m * (SIDE_T / 4) + 255) / 256, nb_db = (a.n * (R / 4) + 255) / 256;
+  if (nb_dt + nb_db > 0) {
+    hipLaunchKernelGGL((k_side_join<R>), dim3((unsigned)(nb_dt + nb_db)), block, 0, stream, a.ws, p.s1 * p.wn, a.m,
+                       a.sa, a.dt, a.ws + p.off4, a.ws + p.off2, p.s2, a.n, a.db, a.lddb, a.alpha, a.r, (unsigned)nb_dt);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (p.s3 > 0) {
-    o.big = a.qa;
-    o.ldbig = a.ldqa;
-    o.width = a.k;
-    o.small = a.ws;
-    o.np = p.s1 * p.wn;
-    o.alpha = a.alpha;
-    o.sa = a.sa;
-    o.dt = a.dt;
-    o.splits = p.s3;
-    o.chunks_per_split = p.cps3;
-    o.part = a.ws + p.off3;
-    hipLaunchKernelGGL((k_side_outer<SrcI8, R, true>), dim3((unsigned)(p.cb3 * p.s3)), block, 0, stream, o);
+  if (a.m > 0) {
+    const OuterArgs o{a.qa, a.ldqa, a.k, a.ws + p.off4, a.m, a.r, p.s3, p.cps3, p.nmc, a.ws + p.off3};
+    hipLaunchKernelGGL((k_side_outer<SrcI8, R>), dim3((unsigned)(p.cb3 * p.s3 * OuterShape<R>::HALVES)), block, 0, stream, o);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const int64_t nb_db = (a.n * (R / 4) + 255) / 256;
   const int64_t nb_da = ((int64_t)a.r * (a.k / 256) + 7) / 8;
-  hipLaunchKernelGGL((k_side_join<R>), dim3((unsigned)(nb_db + nb_da)), block, 0, stream, a.ws + p.off2, p.s2, a.n,
-                     a.alpha, a.db, a.lddb, a.ws + p.off3, p.s3, (int)a.k, a.da, a.ldda, a.rotate, a.r, nb_db);
+  hipLaunchKernelGGL((k_side_join_da<R>), dim3((unsigned)nb_da), dim3(1024), 0, stream, a.ws + p.off3, p.s3, (int)a.k, a.da,
+                     a.ldda, a.rotate, a.r);
+  return hipGetLastError();
+}
+
+template <typename TA, int R>
+hipError_t down_r(const SideDownArgs& a, hipStream_t stream) {
+  const DownPlan p = down_plan(a.m, a.k, a.r);
+  const DownArgs d{a.qa, a.ldqa, a.a, a.lda, a.m, a.r, p.s, p.cps, (int)(a.k / SD_KC), a.ws};
+  const dim3 grid((unsigned)(p.rb * p.s)), block(256);
+  if (p.wr == 1)
+    hipLaunchKernelGGL((k_side_down<TA, R, 1, 1>), grid, block, 0, stream, d);
+  else if (p.fm == 1)
+    hipLaunchKernelGGL((k_side_down<TA, R, 4, 1>), grid, block, 0, stream, d);
+  else
+    hipLaunchKernelGGL((k_side_down<TA, R, 4, 2>), grid, block, 0, stream, d);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const unsigned nb = (unsigned)((a.m * (SIDE_T / 4) + 255) / 256);
+  hipLaunchKernelGGL((k_side_join<R>), dim3(nb), block, 0, stream, a.ws, p.s * p.wn, a.m, a.sa,
+                     (float*)nullptr, a.t, (const float*)nullptr, 0, (int64_t)0, (float*)nullptr, (int64_t)0, 1.f, a.r, nb);
   return hipGetLastError();
 }
 
 template <typename TA>
-hipError_t down_a(const int8_t* qa, int64_t ldqa, const float* sa, const TA* a, int64_t lda, int64_t m, int64_t k,
-                  int r, float* t, hipStream_t stream) {
-  const int64_t rb = (m + 15) / 16;
-  const dim3 grid((unsigned)(rb < 65536 ? rb : 65536)), block(64 * SD_WAVES);
-#define TP_SIDE_DOWN(R) \
-  hipLaunchKernelGGL((k_side_down<TA, R>), grid, block, 0, stream, qa, ldqa, sa, a, lda, m, (int)k, r, t)
-  if (r <= 16)
-    TP_SIDE_DOWN(16);
-  else if (r <= 32)
-    TP_SIDE_DOWN(32);
-  else
-    TP_SIDE_DOWN(64);
-#undef TP_SIDE_DOWN
-  return hipGetLastError();
+hipError_t down_a(const SideDownArgs& a, hipStream_t stream) {
+  if (a.r <= 16) return down_r<TA, 16>(a, stream);
+  if (a.r <= 32) return down_r<TA, 32>(a, stream);
+  return down_r<TA, 64>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_side_down(const int8_t* qa, int64_t ldqa, const float* sa, const void* a, bool a_bf16, int64_t lda,
-                            int64_t m, int64_t k, int r, float* t, hipStream_t stream) {
-  return a_bf16 ? down_a(qa, ldqa, sa, (const uint16_t*)a, lda, m, k, r, t, stream)
-                : down_a(qa, ldqa, sa, (const float*)a, lda, m, k, r, t, stream);
+hipError_t launch_side_down(const SideDownArgs& a, hipStream_t stream) {
+  return a.a_bf16 ? down_a<uint16_t>(a, stream) : down_a<float>(a, stream);
 }
+
+int64_t side_down_workspace_floats(int64_t m, int64_t k, int64_t r) { return down_plan(m, k, r).total; }
 
 int64_t side_grad_workspace_floats(int64_t m, int64_t n, int64_t k, int64_t r) { return side_plan(m, n, k, r).total; }
 
 hipError_t launch_side_grad(const SideGradArgs& a, hipStream_t stream) {
   const SidePlan p = side_plan(a.m, a.n, a.k, a.r);
-  if (p.R == 16) return grad_r<16>(a, p, stream);
-  if (p.R == 32) return grad_r<32>(a, p, stream);
+  if (a.r <= 16) return grad_r<16>(a, p, stream);
+  if (a.r <= 32) return grad_r<32>(a, p, stream);
   return grad_r<64>(a, p, stream);
 }
 

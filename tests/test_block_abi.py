@@ -97,8 +97,8 @@ def test_binding_refuses_host_tensors():
 
 
 # ------------------------------------------------- side path on 8-bit activations
-def dn(lib, q=A, ldq=512, s=B, a=C, adt=0, lda=512, m=64, k=512, r=16, t=D, tb=1 << 20):
-    return lib.tp_lora_down_prequantized(q, ldq, s, a, adt, lda, m, k, r, t, tb, None)
+def dn(lib, q=A, ldq=512, s=B, a=C, adt=0, lda=512, m=64, k=512, r=16, t=D, tb=1 << 20, ws=E, wsb=1 << 24):
+    return lib.tp_lora_down_prequantized(q, ldq, s, a, adt, lda, m, k, r, t, tb, ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -106,7 +106,9 @@ def dn(lib, q=A, ldq=512, s=B, a=C, adt=0, lda=512, m=64, k=512, r=16, t=D, tb=1
     (dict(q=0), 1), (dict(s=0), 1), (dict(a=0), 1), (dict(t=0), 1),
     (dict(ldq=511), 4), (dict(lda=500), 4), (dict(q=A + 8), 5), (dict(ldq=520), 5), (dict(a=C + 8), 5),
     (dict(s=B + 1), 5), (dict(t=D + 4), 5), (dict(adt=4), 6), (dict(tb=64 * 256 - 1), 9),
-    (dict(lda=2 ** 62), 8), (dict(t=A + 1024), 10), (dict(t=B), 10), (dict(t=C), 10),
+    (dict(lda=2 ** 62), 8), (dict(t=A + 1024), 10), (dict(t=B), 10), (dict(t=C), 10), (dict(m=2 ** 28), 2),
+    (dict(ws=0), 9), (dict(wsb=16), 9), (dict(ws=E + 8), 5), (dict(ws=A), 10), (dict(ws=B), 10), (dict(ws=C), 10),
+    (dict(ws=D), 10),
 ])
 def test_down_refusals(lib, kw, status):
     assert dn(lib, **kw) == status, _err(lib)
@@ -138,6 +140,12 @@ def gr(lib, dy=A, ydt=0, lddy=512, q=B, ldq=512, s=C, t=D, b=E, bdt=0, ldb=16, a
 def test_grad_refusals(lib, kw, status):
     assert gr(lib, **kw) == status, _err(lib)
     assert _err(lib)
+
+
+def test_down_workspace_query(lib):
+    assert lib.tp_lora_down_prequantized_workspace_size(64, 512, 16) > 0
+    for args in ((-1, 256, 4), (0, 256, 4), (8, 300, 4), (8, 0, 4), (8, 256, 0), (8, 256, 65), (2 ** 28, 256, 4)):
+        assert lib.tp_lora_down_prequantized_workspace_size(*args) == 0
 
 
 def test_grad_workspace_query(lib):
