@@ -24,6 +24,12 @@ _DTYPE = {torch.float32: _lib.TP_F32, torch.bfloat16: _lib.TP_BF16}
 _KIND = {"i8": (TP_NORM_OUT_I8, torch.int8), "bf16": (TP_NORM_OUT_BF16, torch.bfloat16)}
 
 
+# A call on a handful of rows takes less time on the GPU than in Python, so the
+# checks below take the short way where everything is in order.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _dt(t, name):
     try:
         return _DTYPE[t.dtype]
@@ -31,14 +37,16 @@ def _dt(t, name):
         raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)") from None
 
 
-def _device(first, **others):
-    """The one CUDA (HIP) device of a call's tensors (None: not given)."""
+def _device(first, names, *others):
+    """The one CUDA (HIP) device of a call's tensors (None: not given); names
+    are the others', for the message."""
     if not isinstance(first, torch.Tensor) or not first.is_cuda:
         raise ValueError("the operands must be CUDA (HIP) tensors")
-    for name, t in others.items():
-        if t is not None and (not isinstance(t, torch.Tensor) or t.device != first.device):
-            raise ValueError(f"{name} must be a tensor on {first.device}")
-    return first.device
+    device = first.device
+    for i, t in enumerate(others):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.device != device):
+            raise ValueError(f"{names.split()[i]} must be a tensor on {device}")
+    return device
 
 
 def _elsewhere(device, stream):
@@ -48,34 +56,48 @@ def _elsewhere(device, stream):
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the operands on {device}")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         return torch.cuda.device(device)
     return None
 
 
 def _raw_stream(device):
+    if _raw_stream_of is not None:
+        return _raw_stream_of(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _new(m, k, dtype, device):
+    return torch.empty_strided((m, k), (k, 1), dtype=dtype, device=device)
+
+
+def _new_vec(n, dtype, device):
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
 
 
 def _mat(t, name, shape=None, dtype=None):
     """Checks a 2-D row-major matrix; returns its row pitch in elements (any
     pitch describes a single row: the shortest that the C boundary takes)."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be {'2-D' if shape is None else shape}, got shape {tuple(t.shape)}")
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
+        raise ValueError(f"{name} must be {'2-D' if shape is None else tuple(shape)}, got shape {tuple(size)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = size
+    pitch, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    if t.shape[0] > 1:
-        return t.stride(0)
+    if rows > 1:
+        return pitch
     per = 16 // t.element_size()
-    return -(-t.shape[1] // per) * per
+    return -(-cols // per) * per
 
 
 def _vec(t, name, count, dtype=None):
     """Checks a contiguous vector."""
-    if t.dim() != 1 or t.shape[0] != count or (count > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {count} elements, got shape {tuple(t.shape)}")
+    size = t.shape
+    if len(size) != 1 or size[0] != count or (count > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {count} elements, got shape {tuple(size)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t
@@ -92,8 +114,9 @@ def _scratch(workspace, need, device):
     """Pointer and size of the caller's scratch tensor, or of a new one (kept
     alive by the third value until the launch)."""
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=device)
-    elif not workspace.is_contiguous():
+        workspace = _new_vec(max(need, 16), torch.uint8, device)
+        return workspace.data_ptr(), need, workspace
+    if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
@@ -106,7 +129,7 @@ def tp_rmsnorm_rotate(x, gamma=None, eps=1e-6, residual=None, rotate=True, out_k
     ("bf16"). Returns (codes, scales) or rows; with a residual also t, the new
     stream: (codes, scales, t) or (rows, t). sum_out may be residual (or x)
     itself."""
-    dev = _device(x, gamma=gamma, residual=residual, out=out, scales=scales, sum_out=sum_out)
+    dev = _device(x, "gamma residual out scales sum_out", gamma, residual, out, scales, sum_out)
     scope = _elsewhere(dev, stream)
     if scope is not None:
         with scope:
@@ -123,18 +146,18 @@ def tp_rmsnorm_rotate(x, gamma=None, eps=1e-6, residual=None, rotate=True, out_k
         ldr = _mat(residual, "residual", (m, k))
         s_dt = _dt(residual, "residual")
         if sum_out is None:
-            sum_out = torch.empty((m, k), dtype=residual.dtype, device=dev)
+            sum_out = _new(m, k, residual.dtype, dev)
         lds = _mat(sum_out, "sum_out", (m, k), residual.dtype)
         r_ptr, s_ptr = residual.data_ptr(), sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if out is None:
-        out = torch.empty((m, k), dtype=y_dtype, device=dev)
+        out = _new(m, k, y_dtype, dev)
     ldy = _mat(out, "out", (m, k), y_dtype)
     sc_ptr = None
     if kind == TP_NORM_OUT_I8:
         if scales is None:
-            scales = torch.empty((m,), dtype=torch.float32, device=dev)
+            scales = _new_vec(m, torch.float32, dev)
         sc_ptr = _vec(scales, "scales", m, torch.float32).data_ptr()
     elif scales is not None:
         raise ValueError("scales belong to out_kind 'i8'")
@@ -159,7 +182,7 @@ def tp_rmsnorm_rotate_backward(dy, t, gamma=None, eps=1e-6, dsum=None, rotate=Tr
     x), dsum the gradient that reaches the stream from behind. Returns
     (dx, dgamma); dgamma is None where it is not wanted. dx (default dtype:
     dsum's, else t's) may be dsum or dy itself."""
-    dev = _device(dy, t=t, gamma=gamma, dsum=dsum, dx=dx, dgamma=dgamma, workspace=workspace)
+    dev = _device(dy, "t gamma dsum dx dgamma workspace", t, gamma, dsum, dx, dgamma, workspace)
     scope = _elsewhere(dev, stream)
     if scope is not None:
         with scope:
@@ -170,7 +193,7 @@ def tp_rmsnorm_rotate_backward(dy, t, gamma=None, eps=1e-6, dsum=None, rotate=Tr
     ldt = _mat(t, "t", (m, k))
     g_ptr, g_dt = _weight(gamma, "gamma", k)
     if dx is None:
-        dx = torch.empty((m, k), dtype=dx_dtype or (t if dsum is None else dsum).dtype, device=dev)
+        dx = _new(m, k, dx_dtype or (t if dsum is None else dsum).dtype, dev)
     elif dx_dtype is not None and dx.dtype != dx_dtype:
         raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
     lddx = _mat(dx, "dx", (m, k))
@@ -180,7 +203,7 @@ def tp_rmsnorm_rotate_backward(dy, t, gamma=None, eps=1e-6, dsum=None, rotate=Tr
     ws_bytes = 0
     if want:
         if dgamma is None:
-            dgamma = torch.empty((k,), dtype=torch.float32, device=dev)
+            dgamma = _new_vec(k, torch.float32, dev)
         dg_ptr = _vec(dgamma, "dgamma", k, torch.float32).data_ptr()
         ws_ptr, ws_bytes, ws = _scratch(workspace, tp_rmsnorm_backward_workspace_size(m, k), dev)
     _lib.check(_lib.load().tp_rmsnorm_rotate_backward(
@@ -202,7 +225,7 @@ def tp_lora_down_prequantized(qa, sa, lora_a, t=None, workspace=None, stream=Non
     """T = sa (qa . lora_a^T) in fp32 rows of 64 (zeros past r): the first half
     of the side path on activations held as int8 codes and scales; lora_a
     [r, k] in the codes' domain. Returns T [m, 64], as tp_lora_down does."""
-    dev = _device(qa, sa=sa, lora_a=lora_a, t=t, workspace=workspace)
+    dev = _device(qa, "sa lora_a t workspace", sa, lora_a, t, workspace)
     scope = _elsewhere(dev, stream)
     if scope is not None:
         with scope:
@@ -225,7 +248,7 @@ def tp_lora_down_prequantized(qa, sa, lora_a, t=None, workspace=None, stream=Non
 def _t_rows(t, name, m, device):
     """fp32 [m, 64] contiguous, allocated where it is not given."""
     if t is None:
-        return torch.empty((m, _T), dtype=torch.float32, device=device)
+        return _new(m, _T, torch.float32, device)
     if _mat(t, name, (m, _T), torch.float32) != _T:
         raise ValueError(f"{name} must be contiguous")
     return t
@@ -243,7 +266,7 @@ def tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha, rotate=False, da=Non
     dy^T T, alpha dy . lora_b), fp32. dA is in the codes' domain, or with
     rotate=True rotated back (the gradient of an un-rotated lora_a); dT [m, 64]
     gives dx = dT . lora_a."""
-    dev = _device(dy, qa=qa, sa=sa, t=t, lora_b=lora_b, da=da, db=db, dt=dt, workspace=workspace)
+    dev = _device(dy, "qa sa t lora_b da db dt workspace", qa, sa, t, lora_b, da, db, dt, workspace)
     scope = _elsewhere(dev, stream)
     if scope is not None:
         with scope:
@@ -264,10 +287,10 @@ def tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha, rotate=False, da=Non
         raise ValueError(f"lora_b must be [{n}, r], got shape {tuple(lora_b.shape)}")
     dt = _t_rows(dt, "dt", m, dev)
     if da is None:
-        da = torch.empty((r, k), dtype=torch.float32, device=dev)
+        da = _new(r, k, torch.float32, dev)
     ldda = _mat(da, "da", (r, k), torch.float32)
     if db is None:
-        db = torch.empty((n, r), dtype=torch.float32, device=dev)
+        db = _new(n, r, torch.float32, dev)
     lddb = _mat(db, "db", (n, r), torch.float32)
     ws_ptr, ws_bytes, ws = _scratch(workspace, tp_lora_grad_workspace_size(m, n, k, r), dev)
     _lib.check(_lib.load().tp_lora_grad_prequantized(
@@ -311,7 +334,7 @@ def _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_g
         axes = positions.shape[1]
         pos_ptr = positions.data_ptr()
         freq_ptr = _vec(inv_freq, "inv_freq", pairs, torch.float32).data_ptr()
-        axis = bytes(pairs) if pair_axis is None else bytes(pair_axis)
+        axis = bytes(pairs) if pair_axis is None else pair_axis if type(pair_axis) is bytes else bytes(pair_axis)
         if len(axis) != pairs:
             raise ValueError(f"pair_axis must have {pairs} entries, got {len(axis)}")
     return (qg, kg, g_dt, eps, pos_ptr, ldpos, axes, freq_ptr, axis, pairs, _LAYOUT[layout])
@@ -326,8 +349,8 @@ def tp_qk_norm_rope(q, k, head_dim, positions=None, inv_freq=None, pair_axis=Non
     layout "interleaved" (pairs of neighbours) or "halves". Columns past the
     rotated ones are passed on. Returns (q_out, k_out), which may be the inputs
     themselves; default dtype: the inputs'."""
-    dev = _device(q, k=k, positions=positions, inv_freq=inv_freq, q_gamma=q_gamma, k_gamma=k_gamma, q_out=q_out,
-                  k_out=k_out)
+    dev = _device(q, "k positions inv_freq q_gamma k_gamma q_out k_out", k, positions, inv_freq, q_gamma, k_gamma,
+                  q_out, k_out)
     scope = _elsewhere(dev, stream)
     if scope is not None:
         with scope:
@@ -340,11 +363,11 @@ def tp_qk_norm_rope(q, k, head_dim, positions=None, inv_freq=None, pair_axis=Non
     if out_dtype is None:
         out_dtype = q.dtype if q_out is None else q_out.dtype
     if q_out is None:
-        q_out = torch.empty((m, hq * head_dim), dtype=out_dtype, device=dev)
+        q_out = _new(m, hq * head_dim, out_dtype, dev)
     if k_out is None:
-        k_out = torch.empty((m, hk * head_dim), dtype=out_dtype, device=dev)
-    ldqo = _mat(q_out, "q_out", tuple(q.shape), out_dtype)
-    ldko = _mat(k_out, "k_out", tuple(k.shape), out_dtype)
+        k_out = _new(m, hk * head_dim, out_dtype, dev)
+    ldqo = _mat(q_out, "q_out", q.shape, out_dtype)
+    ldko = _mat(k_out, "k_out", k.shape, out_dtype)
     _lib.check(_lib.load().tp_qk_norm_rope(
         q.data_ptr(), ldq, k.data_ptr(), ldk, _dt(q, "q"), m, hq, hk, head_dim, *shared, q_out.data_ptr(), ldqo,
         k_out.data_ptr(), ldko, _dt(q_out, "q_out"), _raw_stream(dev)))
@@ -364,8 +387,8 @@ def tp_qk_norm_rope_backward(dq_out, dk_out, q, k, head_dim, positions=None, inv
     None for a tensor without a norm or where want_dgamma is False. q and k (the
     forward's inputs) may be None for a tensor without a norm. Default dtype of
     dq and dk: dq_out's."""
-    dev = _device(dq_out, dk_out=dk_out, q=q, k=k, positions=positions, inv_freq=inv_freq, q_gamma=q_gamma,
-                  k_gamma=k_gamma, dq=dq, dk=dk, dq_gamma=dq_gamma, dk_gamma=dk_gamma, workspace=workspace)
+    dev = _device(dq_out, "dk_out q k positions inv_freq q_gamma k_gamma dq dk dq_gamma dk_gamma workspace", dk_out,
+                  q, k, positions, inv_freq, q_gamma, k_gamma, dq, dk, dq_gamma, dk_gamma, workspace)
     scope = _elsewhere(dev, stream)
     if scope is not None:
         with scope:
@@ -382,24 +405,24 @@ def tp_qk_norm_rope_backward(dq_out, dk_out, q, k, head_dim, positions=None, inv
             continue
         if x is None:
             raise ValueError(f"{name} is needed for the gradient of its norm")
-        x_ld[i] = _mat(x, name, tuple(like.shape))
+        x_ld[i] = _mat(x, name, like.shape)
         if x_dt is not None and _dt(x, name) != x_dt:
             raise TypeError("q and k must have one dtype")
         x_ptr[i], x_dt = x.data_ptr(), _dt(x, name)
     if dx_dtype is None:
         dx_dtype = dq_out.dtype if dq is None else dq.dtype
     if dq is None:
-        dq = torch.empty(tuple(dq_out.shape), dtype=dx_dtype, device=dev)
+        dq = _new(m, hq * head_dim, dx_dtype, dev)
     if dk is None:
-        dk = torch.empty(tuple(dk_out.shape), dtype=dx_dtype, device=dev)
-    lddq = _mat(dq, "dq", tuple(dq_out.shape), dx_dtype)
-    lddk = _mat(dk, "dk", tuple(dk_out.shape), dx_dtype)
+        dk = _new(m, hk * head_dim, dx_dtype, dev)
+    lddq = _mat(dq, "dq", dq_out.shape, dx_dtype)
+    lddk = _mat(dk, "dk", dk_out.shape, dx_dtype)
     if q_gamma is None and dq_gamma is not None or k_gamma is None and dk_gamma is not None:
         raise ValueError("the gradient of a weight that is not given")
     if want_dgamma and q_gamma is not None and dq_gamma is None:
-        dq_gamma = torch.empty((head_dim,), dtype=torch.float32, device=dev)
+        dq_gamma = _new_vec(head_dim, torch.float32, dev)
     if want_dgamma and k_gamma is not None and dk_gamma is None:
-        dk_gamma = torch.empty((head_dim,), dtype=torch.float32, device=dev)
+        dk_gamma = _new_vec(head_dim, torch.float32, dev)
     dg_ptr = [None if t is None else _vec(t, n, head_dim, torch.float32).data_ptr()
               for t, n in ((dq_gamma, "dq_gamma"), (dk_gamma, "dk_gamma"))]
     ws_ptr = ws = None
