@@ -6,9 +6,9 @@
 //   theta_p = position[axis(p)] f_p for the pairs p of a head
 //   (a, b) -> (a cos theta - b sin theta, a sin theta + b cos theta)
 //
-// The angles of a token are the same for all its heads: a block takes a token
-// at a time, works out the cosines and sines of its pairs once, into LDS, and
-// turns every head of q and k with them. The angle is an fp64 product (a far
+// The angles of a token are the same for all its heads: a block takes a few
+// tokens at a time, works out the cosines and sines of their pairs once, into
+// LDS, and turns every head of q and k with them. The angle is an fp64 product (a far
 // position times a frequency does not fit in fp32), reduced to a fraction of a
 // turn there and only then taken to fp32.
 //
@@ -24,28 +24,67 @@ namespace tp {
 constexpr int ROPE_THREADS = 256;
 constexpr double TURN_HI = 0x1.45f306dc9c883p-3, TURN_LO = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
 
-__device__ __forceinline__ void load4(const void* p, int bf16, int64_t i, float (&v)[4]) {
-  if (bf16) {
-    const uint2 w = *reinterpret_cast<const uint2*>((const uint16_t*)p + i);
-    v[0] = bf16_lo(w.x);
-    v[1] = bf16_hi(w.x);
-    v[2] = bf16_lo(w.y);
-    v[3] = bf16_hi(w.y);
-  } else {
-    const f32x4_t w = *reinterpret_cast<const f32x4_t*>((const float*)p + i);
-    v[0] = w.x;
-    v[1] = w.y;
-    v[2] = w.z;
-    v[3] = w.w;
-  }
-}
+// A lane's eight elements of a head: two runs of four.
+template <typename T>
+struct Eight;
 
-__device__ __forceinline__ void store4(void* p, int bf16, int64_t i, const float (&v)[4]) {
-  if (bf16)
-    *reinterpret_cast<uint2*>((uint16_t*)p + i) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  else
-    *reinterpret_cast<f32x4_t*>((float*)p + i) = f32x4_t{v[0], v[1], v[2], v[3]};
-}
+template <>
+struct Eight<uint16_t> {
+  uint2 w[2];
+  __device__ __forceinline__ void load(const uint16_t* p, int o0, int o1) {
+    w[0] = *reinterpret_cast<const uint2*>(p + o0);
+    w[1] = *reinterpret_cast<const uint2*>(p + o1);
+  }
+  __device__ __forceinline__ void load(const uint16_t* p) {  // one run of eight
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(p);
+    w[0] = uint2{v.x, v.y};
+    w[1] = uint2{v.z, v.w};
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = uint2{0u, 0u}; }
+  __device__ __forceinline__ void get(float (&x)[4], float (&y)[4]) const {
+    x[0] = bf16_lo(w[0].x);
+    x[1] = bf16_hi(w[0].x);
+    x[2] = bf16_lo(w[0].y);
+    x[3] = bf16_hi(w[0].y);
+    y[0] = bf16_lo(w[1].x);
+    y[1] = bf16_hi(w[1].x);
+    y[2] = bf16_lo(w[1].y);
+    y[3] = bf16_hi(w[1].y);
+  }
+  static __device__ __forceinline__ void store(uint16_t* p, int o0, int o1, const float (&x)[4], const float (&y)[4]) {
+    *reinterpret_cast<uint2*>(p + o0) = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    *reinterpret_cast<uint2*>(p + o1) = uint2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+  }
+  static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[4], const float (&y)[4]) {
+    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                             pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+  }
+};
+
+template <>
+struct Eight<float> {
+  f32x4_t w[2];
+  __device__ __forceinline__ void load(const float* p, int o0, int o1) {
+    w[0] = *reinterpret_cast<const f32x4_t*>(p + o0);
+    w[1] = *reinterpret_cast<const f32x4_t*>(p + o1);
+  }
+  __device__ __forceinline__ void load(const float* p) { load(p, 0, 4); }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = f32x4_t{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ void get(float (&x)[4], float (&y)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = w[0][e];
+      y[e] = w[1][e];
+    }
+  }
+  static __device__ __forceinline__ void store(float* p, int o0, int o1, const float (&x)[4], const float (&y)[4]) {
+    *reinterpret_cast<f32x4_t*>(p + o0) = f32x4_t{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4_t*>(p + o1) = f32x4_t{y[0], y[1], y[2], y[3]};
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&x)[4], const float (&y)[4]) {
+    store(p, 0, 4, x, y);
+  }
+};
 
 // Four pairs of a lane: a the first members, b the second ones.
 struct Pairs {
@@ -113,95 +152,101 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
-// The cosines and sines of a token's pairs. 1 / (2 pi) is taken in two doubles
+// The cosines and sines of a token's pair. 1 / (2 pi) is taken in two doubles
 // and the whole turns come off in one fma, so the fraction of a turn carries no
 // more than the angle's own rounding; sincospif takes it from there.
-__device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, float2* turns) {
-  for (int p = threadIdx.x; p < a.pairs; p += ROPE_THREADS) {
-    const double angle = (double)a.positions[token * a.ldpos + a.axis[p]] * (double)a.inv_freq[p];
-    const double turn = fma(angle, TURN_HI, -rint(angle * TURN_HI)) + angle * TURN_LO;
-    float s, c;
-    sincospif((float)(2.0 * turn), &s, &c);
-    turns[p] = float2{c, s};
-  }
+__device__ __forceinline__ float2 turn_of(const RopeArgs& a, int64_t token, int p) {
+  const double angle = (double)a.positions[token * a.ldpos + a.axis[p]] * (double)a.inv_freq[p];
+  const double turn = fma(angle, TURN_HI, -rint(angle * TURN_HI)) + angle * TURN_LO;
+  float s, c;
+  sincospif((float)(2.0 * turn), &s, &c);
+  return float2{c, s};
 }
 
+// What the kernel needs of q or of k.
+struct Heads {
+  const void *x, *dy;
+  void* out;
+  int64_t ldx, lddy, ldout;
+  VecArg gamma;
+  int begin, count;  // the block's heads
+};
+
 // Forward (BWD false): out = R (x r gamma). Backward: g = R^T dy, then the
-// norm's gradient where there is one, with dgamma kept per lane.
-template <bool HALVES, bool BWD>
-__global__ __launch_bounds__(ROPE_THREADS) void k_rope(RopeArgs a, int lanes, int units) {
-  __shared__ float2 turns[2][ROPE_MAX_PAIRS];
+// norm's gradient where there is one, with dgamma kept per lane. A block takes
+// `batch` tokens at a time (as many as its threads have pairs for) and a slice
+// of their heads; the next head's elements are in flight while one is turned.
+template <bool HALVES, bool BWD, typename TX, typename TY, typename TO>
+__global__ __launch_bounds__(ROPE_THREADS) void k_rope(RopeArgs a, int lanes, int slices, int batch) {
+  __shared__ __align__(16) float2 turns[ROPE_THREADS];
   __shared__ float red[2][ROPE_THREADS][8];
-  const int d = a.head_dim, heads = a.heads_q + a.heads_k;
+  const int d = a.head_dim;
   const int u = threadIdx.x & (lanes - 1), g0 = threadIdx.x / lanes, groups = ROPE_THREADS / lanes;
   const Where w = where_of<HALVES>(u, d, a.pairs);
+  const bool turned = w.pair < a.pairs;
   const float inv_d = 1.0f / (float)d, eps = fmaxf((float)a.eps, 0x1p-126f);
-  // The block's slice of a token's heads, for few tokens (units slices).
-  const int slice = (int)(blockIdx.x % (unsigned)units);
-  const int h_begin = heads * slice / units, h_end = heads * (slice + 1) / units;
-  const int64_t first = blockIdx.x / (unsigned)units, step = gridDim.x / (unsigned)units;
+  const int slice = (int)(blockIdx.x % (unsigned)slices);
+  const int64_t first = (int64_t)(blockIdx.x / (unsigned)slices) * batch;
+  const int64_t step = (int64_t)(gridDim.x / (unsigned)slices) * batch;
 
-  Pairs gq, gk;  // weights
-  {
+  auto weight = [&](const VecArg& g, Pairs& p) {
     float x[4] = {1.f, 1.f, 1.f, 1.f}, y[4] = {1.f, 1.f, 1.f, 1.f};
-    if (a.q_gamma.p && w.on) {
-      load4(a.q_gamma.p, a.q_gamma.bf16, w.o0, x);
-      load4(a.q_gamma.p, a.q_gamma.bf16, w.o1, y);
-    }
-    to_pairs<HALVES>(x, y, gq);
-  }
-  {
-    float x[4] = {1.f, 1.f, 1.f, 1.f}, y[4] = {1.f, 1.f, 1.f, 1.f};
-    if (a.k_gamma.p && w.on) {
-      load4(a.k_gamma.p, a.k_gamma.bf16, w.o0, x);
-      load4(a.k_gamma.p, a.k_gamma.bf16, w.o1, y);
-    }
-    to_pairs<HALVES>(x, y, gk);
-  }
-  Pairs sq, sk;  // dgamma of this lane's pairs
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sq.a[e] = sq.b[e] = sk.a[e] = sk.b[e] = 0.f;
-
-  int parity = 0;
-  for (int64_t token = first; token < a.m; token += step, parity ^= 1) {
-    token_turns(a, token, turns[parity]);
-    __syncthreads();  // (slower threads may still read the other parity's turns)
-    Pairs t;  // cosines and sines of the lane's pairs
-    const bool turned = w.pair < a.pairs;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 cs = turned ? turns[parity][w.pair + e] : float2{1.f, 0.f};
-      t.a[e] = cs.x;
-      t.b[e] = BWD ? -cs.y : cs.y;
-    }
-    for (int hb = h_begin; hb < h_end; hb += groups) {  // the same count in every lane: they exchange
-      const int h = hb + g0;
-      const bool live = h < h_end && w.on;
-      const bool is_q = h < a.heads_q;
-      const int head = is_q ? h : h - a.heads_q;
-      const bool norm = is_q ? a.q_gamma.p != nullptr : a.k_gamma.p != nullptr;
-      const Pairs& gm = is_q ? gq : gk;
-      const int64_t off = (int64_t)head * d;
-      float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
-      Pairs x, y;
-      if (!BWD || norm) {
-        if (live) {
-          const void* src = is_q ? a.q : a.k;
-          const int64_t i = token * (is_q ? a.ldq : a.ldk) + off;
-          load4(src, a.x_bf16, i + w.o0, x0);
-          load4(src, a.x_bf16, i + w.o1, x1);
-        }
+    if (g.p != nullptr && w.on) {
+      if (g.bf16) {
+        Eight<uint16_t> r;
+        r.load((const uint16_t*)g.p, w.o0, w.o1);
+        r.get(x, y);
+      } else {
+        Eight<float> r;
+        r.load((const float*)g.p, w.o0, w.o1);
+        r.get(x, y);
       }
-      to_pairs<HALVES>(x0, x1, x);
+    }
+    to_pairs<HALVES>(x, y, p);
+  };
+
+  // One tensor's heads of the tokens t0 .. t0 + nt.
+  auto run = [&](const Heads& h, const Pairs& gm, Pairs& sg, int64_t t0, int nt) {
+    const bool norm = h.gamma.p != nullptr;
+    const int total = nt * h.count;
+    if (total == 0) return;
+    Eight<TX> rx;
+    Eight<TY> ry;
+    auto fetch = [&](int64_t token, int head) {
+      if (!BWD || norm) {
+        const TX* p = (const TX*)h.x + token * h.ldx + (int64_t)head * d;
+        if (HALVES) rx.load(p, w.o0, w.o1); else rx.load(p + w.o0);
+      }
       if (BWD) {
-        float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
-        if (live) {
-          const void* src = is_q ? a.dq_out : a.dk_out;
-          const int64_t i = token * (is_q ? a.lddqo : a.lddko) + off;
-          load4(src, a.dy_bf16, i + w.o0, y0);
-          load4(src, a.dy_bf16, i + w.o1, y1);
-        }
-        to_pairs<HALVES>(y0, y1, y);
+        const TY* p = (const TY*)h.dy + token * h.lddy + (int64_t)head * d;
+        if (HALVES) ry.load(p, w.o0, w.o1); else ry.load(p + w.o0);
+      }
+    };
+    // (token, head) units, one a group of lanes; (t, c) walks them
+    int t = g0 / h.count, c = g0 - t * h.count;
+    rx.zero();
+    if (BWD) ry.zero();
+    if (w.on && t < nt) fetch(t0 + t, h.begin + c);
+    for (int ub = 0; ub < total; ub += groups) {  // the same count in every lane: they exchange
+      const bool live = w.on && t < nt;
+      float x0[4], x1[4], y0[4], y1[4];
+      rx.get(x0, x1);
+      if (BWD) ry.get(y0, y1);
+      const int64_t token = t0 + t;
+      const int head = h.begin + c, tl = min(t, nt - 1);
+      c += groups;
+      while (c >= h.count) {
+        c -= h.count;
+        ++t;
+      }
+      if (w.on && t < nt) fetch(t0 + t, h.begin + c);
+      Pairs x, cs;
+      to_pairs<HALVES>(x0, x1, x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = turned ? turns[tl * a.pairs + w.pair + e] : float2{1.f, 0.f};
+        cs.a[e] = v.x;
+        cs.b[e] = BWD ? -v.y : v.y;
       }
       float r = 1.f;
       if (norm) {
@@ -216,27 +261,27 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(RopeArgs a, int lanes, in
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float na = norm ? x.a[e] * r * gm.a[e] : x.a[e], nb = norm ? x.b[e] * r * gm.b[e] : x.b[e];
-          o.a[e] = turned ? na * t.a[e] - nb * t.b[e] : na;
-          o.b[e] = turned ? na * t.b[e] + nb * t.a[e] : nb;
+          o.a[e] = turned ? na * cs.a[e] - nb * cs.b[e] : na;
+          o.b[e] = turned ? na * cs.b[e] + nb * cs.a[e] : nb;
         }
       } else {
+        Pairs y;
+        to_pairs<HALVES>(y0, y1, y);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          o.a[e] = turned ? y.a[e] * t.a[e] - y.b[e] * t.b[e] : y.a[e];
-          o.b[e] = turned ? y.a[e] * t.b[e] + y.b[e] * t.a[e] : y.b[e];
+          o.a[e] = turned ? y.a[e] * cs.a[e] - y.b[e] * cs.b[e] : y.a[e];
+          o.b[e] = turned ? y.a[e] * cs.b[e] + y.b[e] * cs.a[e] : y.b[e];
         }
         if (norm) {
           float s = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s = fmaf(o.a[e] * gm.a[e], x.a[e], fmaf(o.b[e] * gm.b[e], x.b[e], s));
+          for (int e = 0; e < 4; ++e) s = fmaf(o.a[e] * gm.a[e], x.a[e], fmaf(o.b[e] * gm.b[e], x.b[e], s));
           s = group_sum(s, lanes);
-          const float coef = s * inv_d * r * r * r;
-          Pairs& sg = is_q ? sq : sk;
+          const float coef = s * inv_d * r * r * r, count = live ? r : 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sg.a[e] = fmaf(o.a[e] * r, x.a[e], sg.a[e]);
-            sg.b[e] = fmaf(o.b[e] * r, x.b[e], sg.b[e]);
+            sg.a[e] = fmaf(o.a[e] * count, x.a[e], sg.a[e]);
+            sg.b[e] = fmaf(o.b[e] * count, x.b[e], sg.b[e]);
             o.a[e] = fmaf(o.a[e] * gm.a[e], r, -x.a[e] * coef);
             o.b[e] = fmaf(o.b[e] * gm.b[e], r, -x.b[e] * coef);
           }
@@ -245,13 +290,36 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(RopeArgs a, int lanes, in
       if (live) {
         float o0[4], o1[4];
         from_pairs<HALVES>(o, o0, o1);
-        void* dst = is_q ? a.q_out : a.k_out;
-        const int64_t i = token * (is_q ? a.ldqo : a.ldko) + off;
-        store4(dst, a.out_bf16, i + w.o0, o0);
-        store4(dst, a.out_bf16, i + w.o1, o1);
+        TO* p = (TO*)h.out + token * h.ldout + (int64_t)head * d;
+        if (HALVES) Eight<TO>::store(p, w.o0, w.o1, o0, o1); else Eight<TO>::store(p + w.o0, o0, o1);
       }
     }
+  };
+
+  auto slice_of = [&](int heads, int& begin, int& count) {
+    begin = heads * slice / slices;
+    count = heads * (slice + 1) / slices - begin;
+  };
+  Heads hq{a.q, a.dq_out, a.q_out, a.ldq, a.lddqo, a.ldqo, a.q_gamma, 0, 0};
+  Heads hk{a.k, a.dk_out, a.k_out, a.ldk, a.lddko, a.ldko, a.k_gamma, 0, 0};
+  slice_of(a.heads_q, hq.begin, hq.count);
+  slice_of(a.heads_k, hk.begin, hk.count);
+  Pairs gq, gk, sq, sk;  // weights, and this lane's part of their gradients
+  weight(a.q_gamma, gq);
+  weight(a.k_gamma, gk);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sq.a[e] = sq.b[e] = sk.a[e] = sk.b[e] = 0.f;
+
+  for (int64_t t0 = first; t0 < a.m; t0 += step) {
+    const int nt = (int)min((int64_t)batch, a.m - t0);
+    __syncthreads();
+    for (int e = threadIdx.x; e < nt * a.pairs; e += ROPE_THREADS)
+      turns[e] = turn_of(a, t0 + e / a.pairs, e % a.pairs);
+    __syncthreads();
+    run(hq, gq, sq, t0, nt);
+    run(hk, gk, sk, t0, nt);
   }
+
   if (BWD && a.want_dgamma) {  // the block's dgamma: its groups added in order
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -267,9 +335,9 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(RopeArgs a, int lanes, in
       int lane, slot;
       if (HALVES) {
         const int rest = (d - 2 * a.pairs) / 2;
-        const bool turned = i < 2 * a.pairs;
-        const int j = turned ? i : i - 2 * a.pairs, half = turned ? a.pairs : rest;
-        const int second = j >= half, p = (second ? j - half : j) + (turned ? 0 : a.pairs);
+        const bool first_part = i < 2 * a.pairs;
+        const int j = first_part ? i : i - 2 * a.pairs, half = first_part ? a.pairs : rest;
+        const int second = j >= half, p = (second ? j - half : j) + (first_part ? 0 : a.pairs);
         lane = p >> 2;
         slot = 4 * second + (p & 3);
       } else {
@@ -286,49 +354,77 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(RopeArgs a, int lanes, in
 namespace {
 
 struct RopeShape {
-  int lanes, units;
+  int lanes, slices, batch;
   int64_t blocks;
 };
 
 constexpr int64_t ROPE_BLOCKS = 8192, ROPE_BWD_BLOCKS = 1024;  // blocks walk tokens beyond that many
 
-RopeShape rope_shape(int64_t m, int heads, int d, int64_t max_blocks) {
+RopeShape rope_shape(int64_t m, int heads, int d, int pairs, int64_t max_blocks) {
   RopeShape s;
   s.lanes = 1;
   while (s.lanes * 8 < d) s.lanes *= 2;
   const int groups = ROPE_THREADS / s.lanes;
-  // few tokens: a token's heads go to several blocks
+  // As many tokens at a time as the block's threads work out the turns of (4 at
+  // most), but enough blocks for the chip; with few tokens a token's heads go to
+  // several blocks.
+  s.batch = pairs > 0 ? ROPE_THREADS / pairs : 4;
+  if (s.batch > 4) s.batch = 4;
+  while (s.batch > 1 && (m + s.batch - 1) / s.batch < 1024) s.batch /= 2;
   int most = (heads + groups - 1) / groups;
   if (most < 1) most = 1;
-  int64_t want = m > 0 ? 512 / m : 1;
-  s.units = (int)(want < 1 ? 1 : want > most ? most : want);
-  s.blocks = m * s.units;
-  if (s.blocks > max_blocks) s.blocks = max_blocks / s.units * s.units;
+  const int64_t batches = (m + s.batch - 1) / s.batch;
+  const int64_t want = batches > 0 ? 512 / batches : 1;
+  s.slices = (int)(want < 1 ? 1 : want > most ? most : want);
+  s.blocks = batches * s.slices;
+  if (s.blocks > max_blocks) s.blocks = max_blocks / s.slices * s.slices;
   return s;
+}
+
+template <bool HALVES, typename TX, typename TO>
+void rope_forward(const RopeArgs& a, const RopeShape& s, hipStream_t stream) {
+  hipLaunchKernelGGL((k_rope<HALVES, false, TX, TX, TO>), dim3((unsigned)s.blocks), dim3(ROPE_THREADS), 0, stream, a,
+                     s.lanes, s.slices, s.batch);
+}
+
+template <bool HALVES, typename TX, typename TY>
+void rope_backward(const RopeArgs& a, const RopeShape& s, hipStream_t stream) {
+  if (a.out_bf16)
+    hipLaunchKernelGGL((k_rope<HALVES, true, TX, TY, uint16_t>), dim3((unsigned)s.blocks), dim3(ROPE_THREADS), 0,
+                       stream, a, s.lanes, s.slices, s.batch);
+  else
+    hipLaunchKernelGGL((k_rope<HALVES, true, TX, TY, float>), dim3((unsigned)s.blocks), dim3(ROPE_THREADS), 0, stream,
+                       a, s.lanes, s.slices, s.batch);
+}
+
+template <bool HALVES, typename TX>
+void rope_x(const RopeArgs& a, const RopeShape& s, hipStream_t stream) {
+  if (a.backward)
+    a.dy_bf16 ? rope_backward<HALVES, TX, uint16_t>(a, s, stream) : rope_backward<HALVES, TX, float>(a, s, stream);
+  else
+    a.out_bf16 ? rope_forward<HALVES, TX, uint16_t>(a, s, stream) : rope_forward<HALVES, TX, float>(a, s, stream);
 }
 
 }  // namespace
 
 int64_t rope_partial_rows(int64_t m, int heads, int d) {
-  return rope_shape(m, heads, d, ROPE_BWD_BLOCKS).blocks;
+  // (the most that any number of pairs asks for: the shape's batch goes by them)
+  int64_t most = 0;
+  for (int pairs = 0; pairs <= d / 2; pairs += 4) {
+    const int64_t b = rope_shape(m, heads, d, pairs, ROPE_BWD_BLOCKS).blocks;
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
-  const int heads = a.heads_q + a.heads_k;
-  const RopeShape s = rope_shape(a.m, heads, a.head_dim, a.backward ? ROPE_BWD_BLOCKS : ROPE_BLOCKS);
-  const dim3 grid((unsigned)s.blocks), block(ROPE_THREADS);
+  const RopeShape s = rope_shape(a.m, a.heads_q + a.heads_k, a.head_dim, a.pairs,
+                                 a.backward ? ROPE_BWD_BLOCKS : ROPE_BLOCKS);
   if (s.blocks > 0) {
-    if (a.backward) {
-      if (a.halves)
-        hipLaunchKernelGGL((k_rope<true, true>), grid, block, 0, stream, a, s.lanes, s.units);
-      else
-        hipLaunchKernelGGL((k_rope<false, true>), grid, block, 0, stream, a, s.lanes, s.units);
-    } else {
-      if (a.halves)
-        hipLaunchKernelGGL((k_rope<true, false>), grid, block, 0, stream, a, s.lanes, s.units);
-      else
-        hipLaunchKernelGGL((k_rope<false, false>), grid, block, 0, stream, a, s.lanes, s.units);
-    }
+    if (a.halves)
+      a.x_bf16 ? rope_x<true, uint16_t>(a, s, stream) : rope_x<true, float>(a, s, stream);
+    else
+      a.x_bf16 ? rope_x<false, uint16_t>(a, s, stream) : rope_x<false, float>(a, s, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
