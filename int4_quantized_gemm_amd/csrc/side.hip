@@ -578,66 +578,78 @@ __global__ __launch_bounds__(256) void k_side_dt(DtArgs t) {
   dt_block<SRC, TB, R, WR>(t, blockIdx.x, lds);
 }
 
+// dB's sums and dA's in one launch: the first nb_db blocks take dB's, the others
+// dA's (which alone do not fill the chip).
 template <typename SRC, int R>
-__global__ __launch_bounds__(256) void k_side_outer(OuterArgs o) {
+__global__ __launch_bounds__(256) void k_side_outer(OuterArgs db, OuterArgs da, unsigned nb_db) {
   __shared__ __align__(16) uint16_t lds[OuterShape<R>::LDS];
-  outer_block<SRC, R, std::is_same<SRC, SrcI8>::value>(o, blockIdx.x, lds);
+  if (blockIdx.x < nb_db)
+    outer_block<SRC, R, false>(db, blockIdx.x, lds);
+  else
+    outer_block<SrcI8, R, true>(da, blockIdx.x - nb_db, lds);
 }
 
 // --------------------------------------------------------------------- join
-// The splits of T or dT (the first nb_t blocks) and of dB added in order, four
-// ranks a thread, times alpha. T's and dT's rows are 64 long, zeros past the
-// rank; `scaled` gets them times the rows' factors, t without (either may be
-// null).
+// The sum of `splits` partial sums, `pitch` floats apart, in order: eight loads
+// in flight, the last ones clamped.
+__device__ __forceinline__ f32x4_t sum_splits(const float* p, int64_t pitch, int splits) {
+  f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+  for (int q0 = 0; q0 < splits; q0 += 8) {
+    f32x4_t w[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[q] = *reinterpret_cast<const f32x4_t*>(p + min(q0 + q, splits - 1) * pitch);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q0 + q < splits) s += w[q];
+  }
+  return s;
+}
+
+// The splits of T or dT added in order, four ranks a thread, times alpha: rows
+// of 64, zeros past the rank. `scaled` gets them times the rows' factors, t
+// without (or null).
 template <int R>
-__global__ __launch_bounds__(256) void k_side_join(const float* __restrict__ pt, int st, int64_t M,
-                                                   const float* __restrict__ rowscale, float* __restrict__ t,
-                                                   float* __restrict__ scaled,
-                                                   const float* __restrict__ pb, int sb, int64_t N,
-                                                   float* __restrict__ db, int64_t lddb, float alpha, int r,
-                                                   unsigned nb_t) {
-  const bool is_t = blockIdx.x < nb_t;
-  const int64_t e = (int64_t)(is_t ? blockIdx.x : blockIdx.x - nb_t) * 256 + threadIdx.x;
-  const int64_t row = e / (is_t ? SIDE_T / 4 : R / 4), rows = is_t ? M : N;
-  const int j = (int)(e % (is_t ? SIDE_T / 4 : R / 4)) * 4;
-  if (row >= rows) return;
-  const float* p = is_t ? pt : pb;
-  const int splits = is_t ? st : sb;
+__global__ __launch_bounds__(256) void k_side_join_t(const float* __restrict__ p, int splits, int64_t M,
+                                                     const float* __restrict__ rowscale, float alpha, int r,
+                                                     float* __restrict__ t, float* __restrict__ scaled) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, row = e / (SIDE_T / 4);
+  const int j = (int)(e % (SIDE_T / 4)) * 4;
+  if (row >= M) return;
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
   if (j < r) {
-    for (int q0 = 0; q0 < splits; q0 += 8) {  // eight loads in flight, the last ones clamped
-      f32x4_t w[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        w[q] = *reinterpret_cast<const f32x4_t*>(p + ((int64_t)min(q0 + q, splits - 1) * rows + row) * R + j);
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q0 + q < splits) s += w[q];
-    }
+    s = sum_splits(p + row * R + j, M * R, splits);
 #pragma unroll
     for (int v = 0; v < 4; ++v) s[v] = j + v < r ? s[v] * alpha : 0.f;
   }
-  if (is_t) {
-    if (t != nullptr) *reinterpret_cast<f32x4_t*>(t + row * SIDE_T + j) = s;
-    *reinterpret_cast<f32x4_t*>(scaled + row * SIDE_T + j) = s * rowscale[row];
-  } else {
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-      if (j + v < r) db[row * lddb + j + v] = s[v];
-  }
+  if (t != nullptr) *reinterpret_cast<f32x4_t*>(t + row * SIDE_T + j) = s;
+  *reinterpret_cast<f32x4_t*>(scaled + row * SIDE_T + j) = s * rowscale[row];
 }
 
-// The splits of dA [splits, R, K] added: a half wave takes every fourth split of
-// a 256-group of one rank, eight of these units a block; the four sums are
-// joined in LDS, and the first half wave of a unit rotates the group back on
-// request.
+// The splits of dB [splits, N, R] and dA [splits, R, K] added. The first nb_db
+// blocks take dB, four ranks a thread, times alpha. In the others a half wave
+// takes every fourth split of a 256-group of one rank of dA, eight of these
+// units a block; the four sums are joined in LDS, and the first half wave of a
+// unit rotates the group back on request.
 template <int R>
-__global__ __launch_bounds__(1024) void k_side_join_da(const float* __restrict__ pa, int splits, int K,
-                                                       float* __restrict__ da, int64_t ldda, int rotate, int r) {
+__global__ __launch_bounds__(1024) void k_side_join(const float* __restrict__ pb, int sb, int64_t N,
+                                                    float* __restrict__ db, int64_t lddb, float alpha,
+                                                    const float* __restrict__ pa, int splits, int K,
+                                                    float* __restrict__ da, int64_t ldda, int rotate, int r,
+                                                    unsigned nb_db) {
   __shared__ __align__(16) float sums[4][8][256];
+  if (blockIdx.x < nb_db) {
+    const int64_t e = (int64_t)blockIdx.x * 1024 + threadIdx.x, row = e / (R / 4);
+    const int j = (int)(e % (R / 4)) * 4;
+    if (row >= N || j >= r) return;
+    const f32x4_t s = sum_splits(pb + row * R + j, N * R, sb);
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (j + v < r) db[row * lddb + j + v] = s[v] * alpha;
+    return;
+  }
   const int lane32 = threadIdx.x & 31, i = (threadIdx.x >> 5) & 7, part = threadIdx.x >> 8;
   const int groups = K / 256, units = r * groups;
-  const int unit = (int)blockIdx.x * 8 + i;
+  const int unit = (int)(blockIdx.x - nb_db) * 8 + i;
   const int j = unit / groups, c = (unit - j * groups) * 256 + lane32 * 8;
   float v[8];
 #pragma unroll
@@ -745,45 +757,52 @@ DownPlan down_plan(int64_t m, int64_t k, int64_t r) {
 }
 
 template <typename SRC, typename TB, int R>
-hipError_t dy_launch(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) {
-  DtArgs t{a.dy, a.lddy, a.b, a.ldb, a.m, a.n, a.r, p.s1, p.cps1, a.ws};
-  OuterArgs o{a.dy, a.lddy, a.n, a.t, a.m, a.r, p.s2, p.cps2, p.nmc, a.ws + p.off2};
+hipError_t dt_launch(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) {
+  const DtArgs t{a.dy, a.lddy, a.b, a.ldb, a.m, a.n, a.r, p.s1, p.cps1, a.ws};
   const dim3 grid((unsigned)(p.rb * p.s1)), block(256);
   if (p.wr == 4)
     hipLaunchKernelGGL((k_side_dt<SRC, TB, R, 4>), grid, block, 0, stream, t);
   else
     hipLaunchKernelGGL((k_side_dt<SRC, TB, R, 1>), grid, block, 0, stream, t);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_side_outer<SRC, R>), dim3((unsigned)(p.cb2 * p.s2 * OuterShape<R>::HALVES)), block, 0, stream, o);
+  return hipGetLastError();
+}
+
+template <int R>
+hipError_t join_t_launch(const float* part, int splits, int64_t m, const float* sa, float alpha, int r, float* t,
+                         float* scaled, hipStream_t stream) {
+  hipLaunchKernelGGL((k_side_join_t<R>), dim3((unsigned)((m * (SIDE_T / 4) + 255) / 256)), dim3(256), 0, stream, part,
+                     splits, m, sa, alpha, r, t, scaled);
   return hipGetLastError();
 }
 
 template <int R>
 hipError_t grad_r(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) {
   hipError_t e = hipSuccess;
-  const dim3 block(256);
-  if (a.m > 0 && a.n > 0) {
-    if (a.dy_bf16)
-      e = a.b_bf16 ? dy_launch<SrcBf16, uint16_t, R>(a, p, stream) : dy_launch<SrcBf16, float, R>(a, p, stream);
-    else
-      e = a.b_bf16 ? dy_launch<SrcF32, uint16_t, R>(a, p, stream) : dy_launch<SrcF32, float, R>(a, p, stream);
-    if (e != hipSuccess) return e;
-  }
-  const int64_t nb_dt = (a.m * (SIDE_T / 4) + 255) / 256, nb_db = (a.n * (R / 4) + 255) / 256;
-  if (nb_dt + nb_db > 0) {
-    hipLaunchKernelGGL((k_side_join<R>), dim3((unsigned)(nb_dt + nb_db)), block, 0, stream, a.ws, p.s1 * p.wn, a.m,
-                       a.sa, a.dt, a.ws + p.off4, a.ws + p.off2, p.s2, a.n, a.db, a.lddb, a.alpha, a.r, (unsigned)nb_dt);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
   if (a.m > 0) {
-    const OuterArgs o{a.qa, a.ldqa, a.k, a.ws + p.off4, a.m, a.r, p.s3, p.cps3, p.nmc, a.ws + p.off3};
-    hipLaunchKernelGGL((k_side_outer<SrcI8, R>), dim3((unsigned)(p.cb3 * p.s3 * OuterShape<R>::HALVES)), block, 0, stream, o);
+    if (a.n > 0) {
+      if (a.dy_bf16)
+        e = a.b_bf16 ? dt_launch<SrcBf16, uint16_t, R>(a, p, stream) : dt_launch<SrcBf16, float, R>(a, p, stream);
+      else
+        e = a.b_bf16 ? dt_launch<SrcF32, uint16_t, R>(a, p, stream) : dt_launch<SrcF32, float, R>(a, p, stream);
+      if (e != hipSuccess) return e;
+    }
+    float* scaled = a.ws + p.off4;
+    e = join_t_launch<R>(a.ws, p.s1 * p.wn, a.m, a.sa, a.alpha, a.r, a.dt, scaled, stream);
+    if (e != hipSuccess) return e;
+    const OuterArgs db{a.dy, a.lddy, a.n, a.t, a.m, a.r, p.s2, p.cps2, p.nmc, a.ws + p.off2};
+    const OuterArgs da{a.qa, a.ldqa, a.k, scaled, a.m, a.r, p.s3, p.cps3, p.nmc, a.ws + p.off3};
+    const unsigned nb_db = (unsigned)(p.cb2 * p.s2 * OuterShape<R>::HALVES);
+    const dim3 grid(nb_db + (unsigned)(p.cb3 * p.s3 * OuterShape<R>::HALVES)), block(256);
+    if (a.dy_bf16)
+      hipLaunchKernelGGL((k_side_outer<SrcBf16, R>), grid, block, 0, stream, db, da, nb_db);
+    else
+      hipLaunchKernelGGL((k_side_outer<SrcF32, R>), grid, block, 0, stream, db, da, nb_db);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const int64_t nb_da = ((int64_t)a.r * (a.k / 256) + 7) / 8;
-  hipLaunchKernelGGL((k_side_join_da<R>), dim3((unsigned)nb_da), dim3(1024), 0, stream, a.ws + p.off3, p.s3, (int)a.k, a.da,
-                     a.ldda, a.rotate, a.r);
+  const unsigned nb_db = (unsigned)((a.n * (R / 4) + 1023) / 1024);
+  const unsigned nb_da = (unsigned)(((int64_t)a.r * (a.k / 256) + 7) / 8);
+  hipLaunchKernelGGL((k_side_join<R>), dim3(nb_db + nb_da), dim3(1024), 0, stream, a.ws + p.off2, p.s2, a.n, a.db,
+                     a.lddb, a.alpha, a.ws + p.off3, p.s3, (int)a.k, a.da, a.ldda, a.rotate, a.r, nb_db);
   return hipGetLastError();
 }
 
@@ -800,10 +819,7 @@ hipError_t down_r(const SideDownArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((k_side_down<TA, R, 4, 2>), grid, block, 0, stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const unsigned nb = (unsigned)((a.m * (SIDE_T / 4) + 255) / 256);
-  hipLaunchKernelGGL((k_side_join<R>), dim3(nb), block, 0, stream, a.ws, p.s * p.wn, a.m, a.sa,
-                     (float*)nullptr, a.t, (const float*)nullptr, 0, (int64_t)0, (float*)nullptr, (int64_t)0, 1.f, a.r, nb);
-  return hipGetLastError();
+  return join_t_launch<R>(a.ws, p.s * p.wn, a.m, a.sa, 1.f, a.r, nullptr, a.t, stream);
 }
 
 template <typename TA>
