@@ -24,73 +24,80 @@ _DTYPE = {torch.float32: _lib.TP_F32, torch.bfloat16: _lib.TP_BF16}
 _KIND = {"i8": (TP_NORM_OUT_I8, torch.int8), "bf16": (TP_NORM_OUT_BF16, torch.bfloat16)}
 
 
-# A call on a handful of rows takes less time on the GPU than in Python, so the
-# checks below take the short way where everything is in order.
+# A call on a handful of rows takes less time on the GPU than in Python (a
+# single token's rope: 4 us against 10), so the checks below take the short way
+# where everything is in order, and what a call allocates itself is not checked.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_empty = torch.empty_strided
 
 
 def _dt(t, name):
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)")
+    return code
+
+
+def _device(first, names, others):
+    """The index of the one CUDA (HIP) device of a call's tensors (None: not
+    given); names are the others', for the message."""
     try:
-        return _DTYPE[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)") from None
+        index = first.get_device()
+        for t in others:
+            if t is not None and t.get_device() != index:
+                index = -1
+    except AttributeError:
+        index = -1
+    if index < 0:
+        _device_error(first, names.split(), others)
+    return index
 
 
-def _device(first, names, *others):
-    """The one CUDA (HIP) device of a call's tensors (None: not given); names
-    are the others', for the message."""
+def _device_error(first, names, others):
     if not isinstance(first, torch.Tensor) or not first.is_cuda:
         raise ValueError("the operands must be CUDA (HIP) tensors")
-    device = first.device
-    for i, t in enumerate(others):
-        if t is not None and (not isinstance(t, torch.Tensor) or t.device != device):
-            raise ValueError(f"{names.split()[i]} must be a tensor on {device}")
-    return device
+    for name, t in zip(names, others):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.device != first.device):
+            raise ValueError(f"{name} must be a tensor on {first.device}")
+    raise ValueError("the operands must be CUDA (HIP) tensors of one device")
 
 
-def _elsewhere(device, stream):
+def _elsewhere(index, stream):
     """The context a call has to move into: that of an explicit stream, or of
     a device other than the current one; None where the call already is."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the operands on cuda:{index}")
         return torch.cuda.stream(stream)
-    if device.index != _current_device():
-        return torch.cuda.device(device)
+    if index != _current_device():
+        return torch.cuda.device(index)
     return None
 
 
-def _raw_stream(device):
+def _raw_stream(index):
     if _raw_stream_of is not None:
-        return _raw_stream_of(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream_of(index)
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-def _new(m, k, dtype, device):
-    return torch.empty_strided((m, k), (k, 1), dtype=dtype, device=device)
-
-
-def _new_vec(n, dtype, device):
-    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
-
-
-def _mat(t, name, shape=None, dtype=None):
-    """Checks a 2-D row-major matrix; returns its row pitch in elements (any
-    pitch describes a single row: the shortest that the C boundary takes)."""
+def _mat(t, name, rows=None, cols=None, dtype=None):
+    """Checks a 2-D row-major matrix (None: any); returns its row pitch in
+    elements (any pitch describes a single row: the shortest that the C
+    boundary takes)."""
     size = t.shape
-    if len(size) != 2 or (shape is not None and size != shape):
-        raise ValueError(f"{name} must be {'2-D' if shape is None else tuple(shape)}, got shape {tuple(size)}")
+    if len(size) != 2 or (rows is not None and size[0] != rows) or (cols is not None and size[1] != cols):
+        want = f"[{'any' if rows is None else rows}, {'any' if cols is None else cols}]"
+        raise ValueError(f"{name} must have shape {want}, got {tuple(size)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    rows, cols = size
     pitch, unit = t.stride()
-    if unit != 1 and cols > 1:
+    if unit != 1 and size[1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    if rows > 1:
+    if size[0] > 1:
         return pitch
     per = 16 // t.element_size()
-    return -(-cols // per) * per
+    return -(-size[1] // per) * per
 
 
 def _vec(t, name, count, dtype=None):
@@ -106,7 +113,7 @@ def _vec(t, name, count, dtype=None):
 def _weight(t, name, count):
     """Pointer and dtype code of an optional weight vector."""
     if t is None:
-        return None, _lib.TP_F32
+        return None, 0
     return _vec(t, name, count).data_ptr(), _dt(t, name)
 
 
@@ -114,7 +121,7 @@ def _scratch(workspace, need, device):
     """Pointer and size of the caller's scratch tensor, or of a new one (kept
     alive by the third value until the launch)."""
     if workspace is None:
-        workspace = _new_vec(max(need, 16), torch.uint8, device)
+        workspace = _empty((need or 16,), (1,), dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -129,8 +136,8 @@ def tp_rmsnorm_rotate(x, gamma=None, eps=1e-6, residual=None, rotate=True, out_k
     ("bf16"). Returns (codes, scales) or rows; with a residual also t, the new
     stream: (codes, scales, t) or (rows, t). sum_out may be residual (or x)
     itself."""
-    dev = _device(x, "gamma residual out scales sum_out", gamma, residual, out, scales, sum_out)
-    scope = _elsewhere(dev, stream)
+    index = _device(x, "gamma residual out scales sum_out", (gamma, residual, out, scales, sum_out))
+    scope = _elsewhere(index, stream)
     if scope is not None:
         with scope:
             return tp_rmsnorm_rotate(x, gamma, eps, residual, rotate, out_kind, out, scales, sum_out)
@@ -139,40 +146,43 @@ def tp_rmsnorm_rotate(x, gamma=None, eps=1e-6, residual=None, rotate=True, out_k
     kind, y_dtype = _KIND[out_kind]
     ldx = _mat(x, "x")
     m, k = x.shape
+    device = x.device
     g_ptr, g_dt = _weight(gamma, "gamma", k)
-    r_ptr = s_ptr = None
+    r_ptr = s_ptr = sc_ptr = None
     ldr = lds = s_dt = 0
     if residual is not None:
-        ldr = _mat(residual, "residual", (m, k))
+        ldr = _mat(residual, "residual", m, k)
         s_dt = _dt(residual, "residual")
         if sum_out is None:
-            sum_out = _new(m, k, residual.dtype, dev)
-        lds = _mat(sum_out, "sum_out", (m, k), residual.dtype)
+            sum_out, lds = _empty((m, k), (k, 1), dtype=residual.dtype, device=device), k
+        else:
+            lds = _mat(sum_out, "sum_out", m, k, residual.dtype)
         r_ptr, s_ptr = residual.data_ptr(), sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if out is None:
-        out = _new(m, k, y_dtype, dev)
-    ldy = _mat(out, "out", (m, k), y_dtype)
-    sc_ptr = None
+        out, ldy = _empty((m, k), (k, 1), dtype=y_dtype, device=device), k
+    else:
+        ldy = _mat(out, "out", m, k, y_dtype)
     if kind == TP_NORM_OUT_I8:
         if scales is None:
-            scales = _new_vec(m, torch.float32, dev)
-        sc_ptr = _vec(scales, "scales", m, torch.float32).data_ptr()
+            scales = _empty((m,), (1,), dtype=torch.float32, device=device)
+        else:
+            _vec(scales, "scales", m, torch.float32)
+        sc_ptr = scales.data_ptr()
     elif scales is not None:
         raise ValueError("scales belong to out_kind 'i8'")
     _lib.check(_lib.load().tp_rmsnorm_rotate(
         x.data_ptr(), _dt(x, "x"), ldx, r_ptr, ldr, s_ptr, lds, s_dt, g_ptr, g_dt, eps,
-        TP_A_ROTATE if rotate else TP_A_PREROTATED, m, k, kind, out.data_ptr(), ldy, sc_ptr, _raw_stream(dev)))
-    got = (out, scales) if kind == TP_NORM_OUT_I8 else (out,)
-    if residual is not None:
-        got += (sum_out,)
-    return got if len(got) > 1 else out
+        TP_A_ROTATE if rotate else TP_A_PREROTATED, m, k, kind, out.data_ptr(), ldy, sc_ptr, _raw_stream(index)))
+    if kind == TP_NORM_OUT_I8:
+        return (out, scales) if residual is None else (out, scales, sum_out)
+    return out if residual is None else (out, sum_out)
 
 
 def tp_rmsnorm_backward_workspace_size(m, k):
     """Bytes of workspace tp_rmsnorm_rotate_backward needs for dgamma."""
-    return int(_lib.load().tp_rmsnorm_backward_workspace_size(m, k))
+    return _lib.load().tp_rmsnorm_backward_workspace_size(m, k)
 
 
 def tp_rmsnorm_rotate_backward(dy, t, gamma=None, eps=1e-6, dsum=None, rotate=True, dx_dtype=None, want_dgamma=True,
@@ -182,34 +192,38 @@ def tp_rmsnorm_rotate_backward(dy, t, gamma=None, eps=1e-6, dsum=None, rotate=Tr
     x), dsum the gradient that reaches the stream from behind. Returns
     (dx, dgamma); dgamma is None where it is not wanted. dx (default dtype:
     dsum's, else t's) may be dsum or dy itself."""
-    dev = _device(dy, "t gamma dsum dx dgamma workspace", t, gamma, dsum, dx, dgamma, workspace)
-    scope = _elsewhere(dev, stream)
+    index = _device(dy, "t gamma dsum dx dgamma workspace", (t, gamma, dsum, dx, dgamma, workspace))
+    scope = _elsewhere(index, stream)
     if scope is not None:
         with scope:
             return tp_rmsnorm_rotate_backward(dy, t, gamma, eps, dsum, rotate, dx_dtype, want_dgamma, dx, dgamma,
                                               workspace)
     lddy = _mat(dy, "dy")
     m, k = dy.shape
-    ldt = _mat(t, "t", (m, k))
+    device = dy.device
+    ldt = _mat(t, "t", m, k)
     g_ptr, g_dt = _weight(gamma, "gamma", k)
     if dx is None:
-        dx = _new(m, k, dx_dtype or (t if dsum is None else dsum).dtype, dev)
-    elif dx_dtype is not None and dx.dtype != dx_dtype:
-        raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
-    lddx = _mat(dx, "dx", (m, k))
-    ldds = 0 if dsum is None else _mat(dsum, "dsum", (m, k), dx.dtype)
-    want = want_dgamma or dgamma is not None
+        dx = _empty((m, k), (k, 1), dtype=dx_dtype or (t if dsum is None else dsum).dtype, device=device)
+        lddx = k
+    else:
+        lddx = _mat(dx, "dx", m, k, dx_dtype)
+    ds_ptr, ldds = None, 0
+    if dsum is not None:
+        ds_ptr, ldds = dsum.data_ptr(), _mat(dsum, "dsum", m, k, dx.dtype)
     dg_ptr = ws_ptr = ws = None
     ws_bytes = 0
-    if want:
+    if want_dgamma or dgamma is not None:
         if dgamma is None:
-            dgamma = _new_vec(k, torch.float32, dev)
-        dg_ptr = _vec(dgamma, "dgamma", k, torch.float32).data_ptr()
-        ws_ptr, ws_bytes, ws = _scratch(workspace, tp_rmsnorm_backward_workspace_size(m, k), dev)
+            dgamma = _empty((k,), (1,), dtype=torch.float32, device=device)
+        else:
+            _vec(dgamma, "dgamma", k, torch.float32)
+        dg_ptr = dgamma.data_ptr()
+        ws_ptr, ws_bytes, ws = _scratch(workspace, tp_rmsnorm_backward_workspace_size(m, k), device)
     _lib.check(_lib.load().tp_rmsnorm_rotate_backward(
         dy.data_ptr(), _dt(dy, "dy"), lddy, TP_A_ROTATE if rotate else TP_A_PREROTATED, t.data_ptr(), _dt(t, "t"),
-        ldt, g_ptr, g_dt, eps, None if dsum is None else dsum.data_ptr(), ldds, m, k, dx.data_ptr(), _dt(dx, "dx"),
-        lddx, dg_ptr, ws_ptr, ws_bytes, _raw_stream(dev)))
+        ldt, g_ptr, g_dt, eps, ds_ptr, ldds, m, k, dx.data_ptr(), _dt(dx, "dx"), lddx, dg_ptr, ws_ptr, ws_bytes,
+        _raw_stream(index)))
     return dx, dgamma
 
 
@@ -218,45 +232,44 @@ _T = 64  # floats of a row of T and dT
 
 def tp_lora_down_prequantized_workspace_size(m, k, r):
     """Bytes of workspace tp_lora_down_prequantized needs."""
-    return int(_lib.load().tp_lora_down_prequantized_workspace_size(m, k, r))
+    return _lib.load().tp_lora_down_prequantized_workspace_size(m, k, r)
+
+
+def _t_rows(t, name, m, device):
+    """fp32 [m, 64] contiguous, allocated where it is not given."""
+    if t is None:
+        return _empty((m, _T), (_T, 1), dtype=torch.float32, device=device)
+    if _mat(t, name, m, _T, torch.float32) != _T:
+        raise ValueError(f"{name} must be contiguous")
+    return t
 
 
 def tp_lora_down_prequantized(qa, sa, lora_a, t=None, workspace=None, stream=None):
     """T = sa (qa . lora_a^T) in fp32 rows of 64 (zeros past r): the first half
     of the side path on activations held as int8 codes and scales; lora_a
     [r, k] in the codes' domain. Returns T [m, 64], as tp_lora_down does."""
-    dev = _device(qa, "sa lora_a t workspace", sa, lora_a, t, workspace)
-    scope = _elsewhere(dev, stream)
+    index = _device(qa, "sa lora_a t workspace", (sa, lora_a, t, workspace))
+    scope = _elsewhere(index, stream)
     if scope is not None:
         with scope:
             return tp_lora_down_prequantized(qa, sa, lora_a, t, workspace)
     ldqa = _mat(qa, "qa", dtype=torch.int8)
     m, k = qa.shape
+    device = qa.device
     _vec(sa, "sa", m, torch.float32)
-    lda = _mat(lora_a, "lora_a")
+    lda = _mat(lora_a, "lora_a", cols=k)
     r = lora_a.shape[0]
-    if lora_a.shape[1] != k:
-        raise ValueError(f"lora_a must be [r, {k}], got shape {tuple(lora_a.shape)}")
-    t = _t_rows(t, "t", m, dev)
-    ws_ptr, ws_bytes, ws = _scratch(workspace, tp_lora_down_prequantized_workspace_size(m, k, r), dev)
-    _lib.check(_lib.load().tp_lora_down_prequantized(qa.data_ptr(), ldqa, sa.data_ptr(), lora_a.data_ptr(),
-                                                     _dt(lora_a, "lora_a"), lda, m, k, r, t.data_ptr(),
-                                                     m * _T * 4, ws_ptr, ws_bytes, _raw_stream(dev)))
-    return t
-
-
-def _t_rows(t, name, m, device):
-    """fp32 [m, 64] contiguous, allocated where it is not given."""
-    if t is None:
-        return _new(m, _T, torch.float32, device)
-    if _mat(t, name, (m, _T), torch.float32) != _T:
-        raise ValueError(f"{name} must be contiguous")
+    t = _t_rows(t, "t", m, device)
+    ws_ptr, ws_bytes, ws = _scratch(workspace, tp_lora_down_prequantized_workspace_size(m, k, r), device)
+    _lib.check(_lib.load().tp_lora_down_prequantized(
+        qa.data_ptr(), ldqa, sa.data_ptr(), lora_a.data_ptr(), _dt(lora_a, "lora_a"), lda, m, k, r, t.data_ptr(),
+        m * _T * 4, ws_ptr, ws_bytes, _raw_stream(index)))
     return t
 
 
 def tp_lora_grad_workspace_size(m, n, k, r):
     """Bytes of workspace tp_lora_grad_prequantized needs."""
-    return int(_lib.load().tp_lora_grad_workspace_size(m, n, k, r))
+    return _lib.load().tp_lora_grad_workspace_size(m, n, k, r)
 
 
 def tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha, rotate=False, da=None, db=None, dt=None, workspace=None,
@@ -266,37 +279,37 @@ def tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha, rotate=False, da=Non
     dy^T T, alpha dy . lora_b), fp32. dA is in the codes' domain, or with
     rotate=True rotated back (the gradient of an un-rotated lora_a); dT [m, 64]
     gives dx = dT . lora_a."""
-    dev = _device(dy, "qa sa t lora_b da db dt workspace", qa, sa, t, lora_b, da, db, dt, workspace)
-    scope = _elsewhere(dev, stream)
+    index = _device(dy, "qa sa t lora_b da db dt workspace", (qa, sa, t, lora_b, da, db, dt, workspace))
+    scope = _elsewhere(index, stream)
     if scope is not None:
         with scope:
             return tp_lora_grad_prequantized(dy, qa, sa, t, lora_b, alpha, rotate, da, db, dt, workspace)
     lddy = _mat(dy, "dy")
     m, n = dy.shape
-    ldqa = _mat(qa, "qa", dtype=torch.int8)
+    device = dy.device
+    ldqa = _mat(qa, "qa", m, dtype=torch.int8)
     k = qa.shape[1]
-    if qa.shape[0] != m:
-        raise ValueError(f"qa must have {m} rows, got shape {tuple(qa.shape)}")
     _vec(sa, "sa", m, torch.float32)
     if t is None:
         raise ValueError("t (the forward's T) is needed")
-    t = _t_rows(t, "t", m, dev)
-    ldb = _mat(lora_b, "lora_b")
+    _t_rows(t, "t", m, device)
+    ldb = _mat(lora_b, "lora_b", n)
     r = lora_b.shape[1]
-    if lora_b.shape[0] != n:
-        raise ValueError(f"lora_b must be [{n}, r], got shape {tuple(lora_b.shape)}")
-    dt = _t_rows(dt, "dt", m, dev)
+    dt = _t_rows(dt, "dt", m, device)
+    ldda, lddb = k, r
     if da is None:
-        da = _new(r, k, torch.float32, dev)
-    ldda = _mat(da, "da", (r, k), torch.float32)
+        da = _empty((r, k), (k, 1), dtype=torch.float32, device=device)
+    else:
+        ldda = _mat(da, "da", r, k, torch.float32)
     if db is None:
-        db = _new(n, r, torch.float32, dev)
-    lddb = _mat(db, "db", (n, r), torch.float32)
-    ws_ptr, ws_bytes, ws = _scratch(workspace, tp_lora_grad_workspace_size(m, n, k, r), dev)
+        db = _empty((n, r), (r, 1), dtype=torch.float32, device=device)
+    else:
+        lddb = _mat(db, "db", n, r, torch.float32)
+    ws_ptr, ws_bytes, ws = _scratch(workspace, tp_lora_grad_workspace_size(m, n, k, r), device)
     _lib.check(_lib.load().tp_lora_grad_prequantized(
         dy.data_ptr(), _dt(dy, "dy"), lddy, qa.data_ptr(), ldqa, sa.data_ptr(), t.data_ptr(), lora_b.data_ptr(),
-        _dt(lora_b, "lora_b"), ldb, float(alpha), TP_A_ROTATE if rotate else TP_A_PREROTATED, m, n, k, r,
-        dt.data_ptr(), da.data_ptr(), ldda, db.data_ptr(), lddb, ws_ptr, ws_bytes, _raw_stream(dev)))
+        _dt(lora_b, "lora_b"), ldb, alpha, TP_A_ROTATE if rotate else TP_A_PREROTATED, m, n, k, r, dt.data_ptr(),
+        da.data_ptr(), ldda, db.data_ptr(), lddb, ws_ptr, ws_bytes, _raw_stream(index)))
     return da, db, dt
 
 
@@ -304,11 +317,12 @@ _LAYOUT = {"interleaved": TP_ROPE_INTERLEAVED, "halves": TP_ROPE_HALVES}
 
 
 def _heads(t, name, m, head_dim, dtype=None):
-    """Row pitch and head count of a [m, heads * head_dim] matrix."""
-    ld = _mat(t, name, dtype=dtype)
-    if t.shape[0] != m or t.shape[1] % head_dim != 0:
-        raise ValueError(f"{name} must be [{m}, heads * {head_dim}], got shape {tuple(t.shape)}")
-    return ld, t.shape[1] // head_dim
+    """Row pitch, width and head count of a [m, heads * head_dim] matrix."""
+    ld = _mat(t, name, m, dtype=dtype)
+    width = t.shape[1]
+    if width % head_dim != 0:
+        raise ValueError(f"{name} must have a multiple of {head_dim} columns, got shape {tuple(t.shape)}")
+    return ld, width, width // head_dim
 
 
 def _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps):
@@ -317,27 +331,24 @@ def _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_g
         raise ValueError("layout must be 'interleaved' or 'halves'")
     qg, g_dt = _weight(q_gamma, "q_gamma", head_dim)
     kg, k_dt = _weight(k_gamma, "k_gamma", head_dim)
-    if q_gamma is not None and k_gamma is not None and g_dt != k_dt:
-        raise TypeError("q_gamma and k_gamma must have one dtype")
-    if q_gamma is None:
+    if qg is None:
         g_dt = k_dt
+    elif kg is not None and g_dt != k_dt:
+        raise TypeError("q_gamma and k_gamma must have one dtype")
     pairs = 0 if inv_freq is None else inv_freq.shape[0]
-    axes, ldpos, pos_ptr, freq_ptr, axis = 1, 0, None, None, None
-    if pairs:
-        if positions is None:
-            raise ValueError("positions are needed")
-        if positions.dim() == 1:
-            positions = positions[:, None]
-        ldpos = _mat(positions, "positions", dtype=torch.int32)
-        if positions.shape[0] != m:
-            raise ValueError(f"positions must have {m} rows, got shape {tuple(positions.shape)}")
-        axes = positions.shape[1]
-        pos_ptr = positions.data_ptr()
-        freq_ptr = _vec(inv_freq, "inv_freq", pairs, torch.float32).data_ptr()
-        axis = bytes(pairs) if pair_axis is None else pair_axis if type(pair_axis) is bytes else bytes(pair_axis)
-        if len(axis) != pairs:
-            raise ValueError(f"pair_axis must have {pairs} entries, got {len(axis)}")
-    return (qg, kg, g_dt, eps, pos_ptr, ldpos, axes, freq_ptr, axis, pairs, _LAYOUT[layout])
+    if pairs == 0:
+        return qg, kg, g_dt, eps, None, 0, 1, None, None, 0, _LAYOUT[layout]
+    if positions is None:
+        raise ValueError("positions are needed")
+    if positions.dim() == 1:
+        positions = positions[:, None]
+    ldpos = _mat(positions, "positions", m, dtype=torch.int32)
+    _vec(inv_freq, "inv_freq", pairs, torch.float32)
+    axis = pair_axis if type(pair_axis) is bytes else bytes(pairs) if pair_axis is None else bytes(pair_axis)
+    if len(axis) != pairs:
+        raise ValueError(f"pair_axis must have {pairs} entries, got {len(axis)}")
+    return (qg, kg, g_dt, eps, positions.data_ptr(), ldpos, positions.shape[1], inv_freq.data_ptr(), axis, pairs,
+            _LAYOUT[layout])
 
 
 def tp_qk_norm_rope(q, k, head_dim, positions=None, inv_freq=None, pair_axis=None, layout="interleaved", q_gamma=None,
@@ -349,34 +360,46 @@ def tp_qk_norm_rope(q, k, head_dim, positions=None, inv_freq=None, pair_axis=Non
     layout "interleaved" (pairs of neighbours) or "halves". Columns past the
     rotated ones are passed on. Returns (q_out, k_out), which may be the inputs
     themselves; default dtype: the inputs'."""
-    dev = _device(q, "k positions inv_freq q_gamma k_gamma q_out k_out", k, positions, inv_freq, q_gamma, k_gamma,
-                  q_out, k_out)
-    scope = _elsewhere(dev, stream)
+    index = _device(q, "k positions inv_freq q_gamma k_gamma q_out k_out",
+                    (k, positions, inv_freq, q_gamma, k_gamma, q_out, k_out))
+    scope = _elsewhere(index, stream)
     if scope is not None:
         with scope:
             return tp_qk_norm_rope(q, k, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps,
                                    out_dtype, q_out, k_out)
-    m = q.shape[0]
-    ldq, hq = _heads(q, "q", m, head_dim)
-    ldk, hk = _heads(k, "k", m, head_dim, q.dtype)
+    m, x_dtype, device = q.shape[0], q.dtype, q.device
+    ldq, wq, hq = _heads(q, "q", m, head_dim)
+    ldk, wk, hk = _heads(k, "k", m, head_dim, x_dtype)
     shared = _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps)
     if out_dtype is None:
-        out_dtype = q.dtype if q_out is None else q_out.dtype
+        out_dtype = x_dtype if q_out is None else q_out.dtype
+    ldqo, ldko = wq, wk
     if q_out is None:
-        q_out = _new(m, hq * head_dim, out_dtype, dev)
+        q_out = _empty((m, wq), (wq, 1), dtype=out_dtype, device=device)
+    else:
+        ldqo = _mat(q_out, "q_out", m, wq, out_dtype)
     if k_out is None:
-        k_out = _new(m, hk * head_dim, out_dtype, dev)
-    ldqo = _mat(q_out, "q_out", q.shape, out_dtype)
-    ldko = _mat(k_out, "k_out", k.shape, out_dtype)
+        k_out = _empty((m, wk), (wk, 1), dtype=out_dtype, device=device)
+    else:
+        ldko = _mat(k_out, "k_out", m, wk, out_dtype)
     _lib.check(_lib.load().tp_qk_norm_rope(
         q.data_ptr(), ldq, k.data_ptr(), ldk, _dt(q, "q"), m, hq, hk, head_dim, *shared, q_out.data_ptr(), ldqo,
-        k_out.data_ptr(), ldko, _dt(q_out, "q_out"), _raw_stream(dev)))
+        k_out.data_ptr(), ldko, _dt(q_out, "q_out"), _raw_stream(index)))
     return q_out, k_out
 
 
 def tp_qk_norm_rope_workspace_size(m, heads_q, heads_k, head_dim):
     """Bytes of workspace tp_qk_norm_rope_backward needs for the weights' gradients."""
-    return int(_lib.load().tp_qk_norm_rope_workspace_size(m, heads_q, heads_k, head_dim))
+    return _lib.load().tp_qk_norm_rope_workspace_size(m, heads_q, heads_k, head_dim)
+
+
+def _normed(x, gamma, like, name):
+    """Pointer, pitch and dtype code of a normed tensor's input."""
+    if gamma is None:
+        return None, 0, None
+    if x is None:
+        raise ValueError(f"{name} is needed for the gradient of its norm")
+    return x.data_ptr(), _mat(x, name, like.shape[0], like.shape[1]), _dt(x, name)
 
 
 def tp_qk_norm_rope_backward(dq_out, dk_out, q, k, head_dim, positions=None, inv_freq=None, pair_axis=None,
@@ -387,50 +410,55 @@ def tp_qk_norm_rope_backward(dq_out, dk_out, q, k, head_dim, positions=None, inv
     None for a tensor without a norm or where want_dgamma is False. q and k (the
     forward's inputs) may be None for a tensor without a norm. Default dtype of
     dq and dk: dq_out's."""
-    dev = _device(dq_out, "dk_out q k positions inv_freq q_gamma k_gamma dq dk dq_gamma dk_gamma workspace", dk_out,
-                  q, k, positions, inv_freq, q_gamma, k_gamma, dq, dk, dq_gamma, dk_gamma, workspace)
-    scope = _elsewhere(dev, stream)
+    index = _device(dq_out, "dk_out q k positions inv_freq q_gamma k_gamma dq dk dq_gamma dk_gamma workspace",
+                    (dk_out, q, k, positions, inv_freq, q_gamma, k_gamma, dq, dk, dq_gamma, dk_gamma, workspace))
+    scope = _elsewhere(index, stream)
     if scope is not None:
         with scope:
             return tp_qk_norm_rope_backward(dq_out, dk_out, q, k, head_dim, positions, inv_freq, pair_axis, layout,
                                             q_gamma, k_gamma, eps, dx_dtype, want_dgamma, dq, dk, dq_gamma, dk_gamma,
                                             workspace)
-    m = dq_out.shape[0]
-    lddqo, hq = _heads(dq_out, "dq_out", m, head_dim)
-    lddko, hk = _heads(dk_out, "dk_out", m, head_dim, dq_out.dtype)
+    m, y_dtype, device = dq_out.shape[0], dq_out.dtype, dq_out.device
+    lddqo, wq, hq = _heads(dq_out, "dq_out", m, head_dim)
+    lddko, wk, hk = _heads(dk_out, "dk_out", m, head_dim, y_dtype)
     shared = _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps)
-    x_ptr, x_ld, x_dt = [None, None], [0, 0], None
-    for i, (x, gamma, like, name) in enumerate(((q, q_gamma, dq_out, "q"), (k, k_gamma, dk_out, "k"))):
-        if gamma is None:
-            continue
-        if x is None:
-            raise ValueError(f"{name} is needed for the gradient of its norm")
-        x_ld[i] = _mat(x, name, like.shape)
-        if x_dt is not None and _dt(x, name) != x_dt:
-            raise TypeError("q and k must have one dtype")
-        x_ptr[i], x_dt = x.data_ptr(), _dt(x, name)
+    q_ptr, ldq, q_dt = _normed(q, q_gamma, dq_out, "q")
+    k_ptr, ldk, k_dt = _normed(k, k_gamma, dk_out, "k")
+    if q_dt is None:
+        q_dt = k_dt
+    elif k_dt is not None and q_dt != k_dt:
+        raise TypeError("q and k must have one dtype")
     if dx_dtype is None:
-        dx_dtype = dq_out.dtype if dq is None else dq.dtype
+        dx_dtype = y_dtype if dq is None else dq.dtype
+    lddq, lddk = wq, wk
     if dq is None:
-        dq = _new(m, hq * head_dim, dx_dtype, dev)
+        dq = _empty((m, wq), (wq, 1), dtype=dx_dtype, device=device)
+    else:
+        lddq = _mat(dq, "dq", m, wq, dx_dtype)
     if dk is None:
-        dk = _new(m, hk * head_dim, dx_dtype, dev)
-    lddq = _mat(dq, "dq", dq_out.shape, dx_dtype)
-    lddk = _mat(dk, "dk", dk_out.shape, dx_dtype)
-    if q_gamma is None and dq_gamma is not None or k_gamma is None and dk_gamma is not None:
+        dk = _empty((m, wk), (wk, 1), dtype=dx_dtype, device=device)
+    else:
+        lddk = _mat(dk, "dk", m, wk, dx_dtype)
+    if (q_gamma is None and dq_gamma is not None) or (k_gamma is None and dk_gamma is not None):
         raise ValueError("the gradient of a weight that is not given")
-    if want_dgamma and q_gamma is not None and dq_gamma is None:
-        dq_gamma = _new_vec(head_dim, torch.float32, dev)
-    if want_dgamma and k_gamma is not None and dk_gamma is None:
-        dk_gamma = _new_vec(head_dim, torch.float32, dev)
-    dg_ptr = [None if t is None else _vec(t, n, head_dim, torch.float32).data_ptr()
-              for t, n in ((dq_gamma, "dq_gamma"), (dk_gamma, "dk_gamma"))]
-    ws_ptr = ws = None
+    dqg_ptr = dkg_ptr = ws_ptr = ws = None
     ws_bytes = 0
+    if q_gamma is not None and (want_dgamma or dq_gamma is not None):
+        if dq_gamma is None:
+            dq_gamma = _empty((head_dim,), (1,), dtype=torch.float32, device=device)
+        else:
+            _vec(dq_gamma, "dq_gamma", head_dim, torch.float32)
+        dqg_ptr = dq_gamma.data_ptr()
+    if k_gamma is not None and (want_dgamma or dk_gamma is not None):
+        if dk_gamma is None:
+            dk_gamma = _empty((head_dim,), (1,), dtype=torch.float32, device=device)
+        else:
+            _vec(dk_gamma, "dk_gamma", head_dim, torch.float32)
+        dkg_ptr = dk_gamma.data_ptr()
     if dq_gamma is not None or dk_gamma is not None:
-        ws_ptr, ws_bytes, ws = _scratch(workspace, tp_qk_norm_rope_workspace_size(m, hq, hk, head_dim), dev)
+        ws_ptr, ws_bytes, ws = _scratch(workspace, tp_qk_norm_rope_workspace_size(m, hq, hk, head_dim), device)
     _lib.check(_lib.load().tp_qk_norm_rope_backward(
-        dq_out.data_ptr(), lddqo, dk_out.data_ptr(), lddko, _dt(dq_out, "dq_out"), x_ptr[0], x_ld[0], x_ptr[1],
-        x_ld[1], _lib.TP_F32 if x_dt is None else x_dt, m, hq, hk, head_dim, *shared, dq.data_ptr(), lddq,
-        dk.data_ptr(), lddk, _dt(dq, "dq"), dg_ptr[0], dg_ptr[1], ws_ptr, ws_bytes, _raw_stream(dev)))
+        dq_out.data_ptr(), lddqo, dk_out.data_ptr(), lddko, _dt(dq_out, "dq_out"), q_ptr, ldq, k_ptr, ldk, q_dt or 0,
+        m, hq, hk, head_dim, *shared, dq.data_ptr(), lddq, dk.data_ptr(), lddk, _dt(dq, "dq"), dqg_ptr, dkg_ptr,
+        ws_ptr, ws_bytes, _raw_stream(index)))
     return dq, dk, dq_gamma, dk_gamma
