@@ -413,51 +413,50 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
 }
 
 // -------------------------------------------------------------------- outer
-// Partial sums over rows of small^T . big: small [rows, r] fp32 (T, or dT sa)
-// split into three bf16 parts, big [rows, width] streamed from memory. The sum
-// runs over the rows, so a lane loads an 8 x 8 block (8 rows, 8 columns): its
-// column c is an operand of 8 consecutive rows, and 16 lanes cover 128 columns,
-// every eighth at a time. A block owns 128 columns, up to 32 ranks and a run of
-// 32-row chunks, which its four waves take in turn, each with LDS of its own
-// for the small operand; their sums are added in LDS in wave order. The next
-// chunk is in flight while one is multiplied.
-constexpr int OU_MC = 32;            // rows per chunk
-constexpr int OU_PITCH = OU_MC + 8;  // bf16 per LDS row: 16 rows cover the 64 banks
-constexpr int OU_COLS = 128;         // columns of a block
-constexpr int OU_RB = 32;            // ranks of a block, at most
+// Partial sums over rows of small^T . big: small [rows, r] (T, or dT sa) as
+// three bf16 parts in planes of 32-row chunks (k_side_prep), big [rows, width]
+// streamed from memory. The sum runs over the rows, so a lane loads an 8 x 8
+// block (8 rows, 8 columns): its column c is an operand of 8 consecutive rows,
+// and 16 lanes cover 128 columns, every eighth at a time. A block owns 128
+// columns, up to 32 ranks and a run of chunks, which its four waves take in
+// turn; their sums are added in LDS in wave order. The next chunk is in flight
+// while one is multiplied.
+constexpr int OU_MC = 32;     // rows per chunk
+constexpr int OU_COLS = 128;  // columns of a block
+constexpr int OU_RB = 32;     // ranks of a block, at most
 
 struct OuterArgs {
   const void* big;
-  int64_t ldbig, width;  // [m, width]
-  const float* small;    // T, or dT sa: [m, 64]
+  int64_t ldbig, width;   // [m, width]
+  const uint16_t* small;  // planes [3, nmc, R, 32]
   int64_t m;
-  int r, splits, chunks_per_split;
-  int64_t nmc;           // 32-row chunks
-  float* part;           // [splits, width, R]; of codes: [splits, R, width]
+  int splits, chunks_per_split;
+  int64_t nmc;            // 32-row chunks
+  float* part;            // [splits, width, R]; of codes: [splits, R, width]
 };
 
 template <int R> struct OuterShape {
   static constexpr int RB = R < OU_RB ? R : OU_RB;  // ranks of a block
   static constexpr int HALVES = R / RB;
-  static constexpr int LDS = 4 * 3 * RB * OU_PITCH;  // 16-bit words
+  static constexpr int LDS = 4 * 2 * (RB / 16) * 64;  // f32x4: two columns' sums of four waves
 };
 
 template <typename SRC, int R, bool BY_RANK>
-__device__ __forceinline__ void outer_block(const OuterArgs& a, unsigned blk, uint16_t* lds) {
+__device__ __forceinline__ void outer_block(const OuterArgs& a, unsigned blk, f32x4_t* red) {
   typedef typename SRC::elem TY;
   constexpr int RB = OuterShape<R>::RB, HALVES = OuterShape<R>::HALVES;
   constexpr int NF = RB / 16, PS = SRC::PARTS;
-  constexpr int PLANE = RB * OU_PITCH;
   constexpr bool AHEAD = PS == 1;  // fp32 columns leave no registers for a second block
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g4 = lane >> 4;
-  uint16_t* st = lds + wave * 3 * PLANE;
   const int j0 = (int)(blk % HALVES) * RB;
   const int split = (int)(blk / HALVES % (unsigned)a.splits);
   const int64_t col0 = (int64_t)(blk / HALVES / (unsigned)a.splits) * OU_COLS, col = col0 + 8 * l16;
   const int valid = (int)max((int64_t)0, min((int64_t)8, a.width - col));
   const bool inside = col0 + OU_COLS <= a.width;
   const TY* big = (const TY*)a.big + (valid > 0 ? col : 0);
+  const uint16_t* small = a.small + (j0 + l16) * OU_MC + 8 * g4;
+  const int64_t plane = a.nmc * (R * OU_MC);
   const int64_t c0 = (int64_t)split * a.chunks_per_split, c1 = min(c0 + a.chunks_per_split, a.nmc);
   f32x4_t acc[8][NF];
 #pragma unroll
@@ -465,15 +464,13 @@ __device__ __forceinline__ void outer_block(const OuterArgs& a, unsigned blk, ui
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[c][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  float sv[NF][8];
+  bf16x8_t sm[NF][3];
   auto load_small = [&](int64_t ch) {
 #pragma unroll
-    for (int q = 0; q < NF; ++q) {
-      const int u = lane + 64 * q, j = u % RB, oct = u / RB;
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)  // in range always; zeroed where it does not count when it is staged
-        sv[q][i] = a.small[min(ch * OU_MC + 8 * oct + i, a.m - 1) * SIDE_T + j0 + j];
-    }
+      for (int p = 0; p < 3; ++p)
+        sm[f][p] = *reinterpret_cast<const bf16x8_t*>(small + p * plane + ch * (R * OU_MC) + f * (16 * OU_MC));
   };
   auto load_big = [&](int64_t ch, Block8<SRC>& b) {
     const int64_t r0 = ch * OU_MC;
@@ -500,46 +497,29 @@ __device__ __forceinline__ void outer_block(const OuterArgs& a, unsigned blk, ui
   }
   for (; ch < c1; ch += 4) {
     if (!AHEAD) load_big(ch, next);
-    wave_lds_sync();
-#pragma unroll
-    for (int q = 0; q < NF; ++q) {
-      const int u = lane + 64 * q, j = u % RB, oct = u / RB;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        sv[q][i] = ch * OU_MC + 8 * oct + i < a.m && j0 + j < a.r ? sv[q][i] : 0.f;
-      bf16x8_t h, md, l;
-      split3_bf16(sv[q], h, md, l);
-      uint16_t* to = st + j * OU_PITCH + 8 * oct;
-      *reinterpret_cast<bf16x8_t*>(to) = h;
-      *reinterpret_cast<bf16x8_t*>(to + PLANE) = md;
-      *reinterpret_cast<bf16x8_t*>(to + 2 * PLANE) = l;
-    }
-    wave_lds_sync();
     const Block8<SRC> now = next;
+    bf16x8_t sn[NF][3];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) sn[f][p] = sm[f][p];
     if (ch + 4 < c1) {
       load_small(ch + 4);
       if (AHEAD) load_big(ch + 4, next);
     }
-    bf16x8_t sm[NF][3];
-#pragma unroll
-    for (int f = 0; f < NF; ++f)
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-        sm[f][p] = *reinterpret_cast<const bf16x8_t*>(st + p * PLANE + (16 * f + l16) * OU_PITCH + 8 * g4);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       bf16x8_t bc[PS];
       now.column(c, bc);
 #pragma unroll
-      for (int f = 0; f < NF; ++f) acc[c][f] = mfma_parts(sm[f], bc, acc[c][f]);
+      for (int f = 0; f < NF; ++f) acc[c][f] = mfma_parts(sn[f], bc, acc[c][f]);
       if (c & 1) __builtin_amdgcn_sched_barrier(0);  // two columns' operands at a time
     }
   }
   // lane l holds, for column col + c, the ranks j0 + 16 f + 4 (l / 16) + v. Two
   // columns' sums at a time (c and c + 4) go through LDS, where a thread adds
   // the waves' sums of one: four columns in a row after the four rounds.
-  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);  // [wave][column][f][lane]
-  static_assert(4 * 2 * NF * 64 * 16 <= OuterShape<R>::LDS * 2, "the sums fit in the staging area");
+  // red: [wave][column][f][lane]
   const int half = (int)threadIdx.x / (64 * NF), f = (int)threadIdx.x / 64 % NF;
   f32x4_t sum[4];
 #pragma unroll
@@ -582,11 +562,11 @@ __global__ __launch_bounds__(256) void k_side_dt(DtArgs t) {
 // dA's (which alone do not fill the chip).
 template <typename SRC, int R>
 __global__ __launch_bounds__(256) void k_side_outer(OuterArgs db, OuterArgs da, unsigned nb_db) {
-  __shared__ __align__(16) uint16_t lds[OuterShape<R>::LDS];
+  __shared__ f32x4_t red[OuterShape<R>::LDS];
   if (blockIdx.x < nb_db)
-    outer_block<SRC, R, false>(db, blockIdx.x, lds);
+    outer_block<SRC, R, false>(db, blockIdx.x, red);
   else
-    outer_block<SrcI8, R, true>(da, blockIdx.x - nb_db, lds);
+    outer_block<SrcI8, R, true>(da, blockIdx.x - nb_db, red);
 }
 
 // --------------------------------------------------------------------- join
@@ -605,24 +585,71 @@ __device__ __forceinline__ f32x4_t sum_splits(const float* p, int64_t pitch, int
   return s;
 }
 
-// The splits of T or dT added in order, four ranks a thread, times alpha: rows
-// of 64, zeros past the rank. `scaled` gets them times the rows' factors, t
-// without (or null).
+// T: the splits added in order, four ranks a thread, times the rows' factors:
+// rows of 64, zeros past the rank.
 template <int R>
 __global__ __launch_bounds__(256) void k_side_join_t(const float* __restrict__ p, int splits, int64_t M,
-                                                     const float* __restrict__ rowscale, float alpha, int r,
-                                                     float* __restrict__ t, float* __restrict__ scaled) {
+                                                     const float* __restrict__ rowscale, int r,
+                                                     float* __restrict__ t) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, row = e / (SIDE_T / 4);
   const int j = (int)(e % (SIDE_T / 4)) * 4;
   if (row >= M) return;
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
   if (j < r) {
-    s = sum_splits(p + row * R + j, M * R, splits);
+    s = sum_splits(p + row * R + j, M * R, splits) * rowscale[row];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) s[v] = j + v < r ? s[v] * alpha : 0.f;
+    for (int v = 0; v < 4; ++v) s[v] = j + v < r ? s[v] : 0.f;
   }
-  if (t != nullptr) *reinterpret_cast<f32x4_t*>(t + row * SIDE_T + j) = s;
-  *reinterpret_cast<f32x4_t*>(scaled + row * SIDE_T + j) = s * rowscale[row];
+  *reinterpret_cast<f32x4_t*>(t + row * SIDE_T + j) = s;
+}
+
+// The small operands of the outer products, one 32-row chunk a block: the first
+// nmc blocks add dT's splits in order, times alpha, into dt (rows of 64, zeros
+// past the rank), and split dT sa into planes; the others split T. Rows past
+// the last one and ranks past r are zeros in the planes.
+template <int R>
+__global__ __launch_bounds__(512) void k_side_prep(const float* __restrict__ part, int splits, int64_t M,
+                                                   const float* __restrict__ sa, float alpha, int r,
+                                                   const float* __restrict__ t, float* __restrict__ dt,
+                                                   uint16_t* __restrict__ dt_planes,
+                                                   uint16_t* __restrict__ t_planes, int64_t nmc) {
+  __shared__ float tile[OU_MC][R + 1];
+  const bool is_dt = (int64_t)blockIdx.x < nmc;
+  const int64_t ch = is_dt ? blockIdx.x : blockIdx.x - nmc;
+  {
+    const int i = threadIdx.x / (SIDE_T / 4), j = threadIdx.x % (SIDE_T / 4) * 4;  // 32 rows of 16 quads
+    const int64_t row = ch * OU_MC + i;
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+    if (row < M && j < r) {
+      s = is_dt ? sum_splits(part + row * R + j, M * R, splits) * alpha
+                : *reinterpret_cast<const f32x4_t*>(t + row * SIDE_T + j);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) s[v] = j + v < r ? s[v] : 0.f;
+    }
+    if (is_dt && row < M) {
+      *reinterpret_cast<f32x4_t*>(dt + row * SIDE_T + j) = s;
+      s = s * sa[row];
+    }
+    if (j < R) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) tile[i][j + v] = s[v];
+    }
+  }
+  __syncthreads();
+  uint16_t* planes = is_dt ? dt_planes : t_planes;
+  const int64_t plane = nmc * (R * OU_MC);
+  if (threadIdx.x < R * (OU_MC / 8)) {
+    const int j = threadIdx.x % R, oct = threadIdx.x / R;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = tile[8 * oct + i][j];
+    bf16x8_t h, m, l;
+    split3_bf16(v, h, m, l);
+    uint16_t* to = planes + (ch * R + j) * OU_MC + 8 * oct;
+    *reinterpret_cast<bf16x8_t*>(to) = h;
+    *reinterpret_cast<bf16x8_t*>(to + plane) = m;
+    *reinterpret_cast<bf16x8_t*>(to + 2 * plane) = l;
+  }
 }
 
 // The splits of dB [splits, N, R] and dA [splits, R, K] added. The first nb_db
@@ -697,7 +724,8 @@ struct SidePlan {
   int64_t nmc;                   // 32-row chunks (outer)
   int64_t cb2, cb3;              // column blocks of dB and dA
   int s2, cps2, s3, cps3;
-  int64_t off2, off3, off4, total;  // floats: the dB and dA partial sums, dT sa, and all
+  int64_t off2, off3;            // floats: the dB and dA partial sums
+  int64_t off4, off5, total;     // the planes of dT sa and of T, and all
 };
 
 int padded_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
@@ -725,15 +753,19 @@ SidePlan side_plan(int64_t m, int64_t n, int64_t k, int64_t r) {
   p.nmc = (m + OU_MC - 1) / OU_MC;
   p.cb2 = (n + OU_COLS - 1) / OU_COLS;
   p.cb3 = (k + OU_COLS - 1) / OU_COLS;
-  // (a split is at least a chunk for each of the four waves)
-  split_of(n > 0 ? (p.nmc + 3) / 4 : 0, p.cb2 > 0 ? 512 / p.cb2 : 0, &p.s2, &p.cps2);
-  split_of((p.nmc + 3) / 4, 512 / p.cb3, &p.s3, &p.cps3);
+  // Two blocks a compute unit are resident: dB's and dA's together are made to
+  // fit in that once. A split is at least a chunk for each of the four waves.
+  const int64_t quads = (p.nmc + 3) / 4, want = 512 / ((p.cb2 + p.cb3) * (R > OU_RB ? R / OU_RB : 1));
+  split_of(n > 0 ? quads : 0, want, &p.s2, &p.cps2);
+  split_of(quads, want, &p.s3, &p.cps3);
   p.cps2 *= 4;
   p.cps3 *= 4;
   p.off2 = (int64_t)p.s1 * p.wn * m * R;
   p.off3 = p.off2 + (int64_t)p.s2 * n * R;
   p.off4 = p.off3 + (int64_t)p.s3 * k * R;
-  p.total = p.off4 + m * SIDE_T;
+  const int64_t planes = 3 * p.nmc * R * OU_MC / 2;  // in floats
+  p.off5 = p.off4 + planes;
+  p.total = p.off5 + planes;
   return p;
 }
 
@@ -768,14 +800,6 @@ hipError_t dt_launch(const SideGradArgs& a, const SidePlan& p, hipStream_t strea
 }
 
 template <int R>
-hipError_t join_t_launch(const float* part, int splits, int64_t m, const float* sa, float alpha, int r, float* t,
-                         float* scaled, hipStream_t stream) {
-  hipLaunchKernelGGL((k_side_join_t<R>), dim3((unsigned)((m * (SIDE_T / 4) + 255) / 256)), dim3(256), 0, stream, part,
-                     splits, m, sa, alpha, r, t, scaled);
-  return hipGetLastError();
-}
-
-template <int R>
 hipError_t grad_r(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) {
   hipError_t e = hipSuccess;
   if (a.m > 0) {
@@ -786,11 +810,12 @@ hipError_t grad_r(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) 
         e = a.b_bf16 ? dt_launch<SrcF32, uint16_t, R>(a, p, stream) : dt_launch<SrcF32, float, R>(a, p, stream);
       if (e != hipSuccess) return e;
     }
-    float* scaled = a.ws + p.off4;
-    e = join_t_launch<R>(a.ws, p.s1 * p.wn, a.m, a.sa, a.alpha, a.r, a.dt, scaled, stream);
-    if (e != hipSuccess) return e;
-    const OuterArgs db{a.dy, a.lddy, a.n, a.t, a.m, a.r, p.s2, p.cps2, p.nmc, a.ws + p.off2};
-    const OuterArgs da{a.qa, a.ldqa, a.k, scaled, a.m, a.r, p.s3, p.cps3, p.nmc, a.ws + p.off3};
+    uint16_t *dt_planes = (uint16_t*)(a.ws + p.off4), *t_planes = (uint16_t*)(a.ws + p.off5);
+    hipLaunchKernelGGL((k_side_prep<R>), dim3((unsigned)(2 * p.nmc)), dim3(512), 0, stream, a.ws, p.s1 * p.wn, a.m, a.sa,
+                       a.alpha, a.r, a.t, a.dt, dt_planes, t_planes, p.nmc);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const OuterArgs db{a.dy, a.lddy, a.n, t_planes, a.m, p.s2, p.cps2, p.nmc, a.ws + p.off2};
+    const OuterArgs da{a.qa, a.ldqa, a.k, dt_planes, a.m, p.s3, p.cps3, p.nmc, a.ws + p.off3};
     const unsigned nb_db = (unsigned)(p.cb2 * p.s2 * OuterShape<R>::HALVES);
     const dim3 grid(nb_db + (unsigned)(p.cb3 * p.s3 * OuterShape<R>::HALVES)), block(256);
     if (a.dy_bf16)
@@ -819,7 +844,9 @@ hipError_t down_r(const SideDownArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((k_side_down<TA, R, 4, 2>), grid, block, 0, stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return join_t_launch<R>(a.ws, p.s * p.wn, a.m, a.sa, 1.f, a.r, nullptr, a.t, stream);
+  hipLaunchKernelGGL((k_side_join_t<R>), dim3((unsigned)((a.m * (SIDE_T / 4) + 255) / 256)), dim3(256), 0, stream, a.ws,
+                     p.s * p.wn, a.m, a.sa, a.r, a.t);
+  return hipGetLastError();
 }
 
 template <typename TA>
