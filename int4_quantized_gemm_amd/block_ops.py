@@ -320,7 +320,7 @@ def _heads(t, name, m, head_dim, dtype=None):
     """Row pitch, width and head count of a [m, heads * head_dim] matrix."""
     ld = _mat(t, name, m, dtype=dtype)
     width = t.shape[1]
-    if width % head_dim != 0:
+    if head_dim < 1 or width % head_dim != 0:
         raise ValueError(f"{name} must have a multiple of {head_dim} columns, got shape {tuple(t.shape)}")
     return ld, width, width // head_dim
 

@@ -161,8 +161,9 @@ __device__ __forceinline__ Place place_of(int groups, int rows_per_block) {
 // t gamma is exact in fp64, nothing is rounded to a shorter type in between).
 // bf16: fp32 arithmetic, one rounding.
 //
-// Bound by HBM for the bf16 rows and by fp64 issue plus the row's chain (load,
-// transpose, two joins, two divisions) for the codes.
+// Bound by HBM for the bf16 rows (4096 x 3072, bf16 in and stream: 18.6 us, 5.4
+// TB/s) and by fp64 issue plus the row's chain (load, transpose, two joins, two
+// divisions) for the codes (4032 x 3072, fp32 in, bf16 stream: 24.9 us, 4.5 TB/s).
 template <typename TX, typename TS, bool RES, int OUT, int NT>
 __global__ __launch_bounds__(NT, 4) void k_norm_rotate(NormArgs a, int rows_per_block) {
   typedef typename std::conditional<OUT == NORM_OUT_I8, double, float>::type T;
@@ -318,7 +319,10 @@ __global__ __launch_bounds__(NT, 4) void k_norm_rotate(NormArgs a, int rows_per_
 //   g = dy . blockdiag(H / 16) (the rotation is its own inverse), or dy
 //   dt = r gamma g - t r^3 mean(gamma g t) + dsum;   dgamma = sum over rows of g t r
 // in fp32. A thread keeps its 16 columns of dgamma over the rows of its block;
-// the blocks' sums are joined by k_colsum in a fixed order. Bound by HBM.
+// the blocks' sums are joined by k_colsum in a fixed order. Bound by HBM (4096 x
+// 3072, fp32 dy, bf16 t, dsum and dx: 25.4 us, 5.0 TB/s, and 4.2 us for the join
+// of 512 partial rows). Rows of more than 16 groups with a block each (ONE) keep
+// no sums, so that two of 768 threads share a compute unit.
 template <typename TG, typename TT, typename TD, bool DS, int NT, bool ONE>
 __global__ __launch_bounds__(NT, NT == 768 ? 6 : 1) void k_norm_bwd(NormBwdArgs a, int rows_per_block) {
   constexpr int SET_BYTES = 16 * (16 + 4) * 4;

@@ -113,6 +113,7 @@ template <> struct RawOp<float> {
 // 12288 columns at rank 32). Lane l feeds row l % 16 with the 16 codes
 // 16 (l / 16) of each 64; A's columns are stored in the order in which the two
 // products of a step take them. With few rows (WR 1) the waves share a chunk.
+// 4096 x 12288 at rank 32: 14.4 us (3.6 TB/s; two to three chunks a block).
 constexpr int SD_KC = 256;           // columns per chunk
 constexpr int SD_PITCH = SD_KC + 8;  // bf16 per LDS row: rows 4 banks apart
 
@@ -230,7 +231,8 @@ __global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64) ? 
 // Partial sums of dY . B: a block owns 16 WR rows and a run of 256-column
 // chunks; the chunk of B is transposed (and split) into LDS, from where it is
 // the matrix units' second operand, and dY goes straight from memory to the
-// first. With few rows (WR 1) the four waves share the chunk instead.
+// first. With few rows (WR 1) the four waves share the chunk instead. 4096 x 9216
+// bf16 at rank 32: 17.0 us (4.6 TB/s).
 constexpr int DT_NC = 256;            // columns of dY per chunk
 constexpr int DT_PITCH = DT_NC + 8;   // bf16 per LDS row: rows 4 banks apart
 
@@ -420,7 +422,8 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
 // and 16 lanes cover 128 columns, every eighth at a time. A block owns 128
 // columns, up to 32 ranks and a run of chunks, which its four waves take in
 // turn; their sums are added in LDS in wave order. The next chunk is in flight
-// while one is multiplied.
+// while one is multiplied; bound by that chain of loads (4096 x 9216 bf16 and 4096
+// x 3072 codes at rank 32: 20.5 us; dB alone 17.6, of which its loads take 16.7).
 constexpr int OU_MC = 32;     // rows per chunk
 constexpr int OU_COLS = 128;  // columns of a block
 constexpr int OU_RB = 32;     // ranks of a block, at most

@@ -282,3 +282,86 @@ def test_side_gradients_of_more_than_2_31_elements():
     B.assert_sum(f64(db)[host(cols)], yc.T @ t64, np.abs(yc).T @ np.abs(t64), 3 * m, "dB")
     qc, dt64 = f64(qa[:, cols % k]) * f64(sa)[:, None], f64(dt)[:, :r]
     B.assert_sum(f64(da)[:, host(cols % k)], dt64.T @ qc, np.abs(dt64).T @ np.abs(qc), 3 * m, "dA")
+
+
+def _every_argument(blk):
+    """Each call with all its arguments given by name, outputs and workspaces
+    too: (function, inputs, a maker of its output arguments)."""
+    d = blk.x.device
+    m, k, n, r, hd = blk.m, blk.k, blk.n, blk.r, blk.hd
+    qa, sa, t, low, qkv, _ = blk.forward()
+    f = lambda *shape: torch.full(shape, 7.0, device=d)  # noqa: E731
+    b = lambda *shape: torch.full(shape, 7.0, dtype=BF16, device=d)  # noqa: E731
+    ws = lambda size: torch.empty((max(size, 16),), dtype=torch.uint8, device=d)  # noqa: E731
+    q, kk, dq, dk = (v[:, lo:hi] for v in (qkv, blk.grad) for lo, hi in ((0, blk.cq), (blk.cq, blk.ck)))
+    rope = dict(blk.rope(), layout="halves")
+    return [
+        (tp.tp_rmsnorm_rotate, dict(x=blk.x, gamma=blk.gamma, eps=1e-3, residual=blk.res, rotate=False, out_kind="i8"),
+         lambda: dict(out=torch.empty((m, k), dtype=torch.int8, device=d), scales=f(m), sum_out=b(m, k))),
+        (tp.tp_rmsnorm_rotate_backward, dict(dy=blk.x, t=t, gamma=blk.gamma, eps=1e-3, dsum=blk.dsum, rotate=False,
+                                             dx_dtype=BF16, want_dgamma=True),
+         lambda: dict(dx=b(m, k), dgamma=f(k), workspace=ws(tp.tp_rmsnorm_backward_workspace_size(m, k)))),
+        (tp.tp_lora_down_prequantized, dict(qa=qa, sa=sa, lora_a=blk.a),
+         lambda: dict(t=f(m, 64), workspace=ws(tp.tp_lora_down_prequantized_workspace_size(m, k, r)))),
+        (tp.tp_lora_grad_prequantized, dict(dy=blk.grad, qa=qa, sa=sa, t=low, lora_b=blk.b, alpha=ALPHA, rotate=True),
+         lambda: dict(da=f(r, k), db=f(n, r), dt=f(m, 64), workspace=ws(tp.tp_lora_grad_workspace_size(m, n, k, r)))),
+        (tp.tp_qk_norm_rope, dict(rope, q=q, k=kk, out_dtype=BF16), lambda: dict(q_out=b(m, blk.cq), k_out=b(m, blk.ck - blk.cq))),
+        (tp.tp_qk_norm_rope_backward, dict(rope, dq_out=dq, dk_out=dk, q=q, k=kk, dx_dtype=BF16, want_dgamma=True),
+         lambda: dict(dq=b(m, blk.cq), dk=b(m, blk.ck - blk.cq), dq_gamma=f(hd), dk_gamma=f(hd),
+                      workspace=ws(tp.tp_qk_norm_rope_workspace_size(m, blk.hq, blk.hk, hd)))),
+    ]
+
+
+def test_every_argument_on_another_stream_or_device(monkeypatch):
+    """A call that moves to a named stream, or to its tensors' device, passes
+    all its arguments on: the same bytes, in the outputs that it was given."""
+    d = dev()
+    announce("every argument, moved calls")
+    from int4_quantized_gemm_amd import block_ops
+    blk = Block(33, 512, 4, 2, 32, 8, seed=11, d=d)
+    side = torch.cuda.Stream()
+    for fn, inputs, outputs in _every_argument(blk):
+        want = [v.clone() for v in fn(**inputs)] if fn is not tp.tp_lora_down_prequantized else [fn(**inputs).clone()]
+        for how in ("stream", "device"):
+            outs = outputs()
+            torch.cuda.synchronize()
+            if how == "stream":
+                got = fn(**inputs, **outs, stream=side)
+            else:
+                real, first = block_ops._current_device, []
+                monkeypatch.setattr(block_ops, "_current_device",
+                                    lambda: real() if first else first.append(1) or real() + 1)
+                got = fn(**inputs, **outs)
+                monkeypatch.setattr(block_ops, "_current_device", real)
+                assert first
+            side.synchronize()
+            got = list(got) if isinstance(got, tuple) else [got]
+            _equal(got, want, f"{fn.__name__} {how}")
+            given = {v.data_ptr() for name, v in outs.items() if name != "workspace"}
+            assert {v.data_ptr() for v in got} == given, f"{fn.__name__}: outputs of its own"
+
+
+def test_tensors_of_the_host_or_wrong_shape_are_refused():
+    d = dev()
+    blk = Block(8, 256, 2, 1, 32, 8, seed=12, d=d)
+    qa, sa, t, low, qkv, _ = blk.forward()
+    with pytest.raises(ValueError, match="gamma must be a tensor on"):
+        tp.tp_rmsnorm_rotate(blk.x, blk.gamma.cpu())
+    with pytest.raises(ValueError, match="residual must have shape"):
+        tp.tp_rmsnorm_rotate(blk.x, blk.gamma, residual=blk.res[:4])
+    with pytest.raises(TypeError, match="out must be"):
+        tp.tp_rmsnorm_rotate(blk.x, blk.gamma, out=torch.empty((8, 256), device=d))
+    with pytest.raises(ValueError, match="unit stride"):
+        tp.tp_rmsnorm_rotate(blk.x.t().contiguous().t(), blk.gamma)
+    with pytest.raises(ValueError, match="contiguous vector"):
+        tp.tp_lora_down_prequantized(qa, sa[:4], blk.a)
+    with pytest.raises(ValueError, match="lora_b must have shape"):
+        tp.tp_lora_grad_prequantized(blk.grad, qa, sa, low, blk.b[:-1], 1.0)
+    with pytest.raises(ValueError, match="multiple of 48"):
+        tp.tp_qk_norm_rope(qkv[:, :64], qkv[:, 64:96], 48)
+    with pytest.raises(ValueError, match="pair_axis must have 16 entries"):
+        tp.tp_qk_norm_rope(qkv[:, :64], qkv[:, 64:96], 32, blk.pos, blk.freq, [0] * 4)
+    with pytest.raises(ValueError, match="q is needed"):
+        tp.tp_qk_norm_rope_backward(qkv[:, :64], qkv[:, 64:96], None, None, 32, q_gamma=blk.qg)
+    with pytest.raises(tp.TPError, match="workspace"):
+        tp.tp_lora_down_prequantized(qa, sa, blk.a, workspace=torch.empty((16,), dtype=torch.uint8, device=d))
