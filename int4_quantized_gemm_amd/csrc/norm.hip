@@ -150,7 +150,7 @@ __device__ __forceinline__ Place place_of(int groups, int rows_per_block) {
   p.slot = p.set / groups;
   p.grp = p.set - p.slot * groups;
   p.rows = rows_per_block;
-  p.wide = groups >= 4;
+  p.wide = groups >= 4 && rows_per_block == 1;
   p.active = p.slot < rows_per_block;
   return p;
 }
@@ -433,8 +433,22 @@ __global__ __launch_bounds__(NT, NT == 768 ? 6 : 1) void k_norm_bwd(NormBwdArgs 
     if (live) store16((TD*)a.dx + row * a.lddx + col, o);
     if (ONE) break;
   }
-  if (a.dgamma != nullptr && pl.active)
-    store16(a.part + ((int64_t)blockIdx.x * pl.rows + pl.slot) * (a.groups * 256) + col, dg);
+  if (a.dgamma == nullptr) return;
+  float* part = a.part + (int64_t)blockIdx.x * (a.groups * 256);
+  if (pl.rows == 1) {
+    if (pl.active) store16(part + col, dg);
+    return;
+  }
+  // the sums of the block's rows, added in order
+  float* sums = reinterpret_cast<float*>(lds);  // [rows][columns]: 1 KiB of a set's 1.25 KiB
+  __syncthreads();
+  if (pl.active) store16(sums + pl.slot * (a.groups * 256) + col, dg);
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.groups * 256; c += (int)blockDim.x) {
+    float s = sums[c];
+    for (int w = 1; w < pl.rows; ++w) s += sums[w * (a.groups * 256) + c];
+    part[c] = s;
+  }
 }
 
 // Column sums of part [rows, cols]: 64 columns a block, 16 slices of the rows,
@@ -512,9 +526,25 @@ hipError_t norm_x(const NormArgs& a, hipStream_t stream) {
   return a.s_bf16 ? norm_out<TX, uint16_t, true>(a, stream) : norm_out<TX, float, true>(a, stream);
 }
 
+// Short rows share blocks of 16 sets: dgamma's partial sums are one row a block
+// however many rows share it, and blocks of one short row leave compute units
+// idle. 49152 x 256 bf16: 24.6 us with dgamma's join, 44.5 with blocks of 64
+// threads and a partial row each; 12288 x 1024: 23.4 and 42.7. Few rows are spread
+// over more blocks.
+Shape bwd_shape_of(int64_t m, int groups) {
+  Shape s;
+  int64_t rows = groups <= 16 ? 16 / groups : 1;
+  while (rows > 1 && (m + rows - 1) / rows < 256) rows = (rows + 1) / 2;
+  s.rows = (int)rows;
+  s.threads = (s.rows * groups * 16 + 63) / 64 * 64;
+  s.blocks = (m + s.rows - 1) / s.rows;
+  if (s.blocks > NORM_BWD_BLOCKS) s.blocks = NORM_BWD_BLOCKS;
+  return s;
+}
+
 template <typename TG, typename TT, typename TD, bool DS>
 hipError_t bwd_launch(const NormBwdArgs& a, hipStream_t stream) {
-  const Shape s = shape_of(a.m, a.groups, NORM_BWD_BLOCKS);
+  const Shape s = bwd_shape_of(a.m, a.groups);
   const bool one = s.blocks * s.rows >= a.m;
   const size_t lds = (size_t)(s.threads / 16) * (16 * 20 * 4 + 2 * sizeof(double2));
   const dim3 grid((unsigned)s.blocks), block((unsigned)s.threads);
@@ -540,10 +570,7 @@ hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream) {
   return a.x_bf16 ? norm_x<uint16_t>(a, stream) : norm_x<float>(a, stream);
 }
 
-int64_t norm_bwd_partial_rows(int64_t m, int groups) {
-  const Shape s = shape_of(m, groups, NORM_BWD_BLOCKS);
-  return s.blocks * s.rows;
-}
+int64_t norm_bwd_partial_rows(int64_t m, int groups) { return bwd_shape_of(m, groups).blocks; }
 
 hipError_t launch_colsum(const float* part, int64_t rows, int64_t cols, float* out, int64_t first, float* out2,
                          hipStream_t stream) {
