@@ -112,10 +112,18 @@ template <> struct RawOp<float> {
 // memory made one compute unit's loads the bound: 24 us for a single row of
 // 12288 columns at rank 32). Lane l feeds row l % 16 with the 16 codes
 // 16 (l / 16) of each 64; A's columns are stored in the order in which the two
-// products of a step take them. With few rows (WR 1) the waves share a chunk.
+// products of a step take them. With few rows (WR 1) the waves share a chunk and
+// join their sums in LDS (one row of 12288 columns at rank 16: 12.8 us with the
+// join over blocks, 17.3 with a partial sum a wave and no limit on the splits).
 // 4096 x 12288 at rank 32: 14.4 us (3.6 TB/s; two to three chunks a block).
-constexpr int SD_KC = 256;           // columns per chunk
-constexpr int SD_PITCH = SD_KC + 8;  // bf16 per LDS row: rows 4 banks apart
+constexpr int SD_KC = 256;  // columns per chunk of the plan
+
+// Columns in LDS at a time, by the rule of dt_columns (4096 x 12288, fp32 A at rank
+// 64: 30 us, 40 with whole chunks); a row's pitch is 8 more.
+template <typename TA, int R, int WR>
+constexpr int down_columns() {
+  return std::is_same<TA, float>::value && R == 64 && WR == 4 ? SD_KC / 2 : SD_KC;
+}
 
 struct DownArgs {
   const int8_t* qa;
@@ -123,31 +131,35 @@ struct DownArgs {
   const void* a;
   int64_t lda, m;
   int r, splits, chunks_per_split, chunks;
-  float* part;  // [splits * 4 / WR, m, R]
+  float* part;  // [splits, m, R]
 };
 
 template <typename TA, int R, int WR, int FM>
-__global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64) ? 1 : 2) void k_side_down(DownArgs d) {
+__global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64 && WR == 1) ? 1 : 2)  //
+    void k_side_down(DownArgs d) {
   constexpr int NF = R / 16;
   constexpr int PA = std::is_same<TA, float>::value ? 3 : 1;
   constexpr int WN = 4 / WR;
-  constexpr int STEPS = SD_KC / 64 / WN;       // 64-column steps of a wave and chunk
-  constexpr int PLANE = R * SD_PITCH;
-  constexpr int UNITS = R * (SD_KC / 8) / 256;  // runs of 8 columns that a thread stages
+  constexpr int KC = down_columns<TA, R, WR>(), PITCH = KC + 8;
+  constexpr int STEPS = KC / 64 / WN;        // 64-column steps of a wave and chunk
+  constexpr int PLANE = R * PITCH;
+  constexpr int RUNS = KC / 8, RANKS = 256 / RUNS;  // runs of 8 columns, and ranks that the threads stage at a time
+  constexpr int UNITS = R / RANKS;                  // runs that a thread stages
   __shared__ __align__(16) uint16_t at[PA * PLANE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g4 = lane >> 4;
   const int rg = wave % WR, ns = wave / WR;
   const int split = (int)(blockIdx.x % (unsigned)d.splits);
   const int64_t m0 = ((int64_t)(blockIdx.x / (unsigned)d.splits) * WR + rg) * (16 * FM);
-  const int c0 = split * d.chunks_per_split, c1 = min(c0 + d.chunks_per_split, d.chunks);
+  const int c0 = split * d.chunks_per_split * (SD_KC / KC);
+  const int c1 = min(c0 + d.chunks_per_split * (SD_KC / KC), d.chunks * (SD_KC / KC));
   // Rows past the last one and ranks past r read the last row or rank instead:
   // what comes of them is not written.
   const int8_t* xrow[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
     xrow[i] = d.qa + min(m0 + 16 * i + l16, d.m - 1) * d.ldqa + ns * (64 * STEPS) + 16 * g4;
-  const int ar = threadIdx.x >> 5, ak = threadIdx.x & 31;  // rank (of 8 at a time) and run of 8 columns staged
+  const int ar = threadIdx.x / RUNS, ak = threadIdx.x % RUNS;  // rank (of RANKS at a time) and run of 8 columns staged
   u32x4_t x[FM][STEPS];
   RawOp<TA> av[UNITS];
   auto load_x = [&](int c) {
@@ -155,12 +167,12 @@ __global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64) ? 
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
-        x[i][s] = *reinterpret_cast<const u32x4_t*>(xrow[i] + (int64_t)c * SD_KC + 64 * s);
+        x[i][s] = *reinterpret_cast<const u32x4_t*>(xrow[i] + (int64_t)c * KC + 64 * s);
   };
   auto load_a = [&](int c) {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
-      av[u].load((const TA*)d.a + (int64_t)min(ar + 8 * u, d.r - 1) * d.lda + (int64_t)c * SD_KC + 8 * ak);
+      av[u].load((const TA*)d.a + (int64_t)min(ar + RANKS * u, d.r - 1) * d.lda + (int64_t)c * KC + 8 * ak);
   };
   f32x4_t acc[FM][NF];
 #pragma unroll
@@ -181,7 +193,7 @@ __global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64) ? 
       av[u].parts(o);
 #pragma unroll
       for (int p = 0; p < PA; ++p)
-        *reinterpret_cast<bf16x8_t*>(at + p * PLANE + (ar + 8 * u) * SD_PITCH + pos) = o[p];
+        *reinterpret_cast<bf16x8_t*>(at + p * PLANE + (ar + RANKS * u) * PITCH + pos) = o[p];
     }
     __syncthreads();
     u32x4_t now[FM][STEPS];
@@ -206,15 +218,28 @@ __global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64) ? 
           bf16x8_t ap[PA];
 #pragma unroll
           for (int p = 0; p < PA; ++p)
-            ap[p] = *reinterpret_cast<const bf16x8_t*>(at + p * PLANE + (16 * f + l16) * SD_PITCH +
+            ap[p] = *reinterpret_cast<const bf16x8_t*>(at + p * PLANE + (16 * f + l16) * PITCH +
                                                        64 * (ns * STEPS + s) + 32 * h + 8 * g4);
 #pragma unroll
           for (int i = 0; i < FM; ++i) acc[i][f] = mfma_parts(xp[i], ap, acc[i][f]);
         }
       }
   }
+  if constexpr (WN > 1) {  // the waves' sums of the same rows, added in wave order
+    float* red = reinterpret_cast<float*>(at);
+    static_assert(FM == 1 && WN * 16 * R * 4 <= PA * PLANE * 2, "the sums fit in the staging area");
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) *reinterpret_cast<f32x4_t*>(red + ((wave * NF + f) * 64 + lane) * 4) = acc[0][f];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < WN; ++w)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) acc[0][f] += *reinterpret_cast<const f32x4_t*>(red + ((w * NF + f) * 64 + lane) * 4);
+  }
   // lane l holds rows 4 (l / 16) + v, column 16 f + l % 16
-  float* out = d.part + (int64_t)(split * WN + ns) * d.m * R;
+  float* out = d.part + (int64_t)split * d.m * R;
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -233,8 +258,16 @@ __global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64) ? 
 // the matrix units' second operand, and dY goes straight from memory to the
 // first. With few rows (WR 1) the four waves share the chunk instead. 4096 x 9216
 // bf16 at rank 32: 17.0 us (4.6 TB/s).
-constexpr int DT_NC = 256;            // columns of dY per chunk
-constexpr int DT_PITCH = DT_NC + 8;   // bf16 per LDS row: rows 4 banks apart
+constexpr int DT_NC = 256;  // columns of dY per chunk of the plan
+
+// Columns in LDS at a time: half a chunk where 64 ranks of an fp32 B (three
+// planes) would leave one block a compute unit (all four launches, 4096 x 9216
+// fp32: 148 us, 150 with whole chunks; bf16 dY: 95 and 104). A row's pitch is 8
+// more: rows 4 banks apart.
+template <typename TB, int R>
+constexpr int dt_columns() {
+  return std::is_same<TB, float>::value && R == 64 ? DT_NC / 2 : DT_NC;
+}
 
 // Two dwords' low (odd == 0) or high halves in one.
 __device__ __forceinline__ uint32_t pair_of(uint32_t first, uint32_t second, int odd) {
@@ -305,7 +338,7 @@ struct DtArgs {
   const void* b;
   int64_t ldb, m, n;
   int r, splits, chunks_per_split;
-  float* part;  // [splits * 4 / WR, m, R]
+  float* part;  // [splits, m, R]
 };
 
 // The next chunk's dY and B are in flight while a chunk is multiplied (only B
@@ -316,9 +349,10 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
   typedef typename std::conditional<std::is_same<TB, float>::value, SrcF32, SrcBf16>::type BSRC;
   constexpr int NF = R / 16;
   constexpr int PY = SRC::PARTS, PB = BSRC::PARTS;
-  constexpr int WN = 4 / WR;                // waves that share a chunk
-  constexpr int STEPS = DT_NC / 32 / WN;    // 32-column steps of a wave and chunk
-  constexpr int PLANE = R * DT_PITCH;
+  constexpr int NC = dt_columns<TB, R>(), PITCH = NC + 8;
+  constexpr int WN = 4 / WR;             // waves that share a chunk
+  constexpr int STEPS = NC / 32 / WN;    // 32-column steps of a wave and chunk
+  constexpr int PLANE = R * PITCH;
   constexpr bool AHEAD = PY == 1;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g4 = lane >> 4;
@@ -327,19 +361,20 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
   const int64_t m0 = (int64_t)(blk / (unsigned)a.splits) * (16 * WR) + 16 * rg;
   // rows past the last one read that one: what comes of them is not written
   const TY* row = (const TY*)a.dy + min(m0 + l16, a.m - 1) * a.lddy + ns * (32 * STEPS) + 8 * g4;
-  const int64_t nchunks = (a.n + DT_NC - 1) / DT_NC;
-  const int64_t c0 = (int64_t)split * a.chunks_per_split, c1 = min(c0 + a.chunks_per_split, nchunks);
+  const int64_t nchunks = (a.n + NC - 1) / NC;
+  const int per_split = a.chunks_per_split * (DT_NC / NC);
+  const int64_t c0 = (int64_t)split * per_split, c1 = min(c0 + per_split, nchunks);
   // this thread's 8 x 8 block of a chunk of B
   const int nb = threadIdx.x / (R / 8), jb = threadIdx.x % (R / 8);
-  const bool stages = nb < DT_NC / 8;
+  const bool stages = nb < NC / 8;
   const int cols = max(0, min(8, a.r - 8 * jb));
   const TB* bcol = (const TB*)a.b + (cols > 0 ? 8 * jb : 0);
 
   RawOp<TY> y[STEPS];
   Block8<BSRC> bb;
   auto load_y = [&](int64_t c) {
-    const int64_t n0 = c * DT_NC;
-    if (n0 + DT_NC <= a.n) {
+    const int64_t n0 = c * NC;
+    if (n0 + NC <= a.n) {
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) y[s].load(row + n0 + 32 * s);
     } else {
@@ -353,7 +388,7 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
   };
   auto load_b = [&](int64_t c) {
     if (!stages) return;
-    const int64_t n = c * DT_NC + 8 * nb;
+    const int64_t n = c * NC + 8 * nb;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (n + i < a.n)
@@ -379,7 +414,7 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
         bb.column(e, o);
 #pragma unroll
         for (int p = 0; p < PB; ++p)
-          *reinterpret_cast<bf16x8_t*>(bt + p * PLANE + (8 * jb + e) * DT_PITCH + 8 * nb) = o[p];
+          *reinterpret_cast<bf16x8_t*>(bt + p * PLANE + (8 * jb + e) * PITCH + 8 * nb) = o[p];
       }
     }
     __syncthreads();
@@ -399,13 +434,26 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
         bf16x8_t bp[PB];
 #pragma unroll
         for (int p = 0; p < PB; ++p)
-          bp[p] = *reinterpret_cast<const bf16x8_t*>(bt + p * PLANE + (16 * f + l16) * DT_PITCH + ns * (32 * STEPS) +
+          bp[p] = *reinterpret_cast<const bf16x8_t*>(bt + p * PLANE + (16 * f + l16) * PITCH + ns * (32 * STEPS) +
                                                      32 * s + 8 * g4);
         acc[f] = mfma_parts(yp, bp, acc[f]);
       }
     }
   }
-  float* out = a.part + ((int64_t)(split * WN + ns) * a.m + m0) * R;
+  if constexpr (WN > 1) {  // the waves' sums of the same rows, added in wave order
+    float* red = reinterpret_cast<float*>(bt);
+    static_assert(WN * 16 * R * 4 <= PB * PLANE * 2, "the sums fit in the staging area");
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) *reinterpret_cast<f32x4_t*>(red + ((wave * NF + f) * 64 + lane) * 4) = acc[f];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < WN; ++w)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) acc[f] += *reinterpret_cast<const f32x4_t*>(red + ((w * NF + f) * 64 + lane) * 4);
+  }
+  float* out = a.part + ((int64_t)split * a.m + m0) * R;
 #pragma unroll
   for (int v = 0; v < 4; ++v)
     if (m0 + 4 * g4 + v < a.m) {
@@ -557,7 +605,7 @@ __device__ __forceinline__ void outer_block(const OuterArgs& a, unsigned blk, f3
 template <typename SRC, typename TB, int R, int WR>
 __global__ __launch_bounds__(256) void k_side_dt(DtArgs t) {
   constexpr int PB = std::is_same<TB, float>::value ? 3 : 1;
-  __shared__ __align__(16) uint16_t lds[PB * R * DT_PITCH];
+  __shared__ __align__(16) uint16_t lds[PB * R * (dt_columns<TB, R>() + 8)];
   dt_block<SRC, TB, R, WR>(t, blockIdx.x, lds);
 }
 
@@ -721,7 +769,7 @@ namespace {
 // How the sums are split: enough blocks for the chip, as few partial sums as
 // that allows.
 struct SidePlan {
-  int wr, wn;                    // row groups of a dt block, partial sums per split
+  int wr;                        // row groups of a dt block
   int64_t rb, nchunks;           // row blocks, 256-column chunks (dt)
   int s1, cps1;                  // splits of the columns, chunks of a split
   int64_t nmc;                   // 32-row chunks (outer)
@@ -749,10 +797,10 @@ SidePlan side_plan(int64_t m, int64_t n, int64_t k, int64_t r) {
   SidePlan p;
   const int R = padded_rank(r);
   p.wr = m > 16 ? 4 : 1;
-  p.wn = 4 / p.wr;
   p.rb = (m + 16 * p.wr - 1) / (16 * p.wr);
   p.nchunks = (n + DT_NC - 1) / DT_NC;
-  split_of(m > 0 ? p.nchunks : 0, p.rb > 0 ? 768 / p.rb : 0, &p.s1, &p.cps1);
+  const int64_t want1 = p.rb > 0 ? 768 / p.rb : 0;
+  split_of(m > 0 ? p.nchunks : 0, want1 < 24 ? want1 : 24, &p.s1, &p.cps1);  // (as in down_plan)
   p.nmc = (m + OU_MC - 1) / OU_MC;
   p.cb2 = (n + OU_COLS - 1) / OU_COLS;
   p.cb3 = (k + OU_COLS - 1) / OU_COLS;
@@ -763,7 +811,7 @@ SidePlan side_plan(int64_t m, int64_t n, int64_t k, int64_t r) {
   split_of(quads, want, &p.s3, &p.cps3);
   p.cps2 *= 4;
   p.cps3 *= 4;
-  p.off2 = (int64_t)p.s1 * p.wn * m * R;
+  p.off2 = (int64_t)p.s1 * m * R;
   p.off3 = p.off2 + (int64_t)p.s2 * n * R;
   p.off4 = p.off3 + (int64_t)p.s3 * k * R;
   const int64_t planes = 3 * p.nmc * R * OU_MC / 2;  // in floats
@@ -775,7 +823,7 @@ SidePlan side_plan(int64_t m, int64_t n, int64_t k, int64_t r) {
 struct DownPlan {
   int wr, fm;
   int64_t rb;
-  int s, cps, wn;
+  int s, cps;
   int64_t total;  // floats
 };
 
@@ -783,11 +831,12 @@ DownPlan down_plan(int64_t m, int64_t k, int64_t r) {
   DownPlan p;
   p.wr = m > 16 ? 4 : 1;
   p.fm = m > 64 ? 2 : 1;
-  p.wn = 4 / p.wr;
   const int64_t rows = 16 * p.wr * p.fm;
   p.rb = (m + rows - 1) / rows;
-  split_of(m > 0 ? k / SD_KC : 0, p.rb > 0 ? 512 / p.rb : 0, &p.s, &p.cps);
-  p.total = (int64_t)p.s * p.wn * m * padded_rank(r);
+  // (up to 24 splits: the join adds them eight at a time, and more only lengthen it)
+  const int64_t want = p.rb > 0 ? 512 / p.rb : 0;
+  split_of(m > 0 ? k / SD_KC : 0, want < 24 ? want : 24, &p.s, &p.cps);
+  p.total = (int64_t)p.s * m * padded_rank(r);
   return p;
 }
 
@@ -814,7 +863,7 @@ hipError_t grad_r(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) 
       if (e != hipSuccess) return e;
     }
     uint16_t *dt_planes = (uint16_t*)(a.ws + p.off4), *t_planes = (uint16_t*)(a.ws + p.off5);
-    hipLaunchKernelGGL((k_side_prep<R>), dim3((unsigned)(2 * p.nmc)), dim3(512), 0, stream, a.ws, p.s1 * p.wn, a.m, a.sa,
+    hipLaunchKernelGGL((k_side_prep<R>), dim3((unsigned)(2 * p.nmc)), dim3(512), 0, stream, a.ws, p.s1, a.m, a.sa,
                        a.alpha, a.r, a.t, a.dt, dt_planes, t_planes, p.nmc);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const OuterArgs db{a.dy, a.lddy, a.n, t_planes, a.m, p.s2, p.cps2, p.nmc, a.ws + p.off2};
@@ -848,7 +897,7 @@ hipError_t down_r(const SideDownArgs& a, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_side_join_t<R>), dim3((unsigned)((a.m * (SIDE_T / 4) + 255) / 256)), dim3(256), 0, stream, a.ws,
-                     p.s * p.wn, a.m, a.sa, a.r, a.t);
+                     p.s, a.m, a.sa, a.r, a.t);
   return hipGetLastError();
 }
 
