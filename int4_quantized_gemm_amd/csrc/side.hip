@@ -118,8 +118,9 @@ template <> struct RawOp<float> {
 // 4096 x 12288 at rank 32: 14.4 us (3.6 TB/s; two to three chunks a block).
 constexpr int SD_KC = 256;  // columns per chunk of the plan
 
-// Columns in LDS at a time, by the rule of dt_columns (4096 x 12288, fp32 A at rank
-// 64: 30 us, 40 with whole chunks); a row's pitch is 8 more.
+// Columns in LDS at a time: half a chunk where 64 ranks of an fp32 A (three planes,
+// 101 KiB) would leave one block a compute unit (4096 x 12288: 30 us, 40 with
+// whole chunks). A row's pitch is 8 more: rows 4 banks apart.
 template <typename TA, int R, int WR>
 constexpr int down_columns() {
   return std::is_same<TA, float>::value && R == 64 && WR == 4 ? SD_KC / 2 : SD_KC;
@@ -260,13 +261,13 @@ __global__ __launch_bounds__(256, (std::is_same<TA, float>::value && R == 64 && 
 // bf16 at rank 32: 17.0 us (4.6 TB/s).
 constexpr int DT_NC = 256;  // columns of dY per chunk of the plan
 
-// Columns in LDS at a time: half a chunk where 64 ranks of an fp32 B (three
-// planes) would leave one block a compute unit (all four launches, 4096 x 9216
-// fp32: 148 us, 150 with whole chunks; bf16 dY: 95 and 104). A row's pitch is 8
-// more: rows 4 banks apart.
+// Columns in LDS at a time: half a chunk of an fp32 B's three planes, from 32
+// ranks on: with 50 and 101 KiB fewer blocks share a compute unit (4096 x 9216
+// bf16 at rank 64: 30 us, 51 with whole chunks that half of the threads stage; at
+// rank 32 20 and 25). A row's pitch is 8 more: rows 4 banks apart.
 template <typename TB, int R>
 constexpr int dt_columns() {
-  return std::is_same<TB, float>::value && R == 64 ? DT_NC / 2 : DT_NC;
+  return std::is_same<TB, float>::value && R >= 32 ? DT_NC / 2 : DT_NC;
 }
 
 // Two dwords' low (odd == 0) or high halves in one.
@@ -274,11 +275,11 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t first, uint32_t second, int
   return __builtin_amdgcn_perm(second, first, odd ? 0x07060302u : 0x05040100u);
 }
 
-// 8 x 8 elements of a lane (row i, column c), and column c as an operand of
+// 8 x W elements of a lane (row i, column c), and column c as an operand of
 // the 8 rows: 16-bit halves are paired by byte permutes, fp32 columns split.
-template <typename SRC> struct Block8;
+template <typename SRC, int W = 8> struct Block8;
 
-template <> struct Block8<SrcBf16> {
+template <> struct Block8<SrcBf16, 8> {
   u32x4_t w[8];
   __device__ __forceinline__ void zero(int i) { w[i] = u32x4_t{0u, 0u, 0u, 0u}; }
   __device__ __forceinline__ void load(int i, const uint16_t* p) { w[i] = *reinterpret_cast<const u32x4_t*>(p); }
@@ -295,14 +296,30 @@ template <> struct Block8<SrcBf16> {
   }
 };
 
-template <> struct Block8<SrcF32> {
-  float w[8][8];
+template <int W> struct Block8<SrcF32, W> {
+  typedef float run_t __attribute__((ext_vector_type(W < 4 ? W : 4)));
+  static constexpr int RUN = W < 4 ? W : 4;
+  float w[8][W];
   __device__ __forceinline__ void zero(int i) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) w[i][c] = 0.f;
+    for (int c = 0; c < W; ++c) w[i][c] = 0.f;
   }
-  __device__ __forceinline__ void load(int i, const float* p) { load8(p, w[i]); }
-  __device__ __forceinline__ void load(int i, const float* p, int valid) { load_f32x8(p, valid, w[i]); }
+  __device__ __forceinline__ void load(int i, const float* p) {
+#pragma unroll
+    for (int c = 0; c < W; c += RUN) {
+      const run_t v = *reinterpret_cast<const run_t*>(p + c);
+#pragma unroll
+      for (int e = 0; e < RUN; ++e) w[i][c + e] = v[e];
+    }
+  }
+  __device__ __forceinline__ void load(int i, const float* p, int valid) {
+    if (valid >= W) {
+      load(i, p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) w[i][e] = e < valid ? p[e] : 0.f;
+    }
+  }
   __device__ __forceinline__ void column(int c, bf16x8_t (&o)[3]) const {
     float v[8];
 #pragma unroll
@@ -311,7 +328,7 @@ template <> struct Block8<SrcF32> {
   }
 };
 
-template <> struct Block8<SrcI8> {
+template <> struct Block8<SrcI8, 8> {
   uint2 w[8];
   __device__ __forceinline__ void zero(int i) { w[i] = uint2{0u, 0u}; }
   __device__ __forceinline__ void load(int i, const int8_t* p) { w[i] = *reinterpret_cast<const uint2*>(p); }
@@ -341,8 +358,9 @@ struct DtArgs {
   float* part;  // [splits, m, R]
 };
 
-// The next chunk's dY and B are in flight while a chunk is multiplied (only B
-// where dY is fp32: its registers do not allow more).
+// The next chunk's dY and B are in flight while a chunk is multiplied; only B
+// where an fp32 dY's registers would leave one block less a compute unit (fp32 dY
+// and B, 4096 x 9216: 36 us with it and 40 without at rank 32, 56 and 48 at 64).
 template <typename SRC, typename TB, int R, int WR>
 __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t* bt) {
   typedef typename SRC::elem TY;
@@ -353,7 +371,7 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
   constexpr int WN = 4 / WR;             // waves that share a chunk
   constexpr int STEPS = NC / 32 / WN;    // 32-column steps of a wave and chunk
   constexpr int PLANE = R * PITCH;
-  constexpr bool AHEAD = PY == 1;
+  constexpr bool AHEAD = PY == 1 || (NC < DT_NC && R < 64);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g4 = lane >> 4;
   const int rg = wave % WR, ns = wave / WR;
@@ -364,14 +382,20 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
   const int64_t nchunks = (a.n + NC - 1) / NC;
   const int per_split = a.chunks_per_split * (DT_NC / NC);
   const int64_t c0 = (int64_t)split * per_split, c1 = min(c0 + per_split, nchunks);
-  // this thread's 8 x 8 block of a chunk of B
-  const int nb = threadIdx.x / (R / 8), jb = threadIdx.x % (R / 8);
+  // This thread's block of a chunk of B: 8 columns, 8 ranks of a bf16 B; of an fp32
+  // B, which costs a split into three parts, as few as give every thread one.
+  constexpr int W = PB == 1 ? 8 : R * NC / 8 / 256;
+  const int nb = threadIdx.x / (R / W), jb = threadIdx.x % (R / W);
   const bool stages = nb < NC / 8;
-  const int cols = max(0, min(8, a.r - 8 * jb));
-  const TB* bcol = (const TB*)a.b + (cols > 0 ? 8 * jb : 0);
+  const int cols = max(0, min(W, a.r - W * jb));
+  const TB* bcol = (const TB*)a.b + (cols > 0 ? W * jb : 0);
+
+  // Where a run of 8 columns stands in an LDS row: its number, exclusive or the
+  // rank / 8, so that the runs that a wave stores at a time fall on different banks.
+  const int swz[2] = {8 * (g4 ^ (l16 >> 3)), 8 * (g4 ^ (2 + (l16 >> 3)))};
 
   RawOp<TY> y[STEPS];
-  Block8<BSRC> bb;
+  Block8<BSRC, W> bb;
   auto load_y = [&](int64_t c) {
     const int64_t n0 = c * NC;
     if (n0 + NC <= a.n) {
@@ -409,12 +433,12 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
     __syncthreads();
     if (stages) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < W; ++e) {
         bf16x8_t o[PB];
         bb.column(e, o);
 #pragma unroll
         for (int p = 0; p < PB; ++p)
-          *reinterpret_cast<bf16x8_t*>(bt + p * PLANE + (8 * jb + e) * PITCH + 8 * nb) = o[p];
+          *reinterpret_cast<bf16x8_t*>(bt + p * PLANE + (W * jb + e) * PITCH + 8 * (nb ^ (W * jb >> 3))) = o[p];
       }
     }
     __syncthreads();
@@ -434,8 +458,8 @@ __device__ __forceinline__ void dt_block(const DtArgs& a, unsigned blk, uint16_t
         bf16x8_t bp[PB];
 #pragma unroll
         for (int p = 0; p < PB; ++p)
-          bp[p] = *reinterpret_cast<const bf16x8_t*>(bt + p * PLANE + (16 * f + l16) * PITCH + ns * (32 * STEPS) +
-                                                     32 * s + 8 * g4);
+          bp[p] = *reinterpret_cast<const bf16x8_t*>(bt + p * PLANE + (16 * f + l16) * PITCH +
+                                                     32 * ((ns * STEPS + s) ^ (f >> 1)) + swz[f & 1]);
         acc[f] = mfma_parts(yp, bp, acc[f]);
       }
     }
@@ -489,6 +513,7 @@ struct OuterArgs {
 template <int R> struct OuterShape {
   static constexpr int RB = R < OU_RB ? R : OU_RB;  // ranks of a block
   static constexpr int HALVES = R / RB;
+  static unsigned blocks(int64_t units) { return (unsigned)(HALVES > 1 ? (units + 7) / 8 * 8 * HALVES : units); }
   static constexpr int LDS = 4 * 2 * (RB / 16) * 64;  // f32x4: two columns' sums of four waves
 };
 
@@ -500,9 +525,14 @@ __device__ __forceinline__ void outer_block(const OuterArgs& a, unsigned blk, f3
   constexpr bool AHEAD = PS == 1;  // fp32 columns leave no registers for a second block
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int j0 = (int)(blk % HALVES) * RB;
-  const int split = (int)(blk / HALVES % (unsigned)a.splits);
-  const int64_t col0 = (int64_t)(blk / HALVES / (unsigned)a.splits) * OU_COLS, col = col0 + 8 * l16;
+  // Blocks go to the eight XCDs in turn: the halves of the ranks, which read the
+  // same columns, are eight apart, so that one L2 serves both (4096 x 9216 bf16 at
+  // rank 64: 30.0 us, 35.8 as neighbours).
+  const int j0 = HALVES > 1 ? (int)(blk / 8 % HALVES) * RB : 0;
+  const unsigned unit = HALVES > 1 ? blk / (8 * HALVES) * 8 + blk % 8 : blk;
+  const int split = (int)(unit % (unsigned)a.splits);
+  const int64_t col0 = (int64_t)(unit / (unsigned)a.splits) * OU_COLS, col = col0 + 8 * l16;
+  if (col0 >= a.width) return;  // (the units are made up to a multiple of eight)
   const int valid = (int)max((int64_t)0, min((int64_t)8, a.width - col));
   const bool inside = col0 + OU_COLS <= a.width;
   const TY* big = (const TY*)a.big + (valid > 0 ? col : 0);
@@ -868,8 +898,8 @@ hipError_t grad_r(const SideGradArgs& a, const SidePlan& p, hipStream_t stream) 
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const OuterArgs db{a.dy, a.lddy, a.n, t_planes, a.m, p.s2, p.cps2, p.nmc, a.ws + p.off2};
     const OuterArgs da{a.qa, a.ldqa, a.k, dt_planes, a.m, p.s3, p.cps3, p.nmc, a.ws + p.off3};
-    const unsigned nb_db = (unsigned)(p.cb2 * p.s2 * OuterShape<R>::HALVES);
-    const dim3 grid(nb_db + (unsigned)(p.cb3 * p.s3 * OuterShape<R>::HALVES)), block(256);
+    const unsigned nb_db = OuterShape<R>::blocks(p.cb2 * p.s2);
+    const dim3 grid(nb_db + OuterShape<R>::blocks(p.cb3 * p.s3)), block(256);
     if (a.dy_bf16)
       hipLaunchKernelGGL((k_side_outer<SrcBf16, R>), grid, block, 0, stream, db, da, nb_db);
     else
