@@ -537,7 +537,7 @@ tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t 
  *   workspace  tp_lora_down_prequantized_workspace_size(m, k, r) bytes, 16-byte
  *            aligned (partial sums over k; nothing is kept between calls).
  *   Products are exact, summed in fp32 in a fixed order, then scaled. m below
- *   2^27.
+ *   2^26.
  */
 size_t tp_lora_down_prequantized_workspace_size(int64_t m, int64_t k, int64_t r);
 tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float* sa, const void* lora_a,
@@ -570,7 +570,7 @@ tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float*
  *   workspace  tp_lora_grad_workspace_size(m, n, k, r) bytes, 16-byte aligned
  *            (partial sums; nothing is kept between calls).
  *   dt, da, db and the workspace must not overlap any other operand. m == 0 or
- *   n == 0 gives zeros for the sums over nothing. m and n below 2^27.
+ *   n == 0 gives zeros for the sums over nothing. m, n and k below 2^26.
  *   fp32 accuracy: operands that are not bf16 are split exactly into three bf16
  *   parts, the products are summed in fp32 in a fixed order. A part below
  *   2^-126 is lost, so fp32 values below about 2^-108 count with fewer bits.

@@ -832,7 +832,9 @@ tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t 
 
 namespace {
 
-constexpr int64_t SIDE_MAX = (int64_t)1 << 27;  // rows and columns: a launch counts its threads in 32 bits
+// Rows and columns: a launch counts its threads in 32 bits, and the most threads
+// an element (32 for a row's planes and for 64 ranks of a column of A) stay below.
+constexpr int64_t SIDE_MAX = (int64_t)1 << 26;
 
 tp_status check_rank(int64_t r) {
   if (r < 1 || r > 64) return fail(TP_ERR_BAD_SHAPE, "rank r=%lld outside [1, 64]", (long long)r);
@@ -852,7 +854,7 @@ tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float*
   if (!dtype_ok(a_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "a_dtype %d is not TP_F32 or TP_BF16", (int)a_dtype);
   TP_TRY(check_sizes(m, 0, k));
   TP_TRY(check_rank(r));
-  if (m >= SIDE_MAX) return fail(TP_ERR_BAD_SHAPE, "m=%lld: below 2^27", (long long)m);
+  if (m >= SIDE_MAX) return fail(TP_ERR_BAD_SHAPE, "m=%lld: below 2^26", (long long)m);
   const int64_t as = dtype_size(a_dtype);
   Extent eq, es, ea, et, ew;
   TP_TRY(check_matrix("qa", qa, m, k, ldqa, 1, &eq));
@@ -885,7 +887,7 @@ tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float*
 }
 
 size_t tp_lora_grad_workspace_size(int64_t m, int64_t n, int64_t k, int64_t r) {
-  if (m < 0 || n < 0 || m >= SIDE_MAX || n >= SIDE_MAX || k <= 0 || k % 256 != 0 || k > INT_MAX || r < 1 || r > 64)
+  if (m < 0 || n < 0 || m >= SIDE_MAX || n >= SIDE_MAX || k <= 0 || k % 256 != 0 || k >= SIDE_MAX || r < 1 || r > 64)
     return 0;
   return (size_t)(tp::side_grad_workspace_floats(m, n, k, r) * 4);
 }
@@ -900,8 +902,8 @@ tp_status tp_lora_grad_prequantized(const void* dy, tp_dtype dy_dtype, int64_t l
   if (a_flags != TP_A_ROTATE && a_flags != TP_A_PREROTATED) return fail(TP_ERR_BAD_FLAGS, "a_flags=%d", a_flags);
   TP_TRY(check_sizes(m, n, k));
   TP_TRY(check_rank(r));
-  if (m >= SIDE_MAX || n >= SIDE_MAX)
-    return fail(TP_ERR_BAD_SHAPE, "m=%lld, n=%lld: below 2^27 each", (long long)m, (long long)n);
+  if (m >= SIDE_MAX || n >= SIDE_MAX || k >= SIDE_MAX)
+    return fail(TP_ERR_BAD_SHAPE, "m=%lld, n=%lld, k=%lld: below 2^26 each", (long long)m, (long long)n, (long long)k);
   const int64_t ys = dtype_size(dy_dtype), bs = dtype_size(b_dtype);
   Extent edy, eq, es, et, eb, edt, eda, edb, ew;
   TP_TRY(check_matrix("dy", dy, m, n * ys, lddy, ys, &edy));

@@ -106,7 +106,7 @@ def dn(lib, q=A, ldq=512, s=B, a=C, adt=0, lda=512, m=64, k=512, r=16, t=D, tb=1
     (dict(q=0), 1), (dict(s=0), 1), (dict(a=0), 1), (dict(t=0), 1),
     (dict(ldq=511), 4), (dict(lda=500), 4), (dict(q=A + 8), 5), (dict(ldq=520), 5), (dict(a=C + 8), 5),
     (dict(s=B + 1), 5), (dict(t=D + 4), 5), (dict(adt=4), 6), (dict(tb=64 * 256 - 1), 9),
-    (dict(lda=2 ** 62), 8), (dict(t=A + 1024), 10), (dict(t=B), 10), (dict(t=C), 10), (dict(m=2 ** 27), 2),
+    (dict(lda=2 ** 62), 8), (dict(t=A + 1024), 10), (dict(t=B), 10), (dict(t=C), 10), (dict(m=2 ** 27), 2), (dict(m=2 ** 26), 2),
     (dict(ws=0), 9), (dict(wsb=16), 9), (dict(ws=E + 8), 5), (dict(ws=A), 10), (dict(ws=B), 10), (dict(ws=C), 10),
     (dict(ws=D), 10),
 ])
@@ -127,6 +127,7 @@ def gr(lib, dy=A, ydt=0, lddy=512, q=B, ldq=512, s=C, t=D, b=E, bdt=0, ldb=16, a
 @pytest.mark.parametrize("kw,status", [
     (dict(k=300), 3), (dict(k=0), 2), (dict(m=-1), 2), (dict(n=-1), 2), (dict(r=0), 2), (dict(r=65, ldb=68), 2),
     (dict(m=2 ** 27), 2), (dict(n=2 ** 27, lddy=2 ** 27), 2),
+    (dict(m=2 ** 26), 2), (dict(n=2 ** 26, lddy=2 ** 26), 2), (dict(k=2 ** 26, ldq=2 ** 26, ldda=2 ** 26), 2),
     (dict(dy=0), 1), (dict(q=0), 1), (dict(s=0), 1), (dict(t=0), 1), (dict(b=0), 1), (dict(dt=0), 1),
     (dict(da=0), 1), (dict(db=0), 1),
     (dict(lddy=511), 4), (dict(ldq=500), 4), (dict(ldb=15), 4), (dict(ldda=511), 4), (dict(lddb=15), 4),
@@ -144,14 +145,15 @@ def test_grad_refusals(lib, kw, status):
 
 def test_down_workspace_query(lib):
     assert lib.tp_lora_down_prequantized_workspace_size(64, 512, 16) > 0
-    for args in ((-1, 256, 4), (0, 256, 4), (8, 300, 4), (8, 0, 4), (8, 256, 0), (8, 256, 65), (2 ** 27, 256, 4)):
+    for args in ((-1, 256, 4), (0, 256, 4), (8, 300, 4), (8, 0, 4), (8, 256, 0), (8, 256, 65), (2 ** 27, 256, 4), (2 ** 26, 256, 4)):
         assert lib.tp_lora_down_prequantized_workspace_size(*args) == 0
 
 
 def test_grad_workspace_query(lib):
     assert lib.tp_lora_grad_workspace_size(64, 512, 512, 16) > 0
     for args in ((-1, 8, 256, 4), (8, -1, 256, 4), (8, 8, 300, 4), (8, 8, 0, 4), (8, 8, 256, 0), (8, 8, 256, 65),
-                 (2 ** 27, 8, 256, 4), (8, 2 ** 27, 256, 4)):
+                 (2 ** 27, 8, 256, 4), (8, 2 ** 27, 256, 4), (2 ** 26, 8, 256, 4), (8, 2 ** 26, 256, 4),
+                 (8, 8, 2 ** 26, 4)):
         assert lib.tp_lora_grad_workspace_size(*args) == 0
     assert lib.tp_lora_grad_workspace_size(0, 8, 256, 4) == 0  # sums over nothing
 
