@@ -482,7 +482,7 @@ tp_status tp_qgemm_w4a8_prequantized(const int8_t* qa, int64_t ldqa, const float
  *             pitch); any other overlap is refused. With residual NULL,
  *             sum_out must be NULL.
  *   gamma     [k], g_dtype, contiguous, 16-byte aligned; NULL: all ones.
- *   eps       positive and finite.
+ *   eps       within 1e-30 .. 1e30.
  *   k at most 16384 (a row sits in the registers of one workgroup). A row of
  *   zeros gives codes 0 and scale 0, or zeros.
  */
@@ -573,7 +573,8 @@ tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float*
  *   n == 0 gives zeros for the sums over nothing. m, n and k below 2^26.
  *   fp32 accuracy: operands that are not bf16 are split exactly into three bf16
  *   parts, the products are summed in fp32 in a fixed order. A part below
- *   2^-126 is lost, so fp32 values below about 2^-108 count with fewer bits.
+ *   2^-126 is lost, so fp32 values below about 2^-108 count with fewer bits; an
+ *   fp32 operand that bf16 rounds to infinity gives NaN.
  */
 size_t tp_lora_grad_workspace_size(int64_t m, int64_t n, int64_t k, int64_t r);
 tp_status tp_lora_grad_prequantized(const void* dy, tp_dtype dy_dtype, int64_t lddy, const int8_t* qa, int64_t ldqa,
@@ -607,7 +608,7 @@ tp_status tp_lora_grad_prequantized(const void* dy, tp_dtype dy_dtype, int64_t l
  *            NULL). head_dim a multiple of 8, at most 256; heads_q + heads_k at
  *            most 4096.
  *   q_gamma, k_gamma  [head_dim], g_dtype, contiguous, 16-byte aligned, or NULL
- *            (that tensor is not normed). eps positive and finite.
+ *            (that tensor is not normed). eps within 1e-30 .. 1e30.
  *   positions  int32 [m, axes], row pitch ldpos elements, 4-byte aligned; axes
  *            1..4. inv_freq fp32 [pairs].
  *   pair_axis  HOST array of `pairs` axis numbers below axes, read during the

@@ -672,8 +672,10 @@ tp_status tp_qgemm_w4a8_prequantized(const int8_t* qa, int64_t ldqa, const float
 
 namespace {
 
+// (below 1e-30 the factor of a row of zeros and its cube leave fp32: zeros would
+// come out as NaN)
 tp_status check_eps(double eps) {
-  if (!(eps > 0.0) || !(eps < 1e300)) return fail(TP_ERR_BAD_VALUE, "eps=%g is not positive and finite", eps);
+  if (!(eps >= 1e-30) || !(eps <= 1e30)) return fail(TP_ERR_BAD_VALUE, "eps=%g is not within 1e-30 .. 1e30", eps);
   return TP_OK;
 }
 

@@ -186,7 +186,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(RopeArgs a, int lanes, in
   const int u = threadIdx.x & (lanes - 1), g0 = threadIdx.x / lanes, groups = ROPE_THREADS / lanes;
   const Where w = where_of<HALVES>(u, d, a.pairs);
   const bool turned = w.pair < a.pairs;
-  const float inv_d = 1.0f / (float)d, eps = fmaxf((float)a.eps, 0x1p-126f);
+  const float inv_d = 1.0f / (float)d, eps = (float)a.eps;
   const int slice = (int)(blockIdx.x % (unsigned)slices);
   const int64_t first = (int64_t)(blockIdx.x / (unsigned)slices) * batch;
   const int64_t step = (int64_t)(gridDim.x / (unsigned)slices) * batch;

@@ -42,6 +42,7 @@ def nr(lib, x=A, xdt=0, ldx=512, res=B, ldr=512, sm=C, lds=512, sdt=0, g=D, gdt=
     (dict(xdt=2), 6), (dict(sdt=5), 6), (dict(gdt=-1), 6),
     (dict(kind=2), 11), (dict(fl=2), 11),
     (dict(eps=0.0), 13), (dict(eps=-1e-6), 13), (dict(eps=float("nan")), 13), (dict(eps=float("inf")), 13),
+    (dict(eps=9e-31), 13), (dict(eps=1.1e30), 13),
     (dict(ldx=2 ** 62), 8),
     (dict(y=A + 4096), 10), (dict(y=B), 10), (dict(y=C), 10), (dict(y=D), 10), (dict(sc=E + 64), 10),
     (dict(sc=A), 10), (dict(sm=D), 10), (dict(sm=B + 16), 10), (dict(sm=B, lds=516), 10), (dict(sm=A, sdt=1), 10),
@@ -72,7 +73,7 @@ def nb(lib, dy=A, ydt=0, lddy=512, fl=1, t=B, tdt=0, ldt=512, g=C, gdt=0, eps=1e
     (dict(dy=A + 8), 5), (dict(t=B + 2), 5), (dict(g=C + 4), 5), (dict(ds=D + 8), 5), (dict(dx=E + 8), 5),
     (dict(dg=F + 1), 5), (dict(ws=G + 8), 5),
     (dict(ydt=2), 6), (dict(tdt=2), 6), (dict(xdt=2), 6), (dict(gdt=2), 6),
-    (dict(fl=3), 11), (dict(eps=0.0), 13), (dict(ldt=2 ** 62), 8),
+    (dict(fl=3), 11), (dict(eps=0.0), 13), (dict(eps=1e-300), 13), (dict(ldt=2 ** 62), 8),
     (dict(ws=0), 9), (dict(wsb=100), 9),
     (dict(dx=B), 10), (dict(dx=C), 10), (dict(dx=A, ydt=1), 10), (dict(dx=A + 16), 10), (dict(dx=D, lddx=516), 10),
     (dict(dg=E), 10), (dict(dg=A), 10), (dict(ws=A), 10), (dict(ws=E), 10), (dict(ws=F), 10),
@@ -182,7 +183,7 @@ ROPE_SHARED = [
     (dict(d=0), 2), (dict(d=12), 2), (dict(d=264), 2), (dict(pairs=6), 2), (dict(pairs=68), 2), (dict(pairs=-4), 2),
     (dict(axes=0), 2), (dict(axes=5), 2), (dict(axes=2), 13), (dict(ax=None), 1), (dict(pos=0), 1), (dict(fr=0), 1),
     (dict(ldp=2), 4), (dict(pos=E + 2), 5), (dict(fr=F + 1), 5), (dict(qg=C + 8), 5), (dict(gdt=2), 6),
-    (dict(lay=2), 11), (dict(eps=0.0), 13), (dict(eps=float("nan")), 13),
+    (dict(lay=2), 11), (dict(eps=0.0), 13), (dict(eps=float("nan")), 13), (dict(eps=1e-38), 13),
 ]
 
 

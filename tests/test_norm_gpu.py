@@ -186,3 +186,35 @@ def test_norm_backward_in_place_unwanted_and_empty():
     assert dx.shape == (0, k) and torch.all(dg == 0)
     q, s = tp.tp_rmsnorm_rotate(empty, gamma)
     assert q.shape == (0, k) and s.shape == (0,)
+
+
+@pytest.mark.parametrize("m,k", [(9001, 256), (2700, 768), (2101, 1024)])
+def test_norm_backward_short_rows_share_blocks(m, k):
+    """More rows than all blocks take at a time, several of them a block."""
+    d = dev()
+    announce("tp_rmsnorm_rotate_backward short rows", m, k)
+    dy, t, ds = _draw(m, k, F32, seed=m, scale=0.02), _draw(m, k, BF16, seed=m + 1), _draw(m, k, BF16, seed=m + 2)
+    gamma = _gamma(k, F32, seed=k)
+    dx, dg = tp.tp_rmsnorm_rotate_backward(dy.to(d), t.to(d), gamma.to(d), dsum=ds.to(d))
+    want, bound, wdg, bdg = B.norm_backward(f64(dy), f64(t), f64(gamma), 1e-6, f64(ds), True, m + 64)
+    B.assert_close(f64(dx), want, bound, True, "dx")
+    B.assert_close(f64(dg), wdg, bdg, False, "dgamma")
+
+
+@pytest.mark.parametrize("m,k", [(40, 512), (600, 256), (30, 2048), (6, 8192)])
+def test_norm_backward_special_rows(m, k):
+    """Rows of zeros at the smallest eps, and non-finite rows beside others:
+    their gradients are their own."""
+    d = dev()
+    announce("tp_rmsnorm_rotate_backward special rows", m, k)
+    dy, t = _draw(m, k, F32, seed=m, scale=0.02), _draw(m, k, F32, seed=m + 1)
+    t[2] = 0.0
+    for eps in (1e-6, 1e-30):
+        dx, dg = tp.tp_rmsnorm_rotate_backward(dy.to(d), t.to(d), None, eps=eps)
+        want, bound, wdg, bdg = B.norm_backward(f64(dy), f64(t), None, eps, None, True, m + 64)
+        B.assert_close(f64(dx), want, bound, False, "dx")
+        B.assert_close(f64(dg), wdg, bdg, False, "dgamma")
+    t[1, 7], t[4, 100], dy[5, 200] = float("nan"), float("inf"), float("-inf")
+    bad, _ = tp.tp_rmsnorm_rotate_backward(dy.to(d), t.to(d), None, eps=1e-30)
+    keep = [i for i in range(m) if i not in (1, 4, 5)]
+    assert torch.equal(bad[keep], dx[keep])

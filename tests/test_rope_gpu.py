@@ -154,3 +154,25 @@ def test_columns_past_the_rotation_pass_anything():
         q, _ = tp.tp_qk_norm_rope(x.to(dv), x[:, :0].to(dv), d, pos.to(dv), freq.to(dv), axis, layout)
         assert torch.equal(q[:, 16:].cpu().view(torch.int32), x[:, 16:].contiguous().view(torch.int32))
         assert torch.all(torch.isfinite(q[:, :16]))
+
+
+def test_heads_of_zeros_at_the_smallest_eps():
+    dv = dev()
+    announce("tp_qk_norm_rope zero heads")
+    m, d = 5, 64
+    x, dy = _draw((m, 3 * d), F32, seed=1), _draw((m, 3 * d), F32, seed=2, scale=0.02)
+    x[3, d:2 * d] = 0.0
+    pos, freq, axis = _plan(m, 32, 1, seed=3, far=50)
+    g = _gamma(d, F32, 4)
+    how = dict(head_dim=d, positions=pos.to(dv), inv_freq=freq.to(dv), pair_axis=axis, q_gamma=g.to(dv), eps=1e-30)
+    xd, none = x.to(dv), x[:, :0].to(dv)
+    for odt in (F32, BF16):
+        y, _ = tp.tp_qk_norm_rope(xd, none, out_dtype=odt, **how)
+        want, bound = B.rope_forward(f64(x), d, pos.numpy(), freq.numpy(), axis, False, f64(g), 1e-30)
+        B.assert_close(f64(y), want, bound, odt == BF16, "out")
+        assert torch.all(y[3, d:2 * d] == 0)
+    dx, _, dg, _ = tp.tp_qk_norm_rope_backward(dy.to(dv), none, xd, none, **how)
+    want, bound, wdg, bdg = B.rope_backward(f64(dy), f64(x), d, pos.numpy(), freq.numpy(), axis, False, f64(g), 1e-30,
+                                            _adds(m, 3))
+    B.assert_close(f64(dx), want, bound, False, "dx")
+    B.assert_close(f64(dg), wdg, bdg, False, "dgamma")
