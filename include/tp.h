@@ -484,7 +484,9 @@ tp_status tp_qgemm_w4a8_prequantized(const int8_t* qa, int64_t ldqa, const float
  *   gamma     [k], g_dtype, contiguous, 16-byte aligned; NULL: all ones.
  *   eps       within 1e-30 .. 1e30.
  *   k at most 16384 (a row sits in the registers of one workgroup). A row of
- *   zeros gives codes 0 and scale 0, or zeros.
+ *   zeros gives codes 0 and scale 0, or zeros. Finite rows may be as large as
+ *   their type allows; for bf16 rows each product t gamma has to be within
+ *   fp32's range too.
  */
 tp_status tp_rmsnorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, const void* residual, int64_t ldr,
                             void* sum_out, int64_t ldsum, tp_dtype s_dtype, const void* gamma,
