@@ -515,7 +515,10 @@ tp_status tp_rmsnorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, const 
  *   dgamma    fp32 [k], or NULL (not wanted). m == 0 gives zeros.
  *   workspace tp_rmsnorm_backward_workspace_size(m, k) bytes, 16-byte aligned,
  *             where dgamma is wanted; not used otherwise.
- *   fp32 arithmetic and sums; dx rounded once. k at most 16384.
+ *   fp32 arithmetic, the two sums of a row in fp64; dx rounded once, dgamma
+ *   summed in fp32. Finite rows of any size, but from a root mean square of
+ *   2^126 on the low bits of rr are lost; gamma g has to be within fp32's
+ *   range. k at most 16384.
  */
 size_t tp_rmsnorm_backward_workspace_size(int64_t m, int64_t k);
 tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t lddy, int a_flags, const void* t,

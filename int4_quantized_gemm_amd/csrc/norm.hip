@@ -334,8 +334,10 @@ __global__ __launch_bounds__(NT, 4) void k_norm_rotate(NormArgs a, int rows_per_
 
 // ----------------------------------------------------------------- backward
 //   g = dy . blockdiag(H / 16) (the rotation is its own inverse), or dy
-//   dt = r gamma g - t r^3 mean(gamma g t) + dsum;   dgamma = sum over rows of g t r
-// in fp32. A thread keeps its 16 columns of dgamma over the rows of its block;
+//   n = t r;   dt = r (gamma g - n r mean(gamma g t)) + dsum;   dgamma = sum over rows of g n
+// in fp32, the two sums of a row in fp64: n, r mean(.) and the difference are of
+// the gradients' size for rows of any size (t r^3 mean(.) taken as such leaves
+// fp32 from rows of 1e21 on). A thread keeps its 16 columns of dgamma over the rows of its block;
 // the blocks' sums are joined by k_colsum in a fixed order. Bound by HBM (4096 x
 // 3072, fp32 dy, bf16 t, dsum and dx: 25.4 us, 5.0 TB/s, and 4.2 us for the join
 // of 512 partial rows). Rows of more than 16 groups with a block each (ONE) keep
@@ -403,12 +405,11 @@ __global__ __launch_bounds__(NT, NT == 768 ? 6 : 1) void k_norm_bwd(NormBwdArgs 
 #pragma unroll
       for (int i = 0; i < 16; ++i) g[i] *= 0.0625f;
     }
-    float c1 = 0.f;
-    double c2 = 0.0;
+    double c1 = 0.0, c2 = 0.0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const double td = (double)t[i];
-      c1 = fmaf(g[i] * gm[i], t[i], c1);
+      c1 = fma((double)(g[i] * gm[i]), td, c1);  // up to 2^256, as the squares
       c2 = fma(td, td, c2);
     }
     asm volatile("" : "+v"(c1), "+v"(c2));  // summed here
@@ -421,11 +422,11 @@ __global__ __launch_bounds__(NT, NT == 768 ? 6 : 1) void k_norm_bwd(NormBwdArgs 
       c1 += __shfl_xor(c1, 32);
       c2 += swz_xor<16>(c2);
       c2 += __shfl_xor(c2, 32);
-      if (lane == 0) rp[wave] = double2{(double)c1, c2};
+      if (lane == 0) rp[wave] = double2{c1, c2};
       first = 0;
       count = waves;
     } else if (pl.l16 == 0) {
-      rp[pl.set] = double2{(double)c1, c2};
+      rp[pl.set] = double2{c1, c2};
     }
     __syncthreads();
     if (!pl.active) {
@@ -440,12 +441,13 @@ __global__ __launch_bounds__(NT, NT == 768 ? 6 : 1) void k_norm_bwd(NormBwdArgs 
     }
     const double rd64 = 1.0 / sqrt(s2 * inv_k + a.eps);
     const float r = (float)rd64;
-    const float coef = (float)(rd64 * rd64 * rd64 * (s1 * inv_k));
+    const float mean = (float)(rd64 * (s1 * inv_k));
     float o[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      o[i] = fmaf(r, g[i] * gm[i], fmaf(-t[i], coef, d[i]));
-      dg[i] = ONE ? g[i] * r * t[i] : fmaf(g[i] * r, t[i], dg[i]);
+      const float n = t[i] * r;
+      o[i] = fmaf(r, fmaf(-n, mean, g[i] * gm[i]), d[i]);
+      dg[i] = ONE ? g[i] * n : fmaf(g[i], n, dg[i]);
     }
     if (live) store16((TD*)a.dx + row * a.lddx + col, o);
     if (ONE) break;

@@ -1,6 +1,7 @@
 """The norms at the far ends of fp32: rows whose elements are finite but whose
-sums would leave fp32's range if they were taken in the wrong order. The bounds
-are those of ordinary rows: nothing is allowed for the size of the values."""
+sums, factors or products of factors would leave fp32's range if they were taken
+in the wrong order. The bounds are those of ordinary rows: nothing is allowed for
+the size of the values."""
 
 import numpy as np
 import pytest
@@ -57,3 +58,50 @@ def test_norm_rows_at_the_end_of_the_range(k, dtype, rotate):
     want, bound = B.norm_rows(f64(x), f64(gamma), 1e-6, rotate)
     B.assert_close(f64(rows), want, bound, True, "rows of the stream")
     assert torch.equal(t.cpu(), x)
+
+
+def _scaled_rows(k, seed):
+    """Rows of every size: with a mean square from far below eps to 2^250."""
+    t = _normal((10, k), seed).numpy()
+    for i, s in enumerate((1.0, 1e-25, 1e-12, 1e6, 1e18, 1e21, 1e23, 1e30, 1e36, 1.0)):
+        t[i] *= np.float32(s)
+    t[8] = np.clip(t[8], -3e36, 3e36)
+    return torch.from_numpy(t)
+
+
+@pytest.mark.parametrize("m,k", [(10, 256), (10, 1024), (10, 4352)])
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("eps", [1e-6, 1e-30])
+def test_norm_backward_of_rows_of_any_size(m, k, rotate, eps):
+    """dx row by row. dgamma too: column sums over rows whose factors are as far
+    apart as 1e25 and 1e-36, which weigh the same in it."""
+    d = dev()
+    announce("tp_rmsnorm_rotate_backward rows of any size", m, k, rotate, eps)
+    t, dy, gamma = _scaled_rows(k, k), _normal((m, k), k + 1) * 1e-3, 1.0 + 0.1 * _normal((k,), k + 2)
+    for gam in (None, gamma):
+        g64 = None if gam is None else f64(gam)
+        dx, dg = tp.tp_rmsnorm_rotate_backward(dy.to(d), t.to(d), None if gam is None else gam.to(d), eps=eps,
+                                               rotate=rotate)
+        want, bound, wdg, bdg = B.norm_backward(f64(dy), f64(t), g64, eps, None, rotate, m + 64)
+        B.assert_close(f64(dx), want, bound, False, "dx")
+        B.assert_close(f64(dg), wdg, bdg, False, "dgamma")
+        # a gradient of the stream beside it
+        ds = _normal((m, k), k + 3)
+        dx, _ = tp.tp_rmsnorm_rotate_backward(dy.to(d), t.to(d), None if gam is None else gam.to(d), eps=eps,
+                                              dsum=ds.to(d), rotate=rotate)
+        want, bound, _, _ = B.norm_backward(f64(dy), f64(t), g64, eps, f64(ds), rotate, m + 64)
+        B.assert_close(f64(dx), want, bound, False, "dx with dsum")
+
+
+@pytest.mark.parametrize("m,k", [(10, 768), (10, 4352)])
+def test_norm_backward_of_large_rows_and_gradients(m, k):
+    """Products of large rows with ordinary and with large gradients: the sum of
+    gamma g t is past fp32 where dx is not."""
+    d = dev()
+    announce("tp_rmsnorm_rotate_backward large rows and gradients", m, k)
+    t, dy = _scaled_rows(k, k + 4), _normal((m, k), k + 5)
+    dy[5:] *= 1e6
+    dx, dg = tp.tp_rmsnorm_rotate_backward(dy.to(d), t.to(d), None)
+    want, bound, wdg, bdg = B.norm_backward(f64(dy), f64(t), None, 1e-6, None, True, m + 64)
+    B.assert_close(f64(dx), want, bound, False, "dx")
+    B.assert_close(f64(dg), wdg, bdg, False, "dgamma")
