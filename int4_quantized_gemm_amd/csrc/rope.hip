@@ -279,13 +279,16 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(RopeArgs a, int lanes, in
 #pragma unroll
           for (int e = 0; e < 4; ++e) s = fmaf(o.a[e] * gm.a[e], x.a[e], fmaf(o.b[e] * gm.b[e], x.b[e], s));
           s = group_sum(s, lanes);
-          const float coef = s * inv_d * r * r * r, count = live ? r : 0.f;
+          // n = x r and r mean(gamma g x) are of the gradients' size; r^3 alone leaves
+          // fp32 where the head's squares still fit
+          const float mean = s * inv_d * r, rl = live ? r : 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sg.a[e] = fmaf(o.a[e] * count, x.a[e], sg.a[e]);
-            sg.b[e] = fmaf(o.b[e] * count, x.b[e], sg.b[e]);
-            o.a[e] = fmaf(o.a[e] * gm.a[e], r, -x.a[e] * coef);
-            o.b[e] = fmaf(o.b[e] * gm.b[e], r, -x.b[e] * coef);
+            const float na = x.a[e] * rl, nb = x.b[e] * rl;
+            sg.a[e] = fmaf(o.a[e], na, sg.a[e]);
+            sg.b[e] = fmaf(o.b[e], nb, sg.b[e]);
+            o.a[e] = fmaf(-na, mean, o.a[e] * gm.a[e]) * r;
+            o.b[e] = fmaf(-nb, mean, o.b[e] * gm.b[e]) * r;
           }
         }
       }

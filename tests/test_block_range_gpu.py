@@ -105,3 +105,28 @@ def test_norm_backward_of_large_rows_and_gradients(m, k):
     want, bound, wdg, bdg = B.norm_backward(f64(dy), f64(t), None, 1e-6, None, True, m + 64)
     B.assert_close(f64(dx), want, bound, False, "dx")
     B.assert_close(f64(dg), wdg, bdg, False, "dgamma")
+
+
+@pytest.mark.parametrize("hd,pairs,layout", [(64, 32, "interleaved"), (80, 16, "halves"), (256, 128, "halves")])
+def test_rope_backward_of_large_and_small_heads(hd, pairs, layout):
+    """Heads whose squares add up just inside fp32, with small gradients: the
+    cube of the head's factor is far below fp32's range, dx is not."""
+    d = dev()
+    announce("tp_qk_norm_rope_backward large heads", hd, pairs, layout)
+    m, heads = 6, 5
+    w = heads * hd
+    x, dy = _normal((m, w), hd).numpy(), _normal((m, w), hd + 1) * 1e-6
+    for i, s in enumerate((1.0, 1e12, 1e16, 6e17, 1e-12, 1.0)):
+        x[i] *= np.float32(s)
+    x = torch.from_numpy(x)
+    rng = np.random.default_rng(hd)
+    pos = torch.from_numpy(rng.integers(-50, 50, size=(m, 1)).astype(np.int32))
+    freq = torch.from_numpy((100.0 ** (-np.arange(pairs) / pairs)).astype(np.float32))
+    gamma = 1.0 + 0.1 * _normal((hd,), hd + 2)
+    none = x[:, :0].to(d)
+    dx, _, dg, _ = tp.tp_qk_norm_rope_backward(dy.to(d), none, x.to(d), none, hd, pos.to(d), freq.to(d), None, layout,
+                                               gamma.to(d), eps=1e-5)
+    want, bound, wdg, bdg = B.rope_backward(f64(dy), f64(x), hd, pos.numpy(), freq.numpy(), [0] * pairs,
+                                            layout == "halves", f64(gamma), 1e-5, m * heads + 400)
+    B.assert_close(f64(dx), want, bound, False, "dx")
+    B.assert_close(f64(dg), wdg, bdg, False, "dgamma")
