@@ -325,6 +325,23 @@ def _heads(t, name, m, head_dim, dtype=None):
     return ld, width, width // head_dim
 
 
+def _axis_bytes(pair_axis, pairs):
+    """The axis of each pair, a byte each. Integers one by one: bytes() of an
+    array is its memory, and of a number that many zeros."""
+    if pair_axis is None:
+        return bytes(pairs)
+    if type(pair_axis) is not bytes:
+        try:
+            pair_axis = bytes(list(pair_axis))
+        except TypeError as e:
+            raise TypeError("pair_axis must be a sequence of integers") from e
+        except (ValueError, OverflowError) as e:
+            raise ValueError("pair_axis must hold axis numbers") from e
+    if len(pair_axis) != pairs:
+        raise ValueError(f"pair_axis must have {pairs} entries, got {len(pair_axis)}")
+    return pair_axis
+
+
 def _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_gamma, eps):
     """The arguments that forward and backward share, in the C order."""
     if layout not in _LAYOUT:
@@ -344,9 +361,7 @@ def _rope_args(m, head_dim, positions, inv_freq, pair_axis, layout, q_gamma, k_g
         positions = positions[:, None]
     ldpos = _mat(positions, "positions", m, dtype=torch.int32)
     _vec(inv_freq, "inv_freq", pairs, torch.float32)
-    axis = pair_axis if type(pair_axis) is bytes else bytes(pairs) if pair_axis is None else bytes(pair_axis)
-    if len(axis) != pairs:
-        raise ValueError(f"pair_axis must have {pairs} entries, got {len(axis)}")
+    axis = _axis_bytes(pair_axis, pairs)
     return (qg, kg, g_dt, eps, positions.data_ptr(), ldpos, positions.shape[1], inv_freq.data_ptr(), axis, pairs,
             _LAYOUT[layout])
 
