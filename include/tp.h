@@ -541,8 +541,11 @@ tp_status tp_rmsnorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t 
  *   t        as in tp_lora_down.
  *   workspace  tp_lora_down_prequantized_workspace_size(m, k, r) bytes, 16-byte
  *            aligned (partial sums over k; nothing is kept between calls).
- *   Products are exact, summed in fp32 in a fixed order, then scaled. m below
- *   2^26.
+ *   Products of the codes with a bf16 lora_a, or with the three bf16 parts that an
+ *   fp32 one is split into, are exact; they are summed in fp32 in a fixed order,
+ *   then scaled. A part below 2^-126 is lost, so fp32 values below about 2^-108
+ *   count with fewer bits; an fp32 value that bf16 rounds to infinity gives NaN.
+ *   m below 2^26.
  */
 size_t tp_lora_down_prequantized_workspace_size(int64_t m, int64_t k, int64_t r);
 tp_status tp_lora_down_prequantized(const int8_t* qa, int64_t ldqa, const float* sa, const void* lora_a,

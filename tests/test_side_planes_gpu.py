@@ -120,6 +120,29 @@ def test_gradients_of_one_product_each(m, n, k, r, ydt, bdt):
     _check(f64(db), a32 * (f64(dy).T @ f64(t)[:, :r]), TWO_SPLITS if ydt == F32 else ONE_SPLIT, "dB")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [5, 40, 130])
+@pytest.mark.parametrize("r", [8, 64])
+def test_down_at_the_ends_of_an_fp32_operand(m, r):
+    """Values of 2^-100, whose third part is still a normal number, count in full;
+    one that bf16 rounds to infinity makes its own rank NaN and no other."""
+    d = dev()
+    announce("tp_lora_down_prequantized ends of fp32", m, r)
+    k = 512
+    qa, _ = _sparse_codes(m, k, m, False)
+    sa = torch.ones(m)
+    a = _values((r, k), F32, r)
+    small = (a * 2.0 ** -100).contiguous()
+    t = tp.tp_lora_down_prequantized(qa.to(d), sa.to(d), small.to(d))
+    _check(f64(t)[:, :r], f64(qa) @ f64(small).T, ONE_SPLIT, "T")
+    whole = tp.tp_lora_down_prequantized(qa.to(d), sa.to(d), a.contiguous().to(d))
+    large = a.contiguous()
+    large[r // 2, 3] = 3.4e38
+    t = tp.tp_lora_down_prequantized(qa.to(d), sa.to(d), large.to(d))
+    keep = [j for j in range(64) if j != r // 2]
+    assert torch.all(torch.isnan(t[:, r // 2])) and torch.equal(t[:, keep], whole[:, keep])
+
+
 # ----------------------------------------------------------- planted on the CPU
 def _bf16(v):
     return torch.from_numpy(v.astype(np.float32)).to(BF16).double().numpy()
