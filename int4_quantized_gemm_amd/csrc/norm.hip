@@ -1,6 +1,7 @@
 // Residual addition, RMS norm and rotation of whole rows in front of a
-// projection, and their gradients (the row kernels around the projections that
-// the TensorFold pull request #948 lists: RMSNorm and the gated residual).
+// projection, and their gradients (the TensorFold pull request #948 lists
+// RMSNorm and the residual among the row kernels around the projections; the
+// residual here is the plain sum, without a gate or modulation).
 //
 //   t  = stream(x + residual), or x          r = (mean(t^2) + eps)^(-1/2)
 //   h  = t r gamma                           h' = h . blockdiag(H / 16)
@@ -164,9 +165,11 @@ __device__ __forceinline__ bool reaches(uint64_t lanes, int lane) { return ((lan
 // t gamma is exact in fp64, nothing is rounded to a shorter type in between).
 // bf16: fp32 arithmetic, one rounding.
 //
-// Bound by HBM for the bf16 rows (4096 x 3072, bf16 in and stream: 18.6 us, 5.4
+// Bound by HBM for the bf16 rows (4096 x 3072, bf16 in and stream: 18.8 us, 5.3
 // TB/s) and by fp64 issue plus the row's chain (load, transpose, two joins, two
-// divisions) for the codes (4032 x 3072, fp32 in, bf16 stream: 24.9 us, 4.5 TB/s).
+// divisions) for the codes (4032 x 3072, fp32 in, bf16 stream: 24.7 us, 4.5 TB/s;
+// 4096 x 8192 58.6 us, 5.1 TB/s; 1024 x 12288, whose 112 KiB of LDS leave one block a
+// compute unit, 31.8 us, 3.6 TB/s).
 template <typename TX, typename TS, bool RES, int OUT, int NT>
 __global__ __launch_bounds__(NT, 4) void k_norm_rotate(NormArgs a, int rows_per_block) {
   typedef typename std::conditional<OUT == NORM_OUT_I8, double, float>::type T;
@@ -339,9 +342,15 @@ __global__ __launch_bounds__(NT, 4) void k_norm_rotate(NormArgs a, int rows_per_
 // the gradients' size for rows of any size (t r^3 mean(.) taken as such leaves
 // fp32 from rows of 1e21 on). A thread keeps its 16 columns of dgamma over the rows of its block;
 // the blocks' sums are joined by k_colsum in a fixed order. Bound by HBM (4096 x
-// 3072, fp32 dy, bf16 t, dsum and dx: 25.4 us, 5.0 TB/s, and 4.2 us for the join
+// 3072, fp32 dy, bf16 t, dsum and dx: 25.7 us, 4.9 TB/s, and 4.7 us for the join
 // of 512 partial rows). Rows of more than 16 groups with a block each (ONE) keep
-// no sums, so that two of 768 threads share a compute unit.
+// no sums, so that two of 768 threads share a compute unit; their partial rows,
+// one a row, are written and read besides (333 x 12288 fp32: 15.7 us and 4.4 for
+// the join). A stream gradient does not fit there: those forms spill 4 to 14 of
+// their 80 registers (the same with it 21.8 and 4.4 us, 3.0 TB/s), and the ones
+// of several wide rows a block 2 to 8 of 128 (bf16 with it, 4096 x 5120: 36.4 us,
+// 4.6 TB/s; 4096 x 8192: 49.8 us, 5.4 TB/s; 1000 x 12288 with an fp32 dy: 34.1 us,
+// 3.6 TB/s).
 template <typename TG, typename TT, typename TD, bool DS, int NT, bool ONE>
 __global__ __launch_bounds__(NT, NT == 768 ? 6 : 1) void k_norm_bwd(NormBwdArgs a, int rows_per_block) {
   constexpr int SET_BYTES = 16 * (16 + 4) * 4;
@@ -518,7 +527,11 @@ Shape shape_of(int64_t m, int groups, int64_t max_blocks) {
   return s;
 }
 
-constexpr int64_t NORM_BLOCKS = 65536;  // blocks walk rows beyond that many
+constexpr int64_t NORM_BLOCKS = 65536;  // blocks walk rows beyond that many (threads of a grid in 32 bits)
+// More blocks hide more of a row's chain, fewer write fewer partial rows of dgamma.
+// bf16 with dsum, the join included: 4096 x 3072 28.4 us, 36.2 with 256 blocks, 30.3
+// with 1024; 12288 x 1024 27.7, 30.1, 32.2; 1024 x 3072 13.5, 14.2, 15.4. Wide rows
+// alone would do with 256 (1000 x 12288, fp32 dy: 40.8, 35.8, 49.6).
 constexpr int64_t NORM_BWD_BLOCKS = 512;
 
 template <typename TX, typename TS, bool RES, int OUT>
@@ -549,7 +562,8 @@ hipError_t norm_x(const NormArgs& a, hipStream_t stream) {
 // however many rows share it, and blocks of one short row leave compute units
 // idle. 49152 x 256 bf16: 24.6 us with dgamma's join, 44.5 with blocks of 64
 // threads and a partial row each; 12288 x 1024: 23.4 and 42.7. Few rows are spread
-// over more blocks.
+// over at least 256 blocks, one a compute unit (256 x 1024: 6.5 us, 8.4 over 128;
+// 1024 x 1024: 8.4, 9.8 over 512).
 Shape bwd_shape_of(int64_t m, int groups) {
   Shape s;
   int64_t rows = groups <= 16 ? 16 / groups : 1;

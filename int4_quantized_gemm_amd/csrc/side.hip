@@ -797,7 +797,13 @@ __global__ __launch_bounds__(1024) void k_side_join(const float* __restrict__ pb
 namespace {
 
 // How the sums are split: enough blocks for the chip, as few partial sums as
-// that allows.
+// that allows. Up to 16 rows a block's waves share a chunk, beyond that each takes
+// 16 rows: whole gradients of 8 rows 15.9 us at n 9216, k 3072, rank 32 (16.3 with
+// 64-row blocks), 14.0 at n 1160, k 1280, rank 8, fp32 (15.4). The border stands where
+// 16-row blocks begin to read B twice; up to 64 rows they would still be the faster
+// ones by 0.6 to 1.4 us (64 rows: 17.6 and 18.2 us, at n 1160 15.0 and 16.4).
+// dT's target of 768 blocks, 512 and 1024 beside it: 4096 rows bf16 49.6 us, 49.3,
+// 49.6; all fp32 at rank 64 113.0, 116.7, 112.9; an fp32 B at rank 64 71.1, 76.1, 71.0.
 struct SidePlan {
   int wr;                        // row groups of a dt block
   int64_t rb, nchunks;           // row blocks, 256-column chunks (dt)
@@ -835,7 +841,9 @@ SidePlan side_plan(int64_t m, int64_t n, int64_t k, int64_t r) {
   p.cb2 = (n + OU_COLS - 1) / OU_COLS;
   p.cb3 = (k + OU_COLS - 1) / OU_COLS;
   // Two blocks a compute unit are resident: dB's and dA's together are made to
-  // fit in that once. A split is at least a chunk for each of the four waves.
+  // fit in that once (4096 rows bf16 49.6 us; 48.5 with 256 blocks and 51.2 with
+  // 1024; fp32 dY at 3072 columns and rank 16 34.3, 36.2, 36.7; all fp32 at rank 64 and
+  // 2048 rows 70.2, 75.7, 70.1). A split is at least a chunk for each of the four waves.
   const int64_t quads = (p.nmc + 3) / 4, want = 512 / ((p.cb2 + p.cb3) * (R > OU_RB ? R / OU_RB : 1));
   split_of(n > 0 ? quads : 0, want, &p.s2, &p.cps2);
   split_of(quads, want, &p.s3, &p.cps3);
@@ -857,6 +865,14 @@ struct DownPlan {
   int64_t total;  // floats
 };
 
+// Up to 16 rows the waves of a block share a chunk (one row of 12288 columns at rank
+// 32 5.5 us, 6.0 with 64-row blocks; 16 rows 6.4, 7.0; 17 to 64 rows would take 0.5 to
+// 0.7 us less that way too). Blocks of 128 rows stage A half as often as blocks of
+// 64, which pays where A's three planes are long: 4096 rows of 3072 columns, fp32 A
+// of 64 ranks, 15.3 and 16.7 us. The rule goes by rows alone; with a bf16 A blocks
+// of 64 rows are the faster ones (4096 x 12288 at rank 32 16.6 with blocks of 128 and
+// 13.5 with blocks of 64, 128 rows 9.2 and 7.7). Target 512
+// blocks, 256 and 1024 beside it: 2048 x 12288 13.2 us, 12.1, 13.2; 4096 16.6, 16.5, 17.0.
 DownPlan down_plan(int64_t m, int64_t k, int64_t r) {
   DownPlan p;
   p.wr = m > 16 ? 4 : 1;
