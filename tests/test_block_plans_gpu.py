@@ -1,5 +1,5 @@
-"""Every form that the operators around the projections are launched in, against
-the fp64 oracle: few rows at every padded rank (the waves of a block share a
+"""Forms of the operators around the projections that the tests of each operator
+leave out, against the fp64 oracle: few rows at every padded rank (the waves of a block share a
 chunk), several tokens a block with a ragged last batch, blocks that walk rows
 or tokens beyond the largest grid, and wide rows of which a block takes several.
 """

@@ -60,6 +60,23 @@ def test_norm_rows_at_the_end_of_the_range(k, dtype, rotate):
     assert torch.equal(t.cpu(), x)
 
 
+@pytest.mark.parametrize("k", [256, 512, 768, 1024, 4352])
+@pytest.mark.parametrize("rotate", [True, False])
+def test_rows_beside_large_and_non_finite_rows_keep_their_bytes(k, rotate):
+    """Rows that share a wave or a block with rows at the end of the range, or
+    with infinities and NaN, are the rows that they are alone."""
+    d = dev()
+    announce("tp_rmsnorm_rotate beside large rows", k, rotate)
+    x = _normal((41, k), k + 9)
+    gamma = (1.0 + 0.1 * _normal((k,), k + 1)).to(d)
+    want = tp.tp_rmsnorm_rotate(x.to(d), gamma, out_kind="bf16", rotate=rotate)
+    bad = x.clone()
+    bad[1], bad[6, 3], bad[11, 5], bad[16, 7], bad[22] = 3e38, float("inf"), float("nan"), float("-inf"), -2e37
+    got = tp.tp_rmsnorm_rotate(bad.to(d), gamma, out_kind="bf16", rotate=rotate)
+    keep = [i for i in range(41) if i not in (1, 6, 11, 16, 22)]
+    assert torch.equal(got[keep].view(torch.int16), want[keep].view(torch.int16))
+
+
 def _scaled_rows(k, seed):
     """Rows of every size: with a mean square from far below eps to 2^250."""
     t = _normal((10, k), seed).numpy()
