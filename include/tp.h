@@ -665,6 +665,172 @@ tp_status tp_qk_norm_rope_backward(const void* dq_out, int64_t lddqo, const void
                                    void* dk, int64_t lddk, tp_dtype dx_dtype, float* dq_gamma, float* dk_gamma,
                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* A dropout (tp_dropout, tp_layernorm_rotate and its backward pass):
+ *
+ *   drop(x)[r, j] = fp32(x[r, j] * f) where the element is kept, 0 where not
+ *
+ *   drop_p   the probability of dropping, 0 .. 1, taken as T / 65536 with
+ *            T = round(65536 drop_p); f = fp32(65536 / (65536 - T)), so the mean
+ *            is kept exactly; T = 65536 drops everything.
+ *   rng      DEVICE memory of two 64-bit numbers, the seed and the offset
+ *            (8-byte aligned; not read, and may be NULL, where drop_p is 0). They
+ *            are read when the kernel runs: a captured graph draws a new mask
+ *            once the caller has changed them.
+ *   The mask is Philox4x32-10 (Salmon and others, 2011), computed where it is
+ *   needed and stored nowhere. Key: seed (low half first); counter: the 64-bit
+ *   number R of a run of eight elements of a row, R = r ceil(k / 8) + j / 8,
+ *   then the offset. Element j of the row takes bits 16 (j % 2) .. + 15 of word
+ *   (j % 8) / 2 and is kept where they are at least T. The same seed, offset, k
+ *   and drop_p give the same mask in every entry point, whatever the pitches;
+ *   calls that need different masks need different offsets (or seeds).
+ */
+
+/*
+ * tp_dropout -- y = drop(x) + residual, the dropout of a block's branch (the
+ * residual among the row kernels around the projections: TensorFold pull request
+ * #948, first comment). The same call without a residual, on the gradient of y,
+ * is its backward pass.
+ *
+ *   x        [m, k], x_dtype, row pitch ldx; any k.
+ *   residual NULL, or [m, k], y_dtype, row pitch ldr.
+ *   y        [m, k], y_dtype, row pitch ldy; may be x or residual itself (same
+ *            pointer, type and pitch); any other overlap is refused.
+ *   fp32 arithmetic, rounded once to y_dtype.
+ */
+tp_status tp_dropout(const void* x, tp_dtype x_dtype, int64_t ldx, const void* residual, int64_t ldr, double drop_p,
+                     const uint64_t* rng, int64_t m, int64_t k, void* y, tp_dtype y_dtype, int64_t ldy,
+                     hipStream_t stream);
+
+/* out_kind of tp_layernorm_rotate, beside TP_NORM_OUT_I8 and TP_NORM_OUT_BF16. */
+#define TP_NORM_OUT_FP8 2 /* e4m3 codes [m, k] and fp32 scales [k / 128, m], as tp_quantize_fp8 */
+
+/*
+ * tp_layernorm_rotate -- tp_rmsnorm_rotate with a layer norm, a bias and the
+ * dropout of the branch, and with 8-bit float codes among its outputs:
+ *
+ *   t[r, j]   residual given: fp32(drop(x) + residual) rounded once more (nearest
+ *             even) to s_dtype, which is what sum_out holds; else x itself
+ *             (drop_p has to be 0 then).
+ *   h[r, j]   (t[r, j] - mean_j(t)) / sqrt(mean_j((t - mean)^2) + eps) * gamma[j]
+ *             + beta[j]
+ *   y         a_flags TP_A_ROTATE: h . blockdiag(Q); TP_A_PREROTATED: h.
+ *             TP_NORM_OUT_I8 and TP_NORM_OUT_BF16 as in tp_rmsnorm_rotate.
+ *             TP_NORM_OUT_FP8: e4m3 [m, k] (row pitch ldy bytes) and scales fp32
+ *             [k / 128, m] (row pitch ldscales elements), the codes and scales
+ *             that tp_quantize_fp8 with block_rows 1 defines for these rows.
+ *             Codes are those of fp64 arithmetic throughout.
+ *
+ *   gamma, beta  [k], g_dtype, contiguous, 16-byte aligned; NULL: all ones, all
+ *             zeros.
+ *   The other arguments as in tp_rmsnorm_rotate; ldscales is used for
+ *   TP_NORM_OUT_FP8 only. For bf16 rows h has to be within fp32's range.
+ */
+tp_status tp_layernorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, const void* residual, int64_t ldr,
+                              void* sum_out, int64_t ldsum, tp_dtype s_dtype, const void* gamma, const void* beta,
+                              tp_dtype g_dtype, double eps, double drop_p, const uint64_t* rng, int a_flags, int64_t m,
+                              int64_t k, int out_kind, void* y, int64_t ldy, float* scales, int64_t ldscales,
+                              hipStream_t stream);
+
+/*
+ * tp_layernorm_rotate_backward -- the gradients of tp_layernorm_rotate, the
+ * quantization taken as the identity (straight through):
+ *
+ *   g         a_flags TP_A_ROTATE: dy . blockdiag(Q); TP_A_PREROTATED: dy.
+ *   n[r, j]   (t[r, j] - mean_j(t)) rr,  rr = 1 / sqrt(mean_j((t - mean)^2) + eps)
+ *   w         gamma g
+ *   dx        rr (w - mean_j(w) - n mean_j(w n)) + dsum   (the residual's gradient)
+ *   dbranch   drop(dx), before dx is rounded               (x's gradient)
+ *   dgamma[j] sum_r g[r, j] n[r, j]       dbeta[j]  sum_r g[r, j]
+ *
+ *   dy        [m, k], dy_dtype, row pitch lddy.
+ *   t         [m, k], t_dtype, row pitch ldt: the forward's sum_out (or x).
+ *   dsum      NULL, or [m, k], dx_dtype, row pitch ldds: the gradient that
+ *             reaches the residual stream from behind.
+ *   drop_p, rng  the forward's. dbranch NULL: not wanted (without a dropout it
+ *             would be dx).
+ *   dx        [m, k], dx_dtype, row pitch lddx; may be dsum or dy itself (same
+ *             pointer, type and pitch); any other overlap is refused.
+ *   dbranch   [m, k], dx_dtype, row pitch lddb; overlaps nothing.
+ *   dgamma, dbeta  fp32 [k], each NULL where it is not wanted. m == 0 gives zeros.
+ *   workspace tp_layernorm_backward_workspace_size(m, k) bytes, 16-byte aligned,
+ *             where dgamma or dbeta is wanted; not used otherwise.
+ *   fp32 arithmetic, the sums of a row and the deviations in fp64; dx and dbranch
+ *   rounded once, dgamma and dbeta summed in fp32 in a fixed order. gamma g has to
+ *   be within fp32's range; from a deviation of 2^126 on the low bits of rr are
+ *   lost. k at most 16384.
+ */
+size_t tp_layernorm_backward_workspace_size(int64_t m, int64_t k);
+tp_status tp_layernorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t lddy, int a_flags, const void* t,
+                                       tp_dtype t_dtype, int64_t ldt, const void* gamma, tp_dtype g_dtype, double eps,
+                                       const void* dsum, int64_t ldds, double drop_p, const uint64_t* rng, int64_t m,
+                                       int64_t k, void* dx, tp_dtype dx_dtype, int64_t lddx, void* dbranch,
+                                       int64_t lddb, float* dgamma, float* dbeta, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * tp_quantize_fp8 -- codes in 8-bit floating point (e4m3: 4 exponent bits of bias
+ * 7, 3 mantissa bits, subnormals, largest value 448) with an fp32 scale for each
+ * block of 128, for tp_qgemm_fp8 (tensai docs, "画像生成", section "GPU": the
+ * device quantizes each product's activations more finely):
+ *
+ *   s     fp32(amax / 448) over the block, 0 for a block of zeros
+ *   code  e4m3(x / s): nearest even, at most 448 in magnitude; 0 where s is 0
+ *
+ *   x        [m, k], x_dtype, row pitch ldx; a_flags TP_A_ROTATE: its rows are
+ *            rotated first (k a multiple of 256), TP_A_PREROTATED: any k.
+ *   With kp and mp standing for k and m rounded up to multiples of 128:
+ *   block_rows 1: for a product that sums over k
+ *     q        [m, kp], row pitch ldq bytes; zeros from column k on.
+ *     scales   [kp / 128, m], row pitch ldscales elements: scales[g, r] is that of
+ *              columns 128 g .. of row r.
+ *   and for one that sums over m (a weight's gradient):
+ *     qt       [k, mp], row pitch ldqt bytes: the transposed codes, zeros from
+ *              column m on.
+ *     scales_t [mp / 128, k], row pitch ldscales_t: scales_t[g, c] is that of rows
+ *              128 g .. of column c.
+ *   block_rows 128: a scale for each block of 128 x 128 (weights)
+ *     q        as above;  scales   [mp / 128, kp / 128], row pitch ldscales.
+ *     qt       the same codes transposed;  scales_t [kp / 128, mp / 128].
+ *   q with scales, or qt with scales_t, may be NULL: not wanted; not all of them.
+ *   Exact arithmetic (fp64 on x, on its rotation where that is exact). Code
+ *   matrices have 16-byte aligned rows, scales are 4-byte aligned. m and k below
+ *   2^26, m k at most 2^36.
+ */
+tp_status tp_quantize_fp8(const void* x, tp_dtype x_dtype, int64_t ldx, int64_t m, int64_t k, int a_flags,
+                          int block_rows, uint8_t* q, int64_t ldq, float* scales, int64_t ldscales, uint8_t* qt,
+                          int64_t ldqt, float* scales_t, int64_t ldscales_t, hipStream_t stream);
+
+/*
+ * tp_qgemm_fp8 -- the product of two matrices of e4m3 codes with a scale for each
+ * block of 128 along k:
+ *
+ *   C[i, c] = sum_g (sa[g, i] sb(g, c)) * sum_{q in block g} a[i, q] b[c, q]
+ *
+ *   a, a_scales  codes [m, k], row pitch lda bytes, and scales [k / 128, m], row
+ *            pitch ldsa: tp_quantize_fp8's q or qt with block_rows 1, or
+ *            tp_layernorm_rotate's.
+ *   b, b_scales  codes [n, k], row pitch ldb bytes. b_block_rows 128: scales
+ *            [n / 128 rounded up, k / 128], row pitch ldsb, sb(g, c) =
+ *            b_scales[c / 128, g] (weights); 1: scales [k / 128, n], sb(g, c) =
+ *            b_scales[g, c].
+ *   c        [m, n], c_dtype, row pitch ldc; aligned to the element.
+ *   workspace  tp_qgemm_fp8_workspace_size(m, n, k) bytes, 16-byte aligned
+ *            (partial sums where k is split; nothing is kept between calls).
+ *   k a positive multiple of 128. A block's sum is the matrix units' fp32 sum of
+ *   exact products; blocks are added in fp32 in a fixed order. Code bytes 0x7f and
+ *   0xff are NaN and reach the outputs that read them. m, n and k below 2^26, m n
+ *   at most 2^36.
+ *
+ *   y = x . w^T     tp_qgemm_fp8(x by rows, w by blocks)
+ *   dx = dy . w     tp_qgemm_fp8(dy by rows, qt of w by blocks)   [k, n rounded up]
+ *   dw = dy^T . x   tp_qgemm_fp8(qt of dy, qt of x, b_block_rows 1)
+ */
+size_t tp_qgemm_fp8_workspace_size(int64_t m, int64_t n, int64_t k);
+tp_status tp_qgemm_fp8(const uint8_t* a, int64_t lda, const float* a_scales, int64_t ldsa, const uint8_t* b,
+                       int64_t ldb, const float* b_scales, int64_t ldsb, int b_block_rows, int64_t m, int64_t n,
+                       int64_t k, void* c, tp_dtype c_dtype, int64_t ldc, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* tp_status_string(tp_status status);
 

@@ -26,6 +26,15 @@ The operators around the projections of a block (block_ops.py):
                                                -> q, k normed per head and turned to their positions
     tp_qk_norm_rope_backward(dq_out, dk_out, q, k, ...)
                                                -> dq, dk, dq_gamma, dk_gamma
+
+The operators of a pre-norm block's branches (branch_ops.py):
+
+    tp_dropout(x, drop_p, rng, residual)       -> drop(x) + residual (its own backward pass)
+    tp_layernorm_rotate(x, gamma, beta, residual=, drop_p=, rng=)
+                                               -> codes, scales (or rows), and the new stream
+    tp_layernorm_rotate_backward(dy, t, gamma) -> dx, dbranch, dgamma, dbeta
+    tp_quantize_fp8(x, block_rows, want)       -> e4m3 codes and a scale for each block of 128
+    tp_qgemm_fp8(a, a_scales, b, b_scales)     -> C
 """
 
 import torch
@@ -37,6 +46,9 @@ from .block_ops import (  # noqa: F401
     tp_lora_grad_workspace_size,
     tp_qk_norm_rope, tp_qk_norm_rope_backward, tp_qk_norm_rope_workspace_size, tp_rmsnorm_backward_workspace_size,
     tp_rmsnorm_rotate, tp_rmsnorm_rotate_backward)
+from .branch_ops import (  # noqa: F401
+    tp_dropout, tp_layernorm_backward_workspace_size, tp_layernorm_rotate, tp_layernorm_rotate_backward,
+    tp_qgemm_fp8, tp_qgemm_fp8_workspace_size, tp_quantize_fp8)
 
 _DTYPE = {torch.float32: _lib.TP_F32, torch.bfloat16: _lib.TP_BF16}
 

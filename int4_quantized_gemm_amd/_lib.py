@@ -32,7 +32,7 @@ TP_A_PREROTATED, TP_A_ROTATE = 0, 1
 TP_OP_QGEMM_W8, TP_OP_QGEMM_W4, TP_OP_QGEMM_W8A8, TP_OP_QGEMM_W8A8_PREQUANTIZED = 1, 2, 3, 4
 TP_OP_QGEMM_W4A8, TP_OP_QGEMM_W4A8_PREQUANTIZED = 5, 6
 TP_FFN_OUT_I8, TP_FFN_OUT_BF16 = 0, 1
-TP_NORM_OUT_I8, TP_NORM_OUT_BF16 = 0, 1
+TP_NORM_OUT_I8, TP_NORM_OUT_BF16, TP_NORM_OUT_FP8 = 0, 1, 2
 TP_ROPE_INTERLEAVED, TP_ROPE_HALVES = 0, 1
 
 _p = ctypes.c_void_p
@@ -84,6 +84,16 @@ SIGNATURES = {
     "tp_qk_norm_rope_backward": (_int, [_p, _i64, _p, _i64, _int, _p, _i64, _p, _i64, _int, _i64, _i64, _i64, _i64, _p,
                                         _p, _int, _dbl, _p, _i64, _int, _p, _p, _i64, _int, _p, _i64, _p, _i64, _int,
                                         _p, _p, _p, _sz, _p]),
+    "tp_dropout": (_int, [_p, _int, _i64, _p, _i64, _dbl, _p, _i64, _i64, _p, _int, _i64, _p]),
+    "tp_layernorm_rotate": (_int, [_p, _int, _i64, _p, _i64, _p, _i64, _int, _p, _p, _int, _dbl, _dbl, _p, _int, _i64,
+                                   _i64, _int, _p, _i64, _p, _i64, _p]),
+    "tp_layernorm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "tp_layernorm_rotate_backward": (_int, [_p, _int, _i64, _int, _p, _int, _i64, _p, _int, _dbl, _p, _i64, _dbl, _p,
+                                            _i64, _i64, _p, _int, _i64, _p, _i64, _p, _p, _p, _sz, _p]),
+    "tp_quantize_fp8": (_int, [_p, _int, _i64, _i64, _i64, _int, _int, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p]),
+    "tp_qgemm_fp8_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "tp_qgemm_fp8": (_int, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _int, _i64, _i64, _i64, _p, _int, _i64, _p, _sz,
+                            _p]),
     "tp_status_string": (ctypes.c_char_p, [_int]),
     "tp_last_error_message": (ctypes.c_char_p, []),
     "tp_abi_version": (_int, []),

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtp.so")
-SOURCES = ["api.cpp", "rotate.hip", "gemm.hip", "lora.hip", "norm.hip", "side.hip", "rope.hip"]
+SOURCES = ["api.cpp", "rotate.hip", "gemm.hip", "lora.hip", "norm.hip", "side.hip", "rope.hip",
+           "layernorm.hip", "dropout.hip", "fp8.hip", "fp8_gemm.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -46,7 +47,7 @@ def _compile(src, verbose):
 
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs

@@ -6,6 +6,7 @@
 // by 256 up front rather than failing halfway).
 #include <hip/hip_runtime.h>
 #include <limits.h>
+#include <math.h>
 #include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -1156,5 +1157,322 @@ tp_status tp_qk_norm_rope_backward(const void* dq_out, int64_t lddqo, const void
   return hip_status(tp::launch_rope(a, stream), "rope backward launch");
 }
 
-}  // extern "C"
+// --------------------------------------------- dropout and layer norm of rows
 
+namespace {
+
+// p in [0, 1] and the device memory of seed and offset (needed where something
+// may drop; NULL where it is not used).
+tp_status check_drop(double p, const uint64_t* rng, tp::DropArg* d, Extent* e) {
+  *d = tp::DropArg{nullptr, 0, 1.f};
+  *e = Extent{};
+  if (!(p >= 0.0) || !(p <= 1.0)) return fail(TP_ERR_BAD_VALUE, "drop_p=%g is not within 0 .. 1", p);
+  if (p == 0.0) return TP_OK;
+  if (!rng) return fail(TP_ERR_NULL_POINTER, "rng is NULL (drop_p=%g)", p);
+  if (((uintptr_t)rng & 7u) != 0) return fail(TP_ERR_MISALIGNED, "rng is not 8-byte aligned");
+  e->lo = (uintptr_t)rng;
+  e->hi = e->lo + 16;
+  d->threshold = (uint32_t)nearbyint(p * 65536.0);
+  d->scale = d->threshold < 65536u ? (float)(65536.0 / (65536.0 - (double)d->threshold)) : 0.f;
+  d->rng = d->threshold > 0 ? rng : nullptr;  // (p below 2^-17 drops nothing)
+  return TP_OK;
+}
+
+}  // namespace
+
+tp_status tp_dropout(const void* x, tp_dtype x_dtype, int64_t ldx, const void* residual, int64_t ldr, double drop_p,
+                     const uint64_t* rng, int64_t m, int64_t k, void* y, tp_dtype y_dtype, int64_t ldy,
+                     hipStream_t stream) {
+  if (!dtype_ok(x_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "x_dtype %d is not TP_F32 or TP_BF16", (int)x_dtype);
+  if (!dtype_ok(y_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "y_dtype %d is not TP_F32 or TP_BF16", (int)y_dtype);
+  if (m < 0 || m > INT_MAX || k < 0 || k > INT_MAX)
+    return fail(TP_ERR_BAD_SHAPE, "m=%lld, k=%lld", (long long)m, (long long)k);
+  tp::DropoutArgs a{};
+  Extent er, ex, es{}, ey;
+  TP_TRY(check_drop(drop_p, rng, &a.drop, &er));
+  const int64_t xs = dtype_size(x_dtype), ys = dtype_size(y_dtype);
+  TP_TRY(check_matrix("x", x, m, k * xs, ldx, xs, &ex));
+  if (residual) TP_TRY(check_matrix("residual", residual, m, k * ys, ldr, ys, &es));
+  TP_TRY(check_matrix("y", y, m, k * ys, ldy, ys, &ey));
+  if (overlaps(ey, er)) return fail(TP_ERR_BAD_ALIASING, "y overlaps rng");
+  if (overlaps(ey, ex) && !same_buffer(y, y_dtype, ldy, x, x_dtype, ldx))
+    return fail(TP_ERR_BAD_ALIASING, "y overlaps x without being the same buffer");
+  if (overlaps(ey, es) && !same_buffer(y, y_dtype, ldy, residual, y_dtype, ldr))
+    return fail(TP_ERR_BAD_ALIASING, "y overlaps residual without being the same buffer");
+  if (m == 0 || k == 0) return ok();
+  a.x = x;
+  a.x_bf16 = x_dtype == TP_BF16;
+  a.ldx = ldx;
+  a.res = residual;
+  a.ldr = ldr;
+  a.m = m;
+  a.k = k;
+  a.y = y;
+  a.y_bf16 = y_dtype == TP_BF16;
+  a.ldy = ldy;
+  return hip_status(tp::launch_dropout(a, stream), "dropout launch");
+}
+
+tp_status tp_layernorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, const void* residual, int64_t ldr,
+                              void* sum_out, int64_t ldsum, tp_dtype s_dtype, const void* gamma, const void* beta,
+                              tp_dtype g_dtype, double eps, double drop_p, const uint64_t* rng, int a_flags, int64_t m,
+                              int64_t k, int out_kind, void* y, int64_t ldy, float* scales, int64_t ldscales,
+                              hipStream_t stream) {
+  if (!dtype_ok(x_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "x_dtype %d is not TP_F32 or TP_BF16", (int)x_dtype);
+  if (out_kind != TP_NORM_OUT_I8 && out_kind != TP_NORM_OUT_BF16 && out_kind != TP_NORM_OUT_FP8)
+    return fail(TP_ERR_BAD_FLAGS, "out_kind=%d", out_kind);
+  if (a_flags != TP_A_ROTATE && a_flags != TP_A_PREROTATED) return fail(TP_ERR_BAD_FLAGS, "a_flags=%d", a_flags);
+  TP_TRY(check_sizes(m, 0, k));
+  TP_TRY(check_norm_k(k));
+  TP_TRY(check_eps(eps));
+  const bool i8 = out_kind == TP_NORM_OUT_I8, bf16 = out_kind == TP_NORM_OUT_BF16;
+  const int64_t xs = dtype_size(x_dtype), os = bf16 ? 2 : 1;
+  tp::LayerNormArgs a{};
+  Extent ex, er{}, esum{}, eg, eb, ey, esc{}, erng;
+  TP_TRY(check_drop(drop_p, rng, &a.drop, &erng));
+  TP_TRY(check_matrix("x", x, m, k * xs, ldx, xs, &ex));
+  if (residual || sum_out) {
+    if (!dtype_ok(s_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "s_dtype %d is not TP_F32 or TP_BF16", (int)s_dtype);
+    const int64_t ss = dtype_size(s_dtype);
+    if (!residual || !sum_out)
+      return fail(TP_ERR_NULL_POINTER, "residual and sum_out are given together or not at all");
+    TP_TRY(check_matrix("residual", residual, m, k * ss, ldr, ss, &er));
+    TP_TRY(check_matrix("sum_out", sum_out, m, k * ss, ldsum, ss, &esum));
+  } else if (drop_p != 0.0) {
+    return fail(TP_ERR_NULL_POINTER, "drop_p=%g needs a residual and sum_out", drop_p);
+  }
+  TP_TRY(check_weight("gamma", gamma, g_dtype, k, &eg));
+  TP_TRY(check_weight("beta", beta, g_dtype, k, &eb));
+  TP_TRY(check_matrix("y", y, m, k * os, ldy, os, &ey));
+  if (i8) TP_TRY(check_vector("scales", scales, m, &esc));
+  if (out_kind == TP_NORM_OUT_FP8) TP_TRY(check_matrix("scales", scales, k / 128, m * 4, ldscales, 4, &esc, 4));
+  const Extent* ins[] = {&ex, &er, &esum, &eg, &eb, &erng};
+  for (const Extent* i : ins)
+    if (overlaps(ey, *i) || overlaps(esc, *i))
+      return fail(TP_ERR_BAD_ALIASING, "y and scales must not overlap x, residual, sum_out, gamma, beta or rng");
+  if (overlaps(ey, esc)) return fail(TP_ERR_BAD_ALIASING, "y and scales overlap");
+  if (overlaps(esum, eg) || overlaps(esum, eb) || overlaps(esum, erng))
+    return fail(TP_ERR_BAD_ALIASING, "sum_out overlaps gamma, beta or rng");
+  if (overlaps(esum, er) && !same_buffer(sum_out, s_dtype, ldsum, residual, s_dtype, ldr))
+    return fail(TP_ERR_BAD_ALIASING, "sum_out overlaps residual without being the same buffer");
+  if (overlaps(esum, ex) && !same_buffer(sum_out, s_dtype, ldsum, x, x_dtype, ldx))
+    return fail(TP_ERR_BAD_ALIASING, "sum_out overlaps x without being the same buffer");
+  if (m == 0) return ok();
+  a.x = x;
+  a.x_bf16 = x_dtype == TP_BF16;
+  a.ldx = ldx;
+  a.res = residual;
+  a.ldr = ldr;
+  a.sum = sum_out;
+  a.ldsum = ldsum;
+  a.s_bf16 = residual && s_dtype == TP_BF16;
+  a.gamma = {gamma, gamma && g_dtype == TP_BF16};
+  a.beta = {beta, beta && g_dtype == TP_BF16};
+  a.eps = eps;
+  a.rotate = a_flags == TP_A_ROTATE;
+  a.m = m;
+  a.groups = (int)(k / 256);
+  a.out = out_kind;
+  a.y = y;
+  a.ldy = ldy;
+  a.scales = bf16 ? nullptr : scales;
+  a.ldscales = ldscales;
+  return hip_status(tp::launch_layernorm(a, stream), "layer norm launch");
+}
+
+size_t tp_layernorm_backward_workspace_size(int64_t m, int64_t k) {
+  if (m <= 0 || k <= 0 || k % 256 != 0 || m > INT_MAX || k / 256 > tp::NORM_MAX_GROUPS) return 0;
+  return (size_t)(tp::layernorm_bwd_partial_rows(m, (int)(k / 256)) * 2 * k * 4);
+}
+
+tp_status tp_layernorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t lddy, int a_flags, const void* t,
+                                       tp_dtype t_dtype, int64_t ldt, const void* gamma, tp_dtype g_dtype, double eps,
+                                       const void* dsum, int64_t ldds, double drop_p, const uint64_t* rng, int64_t m,
+                                       int64_t k, void* dx, tp_dtype dx_dtype, int64_t lddx, void* dbranch,
+                                       int64_t lddb, float* dgamma, float* dbeta, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
+  if (!dtype_ok(dy_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "dy_dtype %d is not TP_F32 or TP_BF16", (int)dy_dtype);
+  if (!dtype_ok(t_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "t_dtype %d is not TP_F32 or TP_BF16", (int)t_dtype);
+  if (!dtype_ok(dx_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "dx_dtype %d is not TP_F32 or TP_BF16", (int)dx_dtype);
+  if (a_flags != TP_A_ROTATE && a_flags != TP_A_PREROTATED) return fail(TP_ERR_BAD_FLAGS, "a_flags=%d", a_flags);
+  TP_TRY(check_sizes(m, 0, k));
+  TP_TRY(check_norm_k(k));
+  TP_TRY(check_eps(eps));
+  const int64_t gs = dtype_size(dy_dtype), ts = dtype_size(t_dtype), xs = dtype_size(dx_dtype);
+  tp::LayerNormBwdArgs a{};
+  Extent edy, et, eg, eds{}, edx, edb{}, edg{}, edbt{}, ew, erng;
+  TP_TRY(check_drop(drop_p, rng, &a.drop, &erng));
+  TP_TRY(check_matrix("dy", dy, m, k * gs, lddy, gs, &edy));
+  TP_TRY(check_matrix("t", t, m, k * ts, ldt, ts, &et));
+  TP_TRY(check_weight("gamma", gamma, g_dtype, k, &eg));
+  if (dsum) TP_TRY(check_matrix("dsum", dsum, m, k * xs, ldds, xs, &eds));
+  TP_TRY(check_matrix("dx", dx, m, k * xs, lddx, xs, &edx));
+  if (dbranch) TP_TRY(check_matrix("dbranch", dbranch, m, k * xs, lddb, xs, &edb));
+  if (dgamma) TP_TRY(check_vector("dgamma", dgamma, k, &edg));
+  if (dbeta) TP_TRY(check_vector("dbeta", dbeta, k, &edbt));
+  TP_TRY(check_scratch("tp_layernorm_backward_workspace_size", workspace, workspace_bytes,
+                       dgamma || dbeta ? (int64_t)tp_layernorm_backward_workspace_size(m, k) : 0, &ew));
+  const Extent* ins[] = {&edy, &et, &eg, &eds, &erng};
+  const Extent* outs[] = {&edb, &edg, &edbt, &ew};  // apart from everything
+  for (int o = 0; o < 4; ++o) {
+    for (const Extent* i : ins)
+      if (overlaps(*outs[o], *i))
+        return fail(TP_ERR_BAD_ALIASING, "dbranch, dgamma, dbeta or the workspace overlaps an input");
+    if (overlaps(*outs[o], edx))
+      return fail(TP_ERR_BAD_ALIASING, "dbranch, dgamma, dbeta or the workspace overlaps dx");
+    for (int p = 0; p < o; ++p)
+      if (overlaps(*outs[o], *outs[p]))
+        return fail(TP_ERR_BAD_ALIASING, "dbranch, dgamma, dbeta and the workspace must not overlap");
+  }
+  if (overlaps(edx, et) || overlaps(edx, eg) || overlaps(edx, erng))
+    return fail(TP_ERR_BAD_ALIASING, "dx overlaps t, gamma or rng");
+  if (overlaps(edx, eds) && !same_buffer(dx, dx_dtype, lddx, dsum, dx_dtype, ldds))
+    return fail(TP_ERR_BAD_ALIASING, "dx overlaps dsum without being the same buffer");
+  if (overlaps(edx, edy) && !same_buffer(dx, dx_dtype, lddx, dy, dy_dtype, lddy))
+    return fail(TP_ERR_BAD_ALIASING, "dx overlaps dy without being the same buffer");
+  if (m == 0 && !dgamma && !dbeta) return ok();
+  a.dy = dy;
+  a.dy_bf16 = dy_dtype == TP_BF16;
+  a.lddy = lddy;
+  a.rotate = a_flags == TP_A_ROTATE;
+  a.t = t;
+  a.t_bf16 = t_dtype == TP_BF16;
+  a.ldt = ldt;
+  a.gamma = {gamma, gamma && g_dtype == TP_BF16};
+  a.eps = eps;
+  a.dsum = dsum;
+  a.ldds = ldds;
+  a.m = m;
+  a.groups = (int)(k / 256);
+  a.dx = dx;
+  a.dx_bf16 = dx_dtype == TP_BF16;
+  a.lddx = lddx;
+  a.dbranch = dbranch;
+  a.lddb = lddb;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.part = (float*)workspace;
+  return hip_status(tp::launch_layernorm_bwd(a, stream), "layer norm backward launch");
+}
+
+// ------------------------------------- products in 8-bit floating point (e4m3)
+
+namespace {
+
+// Sizes of the block-scaled products: the kernels hold rows and columns in 32
+// bits, and a launch counts its threads in 32 bits.
+constexpr int64_t F8_MAX = (int64_t)1 << 26;
+constexpr int64_t F8_MAX_ELEMENTS = (int64_t)1 << 36;  // of a quantized matrix, and of a product
+
+tp_status check_f8_sizes(int64_t m, int64_t n, const char* what) {
+  if (m < 0 || n < 0 || m >= F8_MAX || n >= F8_MAX)
+    return fail(TP_ERR_BAD_SHAPE, "%s: %lld, %lld: 0 .. 2^26 - 1 each", what, (long long)m, (long long)n);
+  if (m * n > F8_MAX_ELEMENTS)
+    return fail(TP_ERR_BAD_SHAPE, "%s: %lld x %lld: at most 2^36 elements", what, (long long)m, (long long)n);
+  return TP_OK;
+}
+
+}  // namespace
+
+tp_status tp_quantize_fp8(const void* x, tp_dtype x_dtype, int64_t ldx, int64_t m, int64_t k, int a_flags,
+                          int block_rows, uint8_t* q, int64_t ldq, float* scales, int64_t ldscales, uint8_t* qt,
+                          int64_t ldqt, float* scales_t, int64_t ldscales_t, hipStream_t stream) {
+  if (!dtype_ok(x_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "x_dtype %d is not TP_F32 or TP_BF16", (int)x_dtype);
+  if (a_flags != TP_A_ROTATE && a_flags != TP_A_PREROTATED) return fail(TP_ERR_BAD_FLAGS, "a_flags=%d", a_flags);
+  if (block_rows != 1 && block_rows != 128) return fail(TP_ERR_BAD_FLAGS, "block_rows=%d (1 or 128)", block_rows);
+  TP_TRY(check_f8_sizes(m, k, "m, k"));
+  if (a_flags == TP_A_ROTATE && k % 256 != 0)
+    return fail(TP_ERR_K_NOT_MULTIPLE_OF_256, "k=%lld is not a multiple of 256 (the rotation group)", (long long)k);
+  if ((q == nullptr) != (scales == nullptr) || (qt == nullptr) != (scales_t == nullptr))
+    return fail(TP_ERR_NULL_POINTER, "codes and their scales are given together or not at all");
+  const int64_t xs = dtype_size(x_dtype), kp = round_up(k, 128), mp = round_up(m, 128);
+  const bool blocks = block_rows == 128;
+  Extent ex, eo[4] = {};
+  TP_TRY(check_matrix("x", x, m, k * xs, ldx, xs, &ex));
+  if (!q && !qt) return m == 0 || k == 0 ? ok() : fail(TP_ERR_NULL_POINTER, "q or qt (or both) is needed");
+  if (m == 0 || k == 0) return ok();
+  if (q) {
+    TP_TRY(check_matrix("q", q, m, kp, ldq, 1, &eo[0]));
+    TP_TRY(check_matrix("scales", scales, blocks ? mp / 128 : kp / 128, (blocks ? kp / 128 : m) * 4, ldscales, 4, &eo[1],
+                        4));
+  }
+  if (qt) {
+    TP_TRY(check_matrix("qt", qt, k, mp, ldqt, 1, &eo[2]));
+    TP_TRY(check_matrix("scales_t", scales_t, blocks ? kp / 128 : mp / 128, (blocks ? mp / 128 : k) * 4, ldscales_t, 4,
+                        &eo[3], 4));
+  }
+  for (int o = 0; o < 4; ++o) {
+    if (overlaps(eo[o], ex)) return fail(TP_ERR_BAD_ALIASING, "codes or scales overlap x");
+    for (int p = 0; p < o; ++p)
+      if (overlaps(eo[o], eo[p])) return fail(TP_ERR_BAD_ALIASING, "codes and scales must not overlap");
+  }
+  tp::QuantFp8Args a{};
+  a.x = x;
+  a.x_bf16 = x_dtype == TP_BF16;
+  a.ldx = ldx;
+  a.m = m;
+  a.k = k;
+  a.rotate = a_flags == TP_A_ROTATE;
+  a.blocks = blocks;
+  a.q = q;
+  a.ldq = ldq;
+  a.s = scales;
+  a.lds = ldscales;
+  a.qt = qt;
+  a.ldqt = ldqt;
+  a.st = scales_t;
+  a.ldst = ldscales_t;
+  return hip_status(tp::launch_quantize_fp8(a, stream), "fp8 quantizer launch");
+}
+
+size_t tp_qgemm_fp8_workspace_size(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || n <= 0 || k <= 0 || k % 128 != 0 || m >= F8_MAX || n >= F8_MAX || k >= F8_MAX ||
+      m * n > F8_MAX_ELEMENTS)
+    return 0;
+  return (size_t)tp::qgemm_fp8_partial_bytes(m, n, k);
+}
+
+tp_status tp_qgemm_fp8(const uint8_t* a, int64_t lda, const float* a_scales, int64_t ldsa, const uint8_t* b,
+                       int64_t ldb, const float* b_scales, int64_t ldsb, int b_block_rows, int64_t m, int64_t n,
+                       int64_t k, void* c, tp_dtype c_dtype, int64_t ldc, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream) {
+  if (!dtype_ok(c_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "c_dtype %d is not TP_F32 or TP_BF16", (int)c_dtype);
+  if (b_block_rows != 1 && b_block_rows != 128) return fail(TP_ERR_BAD_FLAGS, "b_block_rows=%d (1 or 128)", b_block_rows);
+  TP_TRY(check_f8_sizes(m, n, "m, n"));
+  if (k <= 0 || k % 128 != 0 || k >= F8_MAX)
+    return fail(TP_ERR_BAD_SHAPE, "k=%lld: a positive multiple of 128 below 2^26", (long long)k);
+  const int64_t cs = dtype_size(c_dtype), kb = k / 128;
+  const bool rows = b_block_rows == 1;
+  Extent e[4], ec, ew;
+  TP_TRY(check_matrix("a", a, m, k, lda, 1, &e[0]));
+  TP_TRY(check_matrix("a_scales", a_scales, kb, m * 4, ldsa, 4, &e[1], 4));
+  TP_TRY(check_matrix("b", b, n, k, ldb, 1, &e[2]));
+  TP_TRY(check_matrix("b_scales", b_scales, rows ? kb : (n + 127) / 128, (rows ? n : kb) * 4, ldsb, 4, &e[3], 4));
+  TP_TRY(check_matrix("c", c, m, n * cs, ldc, cs, &ec, cs));
+  TP_TRY(check_scratch("tp_qgemm_fp8_workspace_size", workspace, workspace_bytes,
+                       (int64_t)tp_qgemm_fp8_workspace_size(m, n, k), &ew));
+  for (int i = 0; i < 4; ++i)
+    if (overlaps(ec, e[i]) || overlaps(ew, e[i])) return fail(TP_ERR_BAD_ALIASING, "c or the workspace overlaps an input");
+  if (overlaps(ec, ew)) return fail(TP_ERR_BAD_ALIASING, "c and the workspace overlap");
+  if (m == 0 || n == 0) return ok();
+  tp::GemmFp8Args g{};
+  g.a = a;
+  g.lda = lda;
+  g.sa = a_scales;
+  g.ldsa = ldsa;
+  g.b = b;
+  g.ldb = ldb;
+  g.sb = b_scales;
+  g.ldsb = ldsb;
+  g.b_rows = rows;
+  g.m = m;
+  g.n = n;
+  g.k = k;
+  g.c = c;
+  g.c_bf16 = c_dtype == TP_BF16;
+  g.ldc = ldc;
+  g.part = (float*)workspace;
+  return hip_status(tp::launch_qgemm_fp8(g, stream), "fp8 product launch");
+}
+
+}  // extern "C"

@@ -138,4 +138,118 @@ struct RopeArgs {
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 int64_t rope_partial_rows(int64_t m, int heads, int d);
 
+// ----------------------------------------------------------------- philox.hpp
+// A dropout: rng points at two 64-bit numbers in device memory, the seed and
+// the offset (nullptr: none); threshold 0 .. 65536 of 16 random bits; scale
+// 65536 / (65536 - threshold), 0 where everything drops.
+struct DropArg {
+  const uint64_t* rng;
+  uint32_t threshold;
+  float scale;
+};
+
+// -------------------------------------------------------------- layernorm.hip
+struct LayerNormArgs {
+  const void* x;
+  int x_bf16;
+  int64_t ldx;
+  const void* res;  // nullptr: no residual (and no sum, and no dropout)
+  int64_t ldr;
+  void* sum;
+  int64_t ldsum;
+  int s_bf16;
+  VecArg gamma, beta;
+  double eps;
+  DropArg drop;
+  int rotate;
+  int64_t m;
+  int groups;
+  int out;  // TP_NORM_OUT_*
+  void* y;
+  int64_t ldy;
+  float* scales;
+  int64_t ldscales;  // TP_NORM_OUT_FP8: [k / 128, m]
+};
+hipError_t launch_layernorm(const LayerNormArgs& a, hipStream_t stream);
+
+struct LayerNormBwdArgs {
+  const void* dy;
+  int dy_bf16;
+  int64_t lddy;
+  int rotate;
+  const void* t;
+  int t_bf16;
+  int64_t ldt;
+  VecArg gamma;
+  double eps;
+  const void* dsum;  // nullptr: none
+  int64_t ldds;
+  DropArg drop;
+  int64_t m;
+  int groups;
+  void* dx;
+  int dx_bf16;
+  int64_t lddx;
+  void* dbranch;  // nullptr: not wanted; needs drop.rng
+  int64_t lddb;
+  float *dgamma, *dbeta;  // nullptr: not wanted
+  float* part;            // layernorm_bwd_partial_rows(m, groups) rows of 2 groups * 256 floats, where one is
+};
+hipError_t launch_layernorm_bwd(const LayerNormBwdArgs& a, hipStream_t stream);
+int64_t layernorm_bwd_partial_rows(int64_t m, int groups);
+
+// ---------------------------------------------------------------- dropout.hip
+struct DropoutArgs {
+  const void* x;  // [m, k]
+  int x_bf16;
+  int64_t ldx;
+  const void* res;  // nullptr: none; of y's type
+  int64_t ldr;
+  DropArg drop;
+  int64_t m, k;
+  void* y;
+  int y_bf16;
+  int64_t ldy;
+};
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t stream);
+
+// -------------------------------------------------------------------- fp8.hip
+struct QuantFp8Args {
+  const void* x;  // [m, k]
+  int x_bf16;
+  int64_t ldx;
+  int64_t m, k;
+  int rotate;   // k a multiple of 256
+  int blocks;   // a scale per 128 x 128 block (else per 128 elements of a row, or of a column)
+  uint8_t* q;   // [m, kp] codes, kp = k rounded up to 128 (nullptr: not wanted)
+  int64_t ldq;
+  float* s;     // [kp / 128, m], or with blocks [mp / 128, kp / 128]
+  int64_t lds;
+  uint8_t* qt;  // [k, mp] codes of the transpose (nullptr: not wanted)
+  int64_t ldqt;
+  float* st;    // [mp / 128, k], or with blocks [kp / 128, mp / 128]
+  int64_t ldst;
+};
+hipError_t launch_quantize_fp8(const QuantFp8Args& a, hipStream_t stream);
+
+// --------------------------------------------------------------- fp8_gemm.hip
+struct GemmFp8Args {
+  const uint8_t* a;  // [m, k]
+  int64_t lda;
+  const float* sa;  // [k / 128, m]
+  int64_t ldsa;
+  const uint8_t* b;  // [n, k]
+  int64_t ldb;
+  const float* sb;  // [n / 128, k / 128], or with b_rows [k / 128, n]
+  int64_t ldsb;
+  int b_rows;
+  int64_t m, n, k;
+  void* c;  // [m, n]
+  int c_bf16;
+  int64_t ldc;
+  float* part;  // qgemm_fp8_partial_bytes() bytes
+};
+hipError_t launch_qgemm_fp8(const GemmFp8Args& a, hipStream_t stream);
+int64_t qgemm_fp8_partial_bytes(int64_t m, int64_t n, int64_t k);
+
 }  // namespace tp

@@ -1,0 +1,450 @@
+// Product of two e4m3 matrices with a scale for each block of 128 along k:
+//
+//   C[i, c] = sum_g sa[g, i] sb(g, c) sum_{q in block g} a[i, q] b[c, q]
+//
+// sb one number per 128 x 128 block of b (weights), or per row of b and block
+// (an operand that was quantized like a, as in a weight's gradient).
+//
+// A block of k starts from zero on the matrix unit, and its fp32 result is folded
+// into the fp32 sums with the product of the two scales, on the vector unit
+// beside the next instructions. Two ways to sum a block:
+//   bf16 C   one 16x16x128 8-bit float instruction. It adds eight products at a
+//            time aligned to the largest of them and drops what lies below about
+//            2^-15 of it (measured: 1.3e-5 of the result's norm on Gaussian
+//            codes, 3.3e-5 with one row 100 times the others): far inside bf16's
+//            own rounding of 2^-9, not inside fp32's.
+//   fp32 C   four 16x16x32 bf16 instructions on the widened codes (exact), whose
+//            sums are fp32's; half the matrix rate.
+// The instruction's first operand is b and its second a, so that a lane holds
+// consecutive columns of one row of C and needs one scale of a per fragment.
+// Fragment j of a wave takes the rows 4 FN (r / 4) + 4 j + r % 4 of its share
+// of b, r = 0 .. 15, which makes the columns a lane holds 4 FN consecutive ones.
+//
+// LDS: rows of 128 bytes, 16-byte granules; granule c of a row sits at c ^ f,
+// f from two bits of the row chosen so that the 16 lanes that ds_read_b128
+// serves together touch 16 different granules of 256 bytes (gemm_pp.hpp).
+#include <algorithm>
+
+#include "block_ops.hpp"
+#include "gemm_pp.hpp"
+
+namespace tp {
+
+typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+
+namespace {
+
+// 16 x 16 results over 128 of k, from zero.
+__device__ __forceinline__ f32x4_t mfma_e4m3(i32x8_t first, i32x8_t second) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(first, second, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Eight codes (two dwords) as bf16, exact.
+__device__ __forceinline__ bf16x8_t widen_e4m3(int lo, int hi) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+  return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// The 32 codes of a lane, as the matrix instructions take them.
+template <bool EXACT>
+struct Frag;
+
+template <>
+struct Frag<false> {
+  i32x8_t v;
+  __device__ __forceinline__ void set(i32x8_t codes) { v = codes; }
+};
+
+template <>
+struct Frag<true> {
+  bf16x8_t v[4];
+  __device__ __forceinline__ void set(i32x8_t codes) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = widen_e4m3(codes[2 * s], codes[2 * s + 1]);
+  }
+};
+
+// One fragment of a against FN of b, over a block, from zero.
+template <int FN>
+__device__ __forceinline__ void block_sums(const Frag<false> (&b)[FN], const Frag<false>& a, f32x4_t (&p)[FN]) {
+#pragma unroll
+  for (int j = 0; j < FN; ++j) p[j] = mfma_e4m3(b[j].v, a.v);
+}
+
+template <int FN>
+__device__ __forceinline__ void block_sums(const Frag<true> (&b)[FN], const Frag<true>& a, f32x4_t (&p)[FN]) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[s], a.v[s], s ? p[j] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8_t join8(u32x4_t lo, u32x4_t hi) {
+  return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+
+// N consecutive columns of a row of C, as far as it has them.
+template <int N, typename T>
+__device__ __forceinline__ void store_cols(T* p, int left, bool vec, const float (&v)[N]) {
+  if (vec && left >= N) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < N; e += 4) *reinterpret_cast<f32x4_t*>(p + e) = f32x4_t{v[e], v[e + 1], v[e + 2], v[e + 3]};
+    } else if constexpr (N % 8 == 0) {
+#pragma unroll
+      for (int e = 0; e < N; e += 8)
+        *reinterpret_cast<u32x4_t*>(p + e) = u32x4_t{pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
+                                                     pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; e += 4)
+        *reinterpret_cast<uint2*>(p + e) = uint2{pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3])};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < left) {
+        if constexpr (sizeof(T) == 4)
+          p[e] = v[e];
+        else
+          p[e] = (uint16_t)pack_bf16x2(v[e], 0.f);
+      }
+  }
+}
+
+}  // namespace
+
+template <int BM, int BN, int WM, int WN>
+struct F8Cfg {
+  static constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, NT = 64 * NW;
+  static constexpr int FM = WM / 16, FN = WN / 16;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+  static constexpr int STAGE = A_BYTES + B_BYTES + 4 * (BM + BN);  // operands, then their scales
+  static constexpr int LOADS = (BM + BN) / 8, LPW = LOADS / NW;    // direct loads of 1 KB
+  static_assert(LOADS % NW == 0 && BM % 64 == 0 && BN % 64 == 0 && 128 % WN == 0, "whole loads, one block of b a wave");
+};
+
+// PARTIAL: the steps [blockIdx.y * sps, ..) of k, raw sums to part.
+template <int BM, int BN, int WM, int WN, bool BROWS, bool OUT_BF16, bool PARTIAL>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void k_qgemm_fp8(GemmFp8Args g, int tiles_m, int tiles_n,
+                                                                            int gm, int sps, int64_t ldp) {
+  using Cfg = F8Cfg<BM, BN, WM, WN>;
+  constexpr int FM = Cfg::FM, FN = Cfg::FN, LPW = Cfg::LPW;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  int tm, tn;
+  pp_map_tile(blockIdx.x, gridDim.x, tiles_m, tiles_n, gm, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int M = (int)g.m, N = (int)g.n;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm0 = (wave / Cfg::NWN) * WM, wn0 = (wave % Cfg::NWN) * WN;
+  auto swz_a = [](int row) { return (row >> 1) & 5; };
+  auto swz_b = [](int row) { return ((row >> 1) & 1) | (((row / (8 * FN)) & 1) << 2); };
+
+  const int KB = (int)(g.k >> 7);
+  const int ks0 = PARTIAL ? blockIdx.y * sps : 0;
+  const int KS = PARTIAL ? min(sps, KB - ks0) : KB;
+  const uint8_t* src[LPW];
+  int dst[LPW];
+#pragma unroll
+  for (int i = 0; i < LPW; ++i) {
+    const int L = wave * LPW + i;
+    if (L < BM / 8) {
+      const int row = L * 8 + (lane >> 3), c = (lane & 7) ^ swz_a(row);
+      src[i] = g.a + (int64_t)min(m0 + row, M - 1) * g.lda + c * 16;
+    } else {
+      const int row = (L - BM / 8) * 8 + (lane >> 3), c = (lane & 7) ^ swz_b(row);
+      src[i] = g.b + (int64_t)min(n0 + row, N - 1) * g.ldb + c * 16;
+    }
+    src[i] += (int64_t)ks0 * 128;
+    dst[i] = L * 1024;
+  }
+  const float* ssrc[2] = {nullptr, nullptr};  // scales: 64 to a load
+  if (wave < BM / 64) ssrc[0] = g.sa + (int64_t)ks0 * g.ldsa + min(m0 + wave * 64 + lane, M - 1);
+  if (BROWS && wave < BN / 64) ssrc[1] = g.sb + (int64_t)ks0 * g.ldsb + min(n0 + wave * 64 + lane, N - 1);
+  auto issue = [&](int ks) {
+    uint8_t* base = ring + (ks & 1) * Cfg::STAGE;
+#pragma unroll
+    for (int i = 0; i < LPW; ++i)
+      __builtin_amdgcn_global_load_lds((const void*)(src[i] + (int64_t)ks * 128), (lds_void_t*)(base + dst[i]), 16, 0, 0);
+    uint8_t* sbase = base + Cfg::A_BYTES + Cfg::B_BYTES;
+    if (wave < BM / 64)
+      __builtin_amdgcn_global_load_lds((const void*)(ssrc[0] + (int64_t)ks * g.ldsa), (lds_void_t*)(sbase + wave * 256),
+                                       4, 0, 0);
+    if (BROWS && wave < BN / 64)
+      __builtin_amdgcn_global_load_lds((const void*)(ssrc[1] + (int64_t)ks * g.ldsb),
+                                       (lds_void_t*)(sbase + 4 * BM + wave * 256), 4, 0, 0);
+  };
+  // the scale of b that the whole wave shares
+  const float* sbp = BROWS ? nullptr : g.sb + (int64_t)(min(n0 + wn0, N - 1) >> 7) * g.ldsb + ks0;
+
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  issue(0);
+  __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE(0));
+  barrier_only();
+  for (int ks = 0; ks < KS; ++ks) {
+    if (ks + 1 < KS) issue(ks + 1);
+    const uint8_t* as = ring + (ks & 1) * Cfg::STAGE;
+    const uint8_t* bs = as + Cfg::A_BYTES;
+    const float* ss = reinterpret_cast<const float*>(bs + Cfg::B_BYTES);
+    const float sw = BROWS ? 1.f : sbp[ks];
+    Frag<!OUT_BF16> fb[FN], fa;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int row = wn0 + 4 * FN * (r16 >> 2) + 4 * j + (r16 & 3);
+      const uint8_t* p = bs + row * 128;
+      fb[j].set(join8(*reinterpret_cast<const u32x4_t*>(p + (((2 * g4) ^ swz_b(row)) << 4)),
+                      *reinterpret_cast<const u32x4_t*>(p + (((2 * g4 + 1) ^ swz_b(row)) << 4))));
+    }
+    f32x4_t sbv[BROWS ? FN : 1];
+    if constexpr (BROWS) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sbv[j] = *reinterpret_cast<const f32x4_t*>(ss + BM + wn0 + 4 * FN * g4 + 4 * j);
+    }
+    f32x4_t p[2][FN];
+    float sc[2];
+    auto fold = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i][j][e] = fmaf(p[i & 1][j][e], BROWS ? sc[i & 1] * sbv[BROWS ? j : 0][e] : sc[i & 1], acc[i][j][e]);
+    };
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int row = wm0 + i * 16 + r16;
+      const uint8_t* q = as + row * 128;
+      fa.set(join8(*reinterpret_cast<const u32x4_t*>(q + (((2 * g4) ^ swz_a(row)) << 4)),
+                   *reinterpret_cast<const u32x4_t*>(q + (((2 * g4 + 1) ^ swz_a(row)) << 4))));
+      sc[i & 1] = ss[row] * sw;
+      block_sums(fb, fa, p[i & 1]);
+      if (i > 0) fold(i - 1);
+    }
+    fold(FM - 1);
+    __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE(0) & LGKMCNT0_ENCODE);
+    barrier_only();
+  }
+
+  const int nb = n0 + wn0 + 4 * FN * g4;
+  if constexpr (PARTIAL) {
+    float* part = g.part + (int64_t)blockIdx.y * g.m * ldp;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int row = m0 + wm0 + i * 16 + r16;
+      float v[4 * FN];
+#pragma unroll
+      for (int e = 0; e < 4 * FN; ++e) v[e] = acc[i][e >> 2][e & 3];
+      if (row < M) store_cols<4 * FN>(part + (int64_t)row * ldp + nb, (int)ldp - nb, true, v);
+    }
+  } else {
+    typedef typename std::conditional<OUT_BF16, uint16_t, float>::type out_t;
+    const bool vec = (((uintptr_t)g.c | (uintptr_t)(g.ldc * (int64_t)sizeof(out_t))) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int row = m0 + wm0 + i * 16 + r16;
+      float v[4 * FN];
+#pragma unroll
+      for (int e = 0; e < 4 * FN; ++e) v[e] = acc[i][e >> 2][e & 3];
+      if (row < M) store_cols<4 * FN>((out_t*)g.c + (int64_t)row * g.ldc + nb, N - nb, vec, v);
+    }
+  }
+}
+
+// The splits' sums, added in order.
+template <bool OUT_BF16>
+__global__ __launch_bounds__(256) void k_qgemm_fp8_join(GemmFp8Args g, int splits, int64_t ldp) {
+  typedef typename std::conditional<OUT_BF16, uint16_t, float>::type out_t;
+  const int64_t quads = ldp / 4, total = g.m * quads;
+  const bool vec = (((uintptr_t)g.c | (uintptr_t)(g.ldc * (int64_t)sizeof(out_t))) & 15u) == 0;
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
+    const int64_t row = t / quads, c = (t - row * quads) * 4;
+    const float* p = g.part + row * ldp + c;
+    f32x4_t s = *reinterpret_cast<const f32x4_t*>(p);
+    for (int i = 1; i < splits; ++i) {
+      const f32x4_t o = *reinterpret_cast<const f32x4_t*>(p + (int64_t)i * g.m * ldp);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += o[e];
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    store_cols<4>((out_t*)g.c + row * g.ldc + c, (int)min((int64_t)4, g.n - c), vec, v);
+  }
+}
+
+// Few rows: bound by the bytes of b, which go straight to registers (and are
+// summed the exact way whatever C's type). A block
+// takes 16 FN rows of b; its eight waves deal the steps of k among themselves
+// and join their sums through LDS in wave order.
+template <int FM, int FN, bool BROWS, bool OUT_BF16>
+__global__ __launch_bounds__(512, 1) void k_qgemm_fp8_few(GemmFp8Args g) {
+  constexpr int NW = 8;
+  __shared__ f32x4_t sums[NW][FM * FN][64];
+  const int n0 = blockIdx.x * 16 * FN;
+  const int M = (int)g.m, N = (int)g.n, KB = (int)(g.k >> 7);
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint8_t *bp[FN], *ap[FM];
+  const float* sp[FM];
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    bp[j] = g.b + (int64_t)min(n0 + 4 * FN * (r16 >> 2) + 4 * j + (r16 & 3), N - 1) * g.ldb + 32 * g4;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int row = min(16 * i + r16, M - 1);
+    ap[i] = g.a + (int64_t)row * g.lda + 32 * g4;
+    sp[i] = g.sa + row;
+  }
+  const int nb = n0 + 4 * FN * g4;
+  const float* sbp = BROWS ? g.sb : g.sb + (int64_t)(n0 >> 7) * g.ldsb;
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int ks = wave; ks < KB; ks += NW) {
+    Frag<true> fb[FN], fa[FM];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(bp[j] + (int64_t)ks * 128);
+      fb[j].set(join8(p[0], p[1]));
+    }
+    float sc[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(ap[i] + (int64_t)ks * 128);
+      fa[i].set(join8(p[0], p[1]));
+      sc[i] = sp[i][(int64_t)ks * g.ldsa];
+    }
+    f32x4_t sbv[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sbv[j][e] = BROWS ? sbp[(int64_t)ks * g.ldsb + min(nb + 4 * j + e, N - 1)] : sbp[ks];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      f32x4_t p[FN];
+      block_sums(fb, fa[i], p);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[j][e], sc[i] * sbv[j][e], acc[i][j][e]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sums[wave][i * FN + j][lane] = acc[i][j];
+  __syncthreads();
+  typedef typename std::conditional<OUT_BF16, uint16_t, float>::type out_t;
+  const bool vec = (((uintptr_t)g.c | (uintptr_t)(g.ldc * (int64_t)sizeof(out_t))) & 15u) == 0;
+  for (int t = threadIdx.x; t < FM * FN * 64; t += 512) {
+    const int f = t >> 6, l = t & 63, row = 16 * (f / FN) + (l & 15);
+    const int c = n0 + 4 * FN * (l >> 4) + 4 * (f % FN);
+    f32x4_t s = sums[0][f][l];
+#pragma unroll
+    for (int w = 1; w < NW; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += sums[w][f][l][e];
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    if (row < M) store_cols<4>((out_t*)g.c + (int64_t)row * g.ldc + c, N - c, vec, v);
+  }
+}
+
+// ---------------------------------------------------------------- launchers
+namespace {
+
+constexpr int64_t FEW_ROWS = 64;
+constexpr int64_t F8_CUS = 256;
+
+enum F8Tile { F8_FEW, F8_256x256, F8_128x128 };
+struct F8Plan {
+  F8Tile tile;
+  int splits, sps;
+};
+
+int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
+
+F8Plan plan_of(int64_t m, int64_t n, int64_t k) {
+  const int64_t kb = k / 128;
+  if (m <= FEW_ROWS) return F8Plan{F8_FEW, 1, 0};
+  if (tiles_of(m, n, 256, 256) >= F8_CUS / 2) return F8Plan{F8_256x256, 1, 0};
+  const int64_t tiles = tiles_of(m, n, 128, 128);
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(F8_CUS / tiles, kb / 4));
+  const int64_t sps = (kb + splits - 1) / splits;
+  return F8Plan{F8_128x128, (int)((kb + sps - 1) / sps), (int)sps};
+}
+
+int64_t pitch_of(int64_t n) { return (n + 3) / 4 * 4; }
+
+template <int BM, int BN, int WM, int WN, bool BROWS>
+hipError_t tile_launch(const GemmFp8Args& g, const F8Plan& p, hipStream_t stream) {
+  using Cfg = F8Cfg<BM, BN, WM, WN>;
+  const int tiles_m = (int)((g.m + BM - 1) / BM), tiles_n = (int)((g.n + BN - 1) / BN);
+  const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)p.splits), block(Cfg::NT);
+  const size_t lds = 2 * Cfg::STAGE;
+  const int64_t ldp = pitch_of(g.n);
+  // (OUT_BF16 of partial sums: the way a block is summed)
+#define TP_LAUNCH_F8(OB, PA) \
+  hipLaunchKernelGGL((k_qgemm_fp8<BM, BN, WM, WN, BROWS, OB, PA>), grid, block, lds, stream, g, tiles_m, tiles_n, 8, p.sps, ldp)
+  if (p.splits == 1) {
+    if (g.c_bf16) TP_LAUNCH_F8(true, false); else TP_LAUNCH_F8(false, false);
+    return hipGetLastError();
+  }
+  if (g.part == nullptr) return hipErrorInvalidValue;
+  if (g.c_bf16) TP_LAUNCH_F8(true, true); else TP_LAUNCH_F8(false, true);
+#undef TP_LAUNCH_F8
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t blocks = std::min<int64_t>((g.m * (ldp / 4) + 255) / 256, 65536);
+  if (g.c_bf16)
+    hipLaunchKernelGGL((k_qgemm_fp8_join<true>), dim3((unsigned)blocks), dim3(256), 0, stream, g, p.splits, ldp);
+  else
+    hipLaunchKernelGGL((k_qgemm_fp8_join<false>), dim3((unsigned)blocks), dim3(256), 0, stream, g, p.splits, ldp);
+  return hipGetLastError();
+}
+
+template <int FM, bool BROWS>
+hipError_t few_launch(const GemmFp8Args& g, hipStream_t stream) {
+  constexpr int FN = 1;
+  const dim3 grid((unsigned)((g.n + 16 * FN - 1) / (16 * FN))), block(512);
+  if (g.c_bf16)
+    hipLaunchKernelGGL((k_qgemm_fp8_few<FM, FN, BROWS, true>), grid, block, 0, stream, g);
+  else
+    hipLaunchKernelGGL((k_qgemm_fp8_few<FM, FN, BROWS, false>), grid, block, 0, stream, g);
+  return hipGetLastError();
+}
+
+template <bool BROWS>
+hipError_t gemm_launch(const GemmFp8Args& g, hipStream_t stream) {
+  const F8Plan p = plan_of(g.m, g.n, g.k);
+  switch (p.tile) {
+    case F8_FEW:
+      if (g.m <= 16) return few_launch<1, BROWS>(g, stream);
+      if (g.m <= 32) return few_launch<2, BROWS>(g, stream);
+      return few_launch<4, BROWS>(g, stream);
+    case F8_256x256: return tile_launch<256, 256, 128, 64, BROWS>(g, p, stream);
+    case F8_128x128: return tile_launch<128, 128, 64, 32, BROWS>(g, p, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+int64_t qgemm_fp8_partial_bytes(int64_t m, int64_t n, int64_t k) {
+  const F8Plan p = plan_of(m, n, k);
+  return p.splits == 1 ? 0 : (int64_t)p.splits * m * pitch_of(n) * 4;
+}
+
+hipError_t launch_qgemm_fp8(const GemmFp8Args& g, hipStream_t stream) {
+  return g.b_rows ? gemm_launch<true>(g, stream) : gemm_launch<false>(g, stream);
+}
+
+}  // namespace tp
