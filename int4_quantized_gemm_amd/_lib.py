@@ -91,7 +91,7 @@ SIGNATURES = {
     "tp_layernorm_rotate_backward": (_int, [_p, _int, _i64, _int, _p, _int, _i64, _p, _int, _dbl, _p, _i64, _dbl, _p,
                                             _i64, _i64, _p, _int, _i64, _p, _i64, _p, _p, _p, _sz, _p]),
     "tp_quantize_fp8": (_int, [_p, _int, _i64, _i64, _i64, _int, _int, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p]),
-    "tp_qgemm_fp8_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "tp_qgemm_fp8_workspace_size": (_sz, [_i64, _i64, _i64, _int]),
     "tp_qgemm_fp8": (_int, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _int, _i64, _i64, _i64, _p, _int, _i64, _p, _sz,
                             _p]),
     "tp_status_string": (ctypes.c_char_p, [_int]),

@@ -237,9 +237,9 @@ def tp_quantize_fp8(x, block_rows=1, rotate=False, want="rows", q=None, scales=N
     return (q, scales) if want == "rows" else (qt, scales_t)
 
 
-def tp_qgemm_fp8_workspace_size(m, n, k):
+def tp_qgemm_fp8_workspace_size(m, n, k, out_dtype=torch.float32):
     """Bytes of workspace tp_qgemm_fp8 needs (0: none)."""
-    return _lib.load().tp_qgemm_fp8_workspace_size(m, n, k)
+    return _lib.load().tp_qgemm_fp8_workspace_size(m, n, k, _lib.TP_BF16 if out_dtype == torch.bfloat16 else _lib.TP_F32)
 
 
 def tp_qgemm_fp8(a, a_scales, b, b_scales, b_block_rows=128, out_dtype=torch.float32, out=None, workspace=None,
@@ -263,7 +263,7 @@ def tp_qgemm_fp8(a, a_scales, b, b_scales, b_block_rows=128, out_dtype=torch.flo
         out, ldc = _empty((m, n), (n, 1), dtype=out_dtype, device=a.device), n
     else:
         ldc = _mat(out, "out", m, n)
-    need = tp_qgemm_fp8_workspace_size(m, n, k)
+    need = tp_qgemm_fp8_workspace_size(m, n, k, out.dtype)
     ws_ptr, ws_bytes, ws = (None, 0, None) if workspace is None and not need else _scratch(workspace, need, a.device)
     _lib.check(_lib.load().tp_qgemm_fp8(
         a.data_ptr(), lda, a_scales.data_ptr(), ldsa, b.data_ptr(), ldb, b_scales.data_ptr(), ldsb, b_block_rows, m, n,

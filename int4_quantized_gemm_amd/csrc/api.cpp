@@ -1282,7 +1282,7 @@ tp_status tp_layernorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, cons
 
 size_t tp_layernorm_backward_workspace_size(int64_t m, int64_t k) {
   if (m <= 0 || k <= 0 || k % 256 != 0 || m > INT_MAX || k / 256 > tp::NORM_MAX_GROUPS) return 0;
-  return (size_t)(tp::layernorm_bwd_partial_rows(m, (int)(k / 256)) * 2 * k * 4);
+  return (size_t)tp::layernorm_bwd_workspace_bytes(m, (int)(k / 256));
 }
 
 tp_status tp_layernorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_t lddy, int a_flags, const void* t,
@@ -1362,13 +1362,15 @@ namespace {
 // Sizes of the block-scaled products: the kernels hold rows and columns in 32
 // bits, and a launch counts its threads in 32 bits.
 constexpr int64_t F8_MAX = (int64_t)1 << 26;
-constexpr int64_t F8_MAX_ELEMENTS = (int64_t)1 << 36;  // of a quantized matrix, and of a product
+constexpr int64_t F8_MAX_PITCH = (int64_t)1 << 24;  // offsets within a tile of 256 rows are held in 32 bits
+constexpr int64_t F8_MAX_QUANTIZED = (int64_t)1 << 34, F8_MAX_PRODUCT = (int64_t)1 << 36;  // elements
 
-tp_status check_f8_sizes(int64_t m, int64_t n, const char* what) {
+tp_status check_f8_sizes(int64_t m, int64_t n, int64_t most, const char* what) {
   if (m < 0 || n < 0 || m >= F8_MAX || n >= F8_MAX)
     return fail(TP_ERR_BAD_SHAPE, "%s: %lld, %lld: 0 .. 2^26 - 1 each", what, (long long)m, (long long)n);
-  if (m * n > F8_MAX_ELEMENTS)
-    return fail(TP_ERR_BAD_SHAPE, "%s: %lld x %lld: at most 2^36 elements", what, (long long)m, (long long)n);
+  if (m * n > most)
+    return fail(TP_ERR_BAD_SHAPE, "%s: %lld x %lld: at most %lld elements", what, (long long)m, (long long)n,
+                (long long)most);
   return TP_OK;
 }
 
@@ -1380,7 +1382,7 @@ tp_status tp_quantize_fp8(const void* x, tp_dtype x_dtype, int64_t ldx, int64_t 
   if (!dtype_ok(x_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "x_dtype %d is not TP_F32 or TP_BF16", (int)x_dtype);
   if (a_flags != TP_A_ROTATE && a_flags != TP_A_PREROTATED) return fail(TP_ERR_BAD_FLAGS, "a_flags=%d", a_flags);
   if (block_rows != 1 && block_rows != 128) return fail(TP_ERR_BAD_FLAGS, "block_rows=%d (1 or 128)", block_rows);
-  TP_TRY(check_f8_sizes(m, k, "m, k"));
+  TP_TRY(check_f8_sizes(m, k, F8_MAX_QUANTIZED, "m, k"));
   if (a_flags == TP_A_ROTATE && k % 256 != 0)
     return fail(TP_ERR_K_NOT_MULTIPLE_OF_256, "k=%lld is not a multiple of 256 (the rotation group)", (long long)k);
   if ((q == nullptr) != (scales == nullptr) || (qt == nullptr) != (scales_t == nullptr))
@@ -1425,11 +1427,11 @@ tp_status tp_quantize_fp8(const void* x, tp_dtype x_dtype, int64_t ldx, int64_t 
   return hip_status(tp::launch_quantize_fp8(a, stream), "fp8 quantizer launch");
 }
 
-size_t tp_qgemm_fp8_workspace_size(int64_t m, int64_t n, int64_t k) {
-  if (m <= 0 || n <= 0 || k <= 0 || k % 128 != 0 || m >= F8_MAX || n >= F8_MAX || k >= F8_MAX ||
-      m * n > F8_MAX_ELEMENTS)
+size_t tp_qgemm_fp8_workspace_size(int64_t m, int64_t n, int64_t k, tp_dtype c_dtype) {
+  if (!dtype_ok(c_dtype) || m <= 0 || n <= 0 || k <= 0 || k % 128 != 0 || m >= F8_MAX || n >= F8_MAX || k >= F8_MAX_PITCH ||
+      m * n > F8_MAX_PRODUCT)
     return 0;
-  return (size_t)tp::qgemm_fp8_partial_bytes(m, n, k);
+  return (size_t)tp::qgemm_fp8_partial_bytes(m, n, k, c_dtype == TP_BF16);
 }
 
 tp_status tp_qgemm_fp8(const uint8_t* a, int64_t lda, const float* a_scales, int64_t ldsa, const uint8_t* b,
@@ -1438,19 +1440,21 @@ tp_status tp_qgemm_fp8(const uint8_t* a, int64_t lda, const float* a_scales, int
                        hipStream_t stream) {
   if (!dtype_ok(c_dtype)) return fail(TP_ERR_UNSUPPORTED_DTYPE, "c_dtype %d is not TP_F32 or TP_BF16", (int)c_dtype);
   if (b_block_rows != 1 && b_block_rows != 128) return fail(TP_ERR_BAD_FLAGS, "b_block_rows=%d (1 or 128)", b_block_rows);
-  TP_TRY(check_f8_sizes(m, n, "m, n"));
-  if (k <= 0 || k % 128 != 0 || k >= F8_MAX)
-    return fail(TP_ERR_BAD_SHAPE, "k=%lld: a positive multiple of 128 below 2^26", (long long)k);
+  TP_TRY(check_f8_sizes(m, n, F8_MAX_PRODUCT, "m, n"));
+  if (k <= 0 || k % 128 != 0 || k >= F8_MAX_PITCH)
+    return fail(TP_ERR_BAD_SHAPE, "k=%lld: a positive multiple of 128 below 2^24", (long long)k);
   const int64_t cs = dtype_size(c_dtype), kb = k / 128;
   const bool rows = b_block_rows == 1;
   Extent e[4], ec, ew;
   TP_TRY(check_matrix("a", a, m, k, lda, 1, &e[0]));
   TP_TRY(check_matrix("a_scales", a_scales, kb, m * 4, ldsa, 4, &e[1], 4));
   TP_TRY(check_matrix("b", b, n, k, ldb, 1, &e[2]));
+  if (lda >= F8_MAX_PITCH || ldb >= F8_MAX_PITCH)
+    return fail(TP_ERR_BAD_LEADING_DIM, "lda=%lld, ldb=%lld: below 2^24", (long long)lda, (long long)ldb);
   TP_TRY(check_matrix("b_scales", b_scales, rows ? kb : (n + 127) / 128, (rows ? n : kb) * 4, ldsb, 4, &e[3], 4));
   TP_TRY(check_matrix("c", c, m, n * cs, ldc, cs, &ec, cs));
   TP_TRY(check_scratch("tp_qgemm_fp8_workspace_size", workspace, workspace_bytes,
-                       (int64_t)tp_qgemm_fp8_workspace_size(m, n, k), &ew));
+                       (int64_t)tp_qgemm_fp8_workspace_size(m, n, k, c_dtype), &ew));
   for (int i = 0; i < 4; ++i)
     if (overlaps(ec, e[i]) || overlaps(ew, e[i])) return fail(TP_ERR_BAD_ALIASING, "c or the workspace overlaps an input");
   if (overlaps(ec, ew)) return fail(TP_ERR_BAD_ALIASING, "c and the workspace overlap");

@@ -193,10 +193,11 @@ struct LayerNormBwdArgs {
   void* dbranch;  // nullptr: not wanted; needs drop.rng
   int64_t lddb;
   float *dgamma, *dbeta;  // nullptr: not wanted
-  float* part;            // layernorm_bwd_partial_rows(m, groups) rows of 2 groups * 256 floats, where one is
+  float* part;            // layernorm_bwd_workspace_bytes(m, groups) bytes, where one is
+  double* stats;          // (set by the launcher)
 };
 hipError_t launch_layernorm_bwd(const LayerNormBwdArgs& a, hipStream_t stream);
-int64_t layernorm_bwd_partial_rows(int64_t m, int groups);
+int64_t layernorm_bwd_workspace_bytes(int64_t m, int groups);
 
 // ---------------------------------------------------------------- dropout.hip
 struct DropoutArgs {
@@ -250,6 +251,6 @@ struct GemmFp8Args {
   float* part;  // qgemm_fp8_partial_bytes() bytes
 };
 hipError_t launch_qgemm_fp8(const GemmFp8Args& a, hipStream_t stream);
-int64_t qgemm_fp8_partial_bytes(int64_t m, int64_t n, int64_t k);
+int64_t qgemm_fp8_partial_bytes(int64_t m, int64_t n, int64_t k, bool c_bf16);
 
 }  // namespace tp

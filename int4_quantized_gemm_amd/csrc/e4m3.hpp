@@ -15,44 +15,71 @@ __device__ __forceinline__ float e4m3_scale(double amax) { return (float)(amax /
 // The code of q. With e the exponent of |q| (at least -6, where the subnormal
 // codes begin), |q| 2^(3 - e) is below 16 and its nearest integer n is the
 // mantissa with its leading bit: the code is 8 (e + 6) + n, carries into the
-// next exponent included. near is set where |q| is within 1e-9 of a tie of its
-// binade's steps: there a quotient formed as x * (1 / s) may be on the other
-// side of it than x / s.
-__device__ __forceinline__ uint32_t e4m3_code(double q, bool& near) {
+// next exponent included.
+__device__ __forceinline__ uint32_t e4m3_code(double q) {
   constexpr double MAGIC = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer (RNE)
   const uint64_t u = __builtin_bit_cast(uint64_t, q);
   const uint32_t hi = (uint32_t)(u >> 32) & 0x7fffffffu;
   const int e = max((int)(hi >> 20) - 1023, -6);
   const uint32_t scaled = hi + ((uint32_t)(3 - e) << 20);  // (zero and what is far below stay far below 1)
   const double r = __builtin_bit_cast(double, ((uint64_t)scaled << 32) | (uint32_t)u);
-  const double f = r + MAGIC;
-  const double d = r - (f - MAGIC);
-  near |= !(fabs(d) < 0.5 - 1e-9);
-  const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, f);
+  const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, r + MAGIC);
   const uint32_t code = min((uint32_t)(8 * (e + 6)) + n, 126u);
   return code | ((uint32_t)(u >> 56) & 0x80u);
 }
 
-// The codes of N values x(i) with their scales s(i) and inv(i) = 1 / s(i) (0
-// where s(i) is 0), four to a dword. The ones that lie next to a tie are decided
-// by the division itself (one wave in a hundred takes it on random values).
-template <int N, typename X, typename S, typename I>
-__device__ __forceinline__ void e4m3_codes(uint32_t (&w)[N / 4], X x, S s, I inv) {
-  bool near = false;
+// What the quick way of codes needs of a scale: 1 / s from below and from above.
+// s below fp32's normal range has no such bounds (quick false: every code is
+// decided by the division).
+struct E4m3Inverse {
+  float s, lo, hi;
+  bool quick;
+};
+
+__device__ __forceinline__ E4m3Inverse e4m3_inverse(float s) {
+  const bool quick = s >= 0x1p-126f;
+  const float inv = quick ? 1.f / s : 0.f;
+  return E4m3Inverse{s, inv * (1.f - 0x1p-21f), inv * (1.f + 0x1p-21f), quick};
+}
+
+// The codes of N values, four to a dword: x(i) in fp32, exact(i) the value itself
+// in fp64 (x(i) is it, or it rounded), of(i) its scale. Rounding is monotone: the
+// products with 1 / s from below and from above enclose x / s (the roundings of
+// x, 1 / s, the factor and the product are below 2^-22 together), so where both
+// round to one code it is that of x / s. Where they do not (one value in 10^5,
+// one wave in a hundred) the fp64 division decides.
+template <int N, typename X, typename D, typename S>
+__device__ __forceinline__ void e4m3_codes(uint32_t (&w)[N / 4], X x, D exact, S of) {
+  uint32_t up[N / 4];
+  bool open = false;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t c = e4m3_code(x(i) * inv(i), near);
-    w[i >> 2] = (i & 3) == 0 ? c : w[i >> 2] | (c << (8 * (i & 3)));
+  for (int q = 0; q < N / 4; ++q) {
+    int lo = 0, hi = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = 4 * q + 2 * h;
+      const E4m3Inverse a = of(i), b = of(i + 1);
+      const float u = x(i), v = x(i + 1);
+      if (h == 0) {
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.lo, v * b.lo, lo, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.hi, v * b.hi, hi, false);
+      } else {
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.lo, v * b.lo, lo, true);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.hi, v * b.hi, hi, true);
+      }
+      open |= (!a.quick && a.s > 0.f) || (!b.quick && b.s > 0.f);
+    }
+    w[q] = (uint32_t)lo;
+    up[q] = (uint32_t)hi;
+    open |= lo != hi;
   }
-  if (__ballot(near)) {
+  if (__ballot(open)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      bool tie = false, again = false;
-      e4m3_code(x(i) * inv(i), tie);
-      if (tie && inv(i) > 0.0) {
-        const uint32_t c = e4m3_code(x(i) / (double)s(i), again);
-        w[i >> 2] = (w[i >> 2] & ~(0xffu << (8 * (i & 3)))) | (c << (8 * (i & 3)));
-      }
+      const E4m3Inverse a = of(i);
+      const uint32_t mask = 0xffu << (8 * (i & 3));
+      if (((w[i >> 2] ^ up[i >> 2]) & mask) != 0 || (!a.quick && a.s > 0.f))
+        w[i >> 2] = (w[i >> 2] & ~mask) | (e4m3_code(exact(i) / (double)a.s) << (8 * (i & 3)));
       __builtin_amdgcn_sched_barrier(0);  // one division at a time
     }
   }

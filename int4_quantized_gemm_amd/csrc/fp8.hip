@@ -5,15 +5,9 @@
 //
 //   s = fp32(amax / 448)    code = e4m3(x / s), nearest even, saturated
 //
-// computed in fp64, so codes and scales are those of exact arithmetic on x (or
-// on its rotation).
-//
-// A block of 512 threads takes a tile of 128 rows and 256 columns: 32 sets of
-// 16 lanes (row_sets.hpp), four consecutive rows each, so that a lane holds the
-// codes of four rows of a column as one dword when it turns the tile through
-// LDS. Row codes are written as the tile is read; column and block maxima are
-// taken on that first pass and their codes on a second one, which finds the
-// tile in L2.
+// Codes and scales are those of exact arithmetic on x (e4m3.hpp), or on its
+// rotation in fp64. Everything is read once: what a tile's scales are taken
+// from stays in registers until its codes are made.
 #include "block_ops.hpp"
 #include "e4m3.hpp"
 #include "row_sets.hpp"
@@ -22,199 +16,328 @@ namespace tp {
 
 namespace {
 
-constexpr int Q_SETS = 32, Q_ROWS = 128, Q_COLS = 256;
-constexpr int Q_PITCH = 33;  // dwords of a column's 128 codes in LDS
-
-// Element i of a lane: its column in the tile, after the transform or without.
-template <bool ROT>
-__device__ __forceinline__ int col_of(int l16, int i) {
-  return ROT ? 128 * (l16 >> 3) + (l16 & 7) + 8 * i : 128 * (i >> 3) + 8 * l16 + (i & 7);
-}
-
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
 
-// The lane's two runs of a row, zeros past the row's end.
+// Eight elements of a row, zeros from the left-th on.
 template <typename TX>
-__device__ __forceinline__ void load_tail(const TX* p, int64_t left, float (&v)[16]) {
+__device__ __forceinline__ void load_left(const TX* p, int64_t left, float (&v)[8]) {
+  if (left >= 8) {
+    load8(p, v);
+  } else {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (128 * h + 8 <= left) {
-      float u[8];
-      load8(p + 128 * h, u);
+    for (int j = 0; j < 8; ++j) v[j] = j < left ? widen(p[j]) : 0.f;
+  }
+}
+
+__device__ __forceinline__ float max8(const float (&v)[8]) {
+  float m = fabsf(v[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[8 * h + j] = u[j];
+  for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  return m;
+}
+
+__device__ __forceinline__ float set_max(float v) {
+  v = fmaxf(v, swz_xor<1>(v));
+  v = fmaxf(v, swz_xor<2>(v));
+  v = fmaxf(v, swz_xor<4>(v));
+  v = fmaxf(v, swz_xor<8>(v));
+  return v;
+}
+
+// The codes of eight values of one block.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const E4m3Inverse& s) {
+  uint32_t w[2];
+  e4m3_codes<8>(w, [&](int i) { return v[i]; }, [&](int i) { return (double)v[i]; }, [&](int) { return s; });
+  return uint2{w[0], w[1]};
+}
+
+constexpr int Q_ROWS = 128;  // rows of a tile whose columns or blocks are quantized
+constexpr int Q_PITCH = 33;  // dwords of a column's 128 codes in LDS
+
+}  // namespace
+
+// Row codes: a set of 16 lanes takes 128 columns of a row, a block 16 rows.
+template <typename TX>
+__global__ __launch_bounds__(256) void k_fp8_rows(QuantFp8Args a, uint32_t blocks_k) {
+  const int l16 = threadIdx.x & 15;
+  const uint32_t tile = blockIdx.x / blocks_k, g = blockIdx.x - tile * blocks_k;
+  const int64_t row = (int64_t)tile * 16 + (threadIdx.x >> 4), col = (int64_t)g * 128 + 8 * l16;
+  if (row >= a.m) return;
+  float v[8];
+  load_left((const TX*)a.x + row * a.ldx + col, a.k - col, v);
+  const float s = set_max(max8(v)) / (float)E4M3_MAX;
+  *reinterpret_cast<uint2*>(a.q + row * a.ldq + col) = codes8(v, e4m3_inverse(s));
+  if (l16 == 0) a.s[g * a.lds + row] = s;
+}
+
+// A tile of 128 rows and 128 columns: 32 sets of 16 lanes, four consecutive rows
+// each, so that a lane holds the codes of four rows of a column as one dword
+// when it turns the tile through LDS.
+template <typename TX>
+__global__ __launch_bounds__(512) void k_fp8_tile(QuantFp8Args a, uint32_t blocks_k) {
+  __shared__ float part[8][128];
+  __shared__ float scale[128];
+  __shared__ uint32_t cols[128 * Q_PITCH];
+  const int l16 = threadIdx.x & 15, set = threadIdx.x >> 4, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t tile = blockIdx.x / blocks_k, g = blockIdx.x - tile * blocks_k;
+  const int64_t r0 = (int64_t)tile * Q_ROWS, row = r0 + 4 * set, c0 = (int64_t)g * 128, col = c0 + 8 * l16;
+  float v[4][8];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (row + r < a.m) {
+      load_left((const TX*)a.x + (row + r) * a.ldx + col, a.k - col, v[r]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[8 * h + j] = 128 * h + j < left ? widen(p[128 * h + j]) : 0.f;
+      for (int j = 0; j < 8; ++j) v[r][j] = 0.f;
+    }
+
+  if (!a.blocks && a.q != nullptr) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float s = set_max(max8(v[r])) / (float)E4M3_MAX;
+      const uint2 w = codes8(v[r], e4m3_inverse(s));
+      if (row + r < a.m) {
+        *reinterpret_cast<uint2*>(a.q + (row + r) * a.ldq + col) = w;
+        if (l16 == 0) a.s[g * a.lds + row + r] = s;
+      }
     }
   }
+
+  // the scales of the tile's columns, or its one
+  float m[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    m[j] = fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])), fmaxf(fabsf(v[2][j]), fabsf(v[3][j])));
+    m[j] = fmaxf(m[j], swz_xor<16>(m[j]));
+    m[j] = fmaxf(m[j], __shfl_xor(m[j], 32));
+  }
+  if (a.blocks) {
+    const float one = set_max(max8(m));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[j] = one;
+  }
+  if (lane < 16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[wave][8 * l16 + j] = m[j];
+  }
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    float t = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) t = fmaxf(t, part[w][threadIdx.x]);
+    const float s = t / (float)E4M3_MAX;
+    scale[threadIdx.x] = s;
+    if (a.blocks) {
+      if (threadIdx.x == 0) {
+        if (a.q != nullptr) a.s[tile * a.lds + g] = s;
+        if (a.qt != nullptr) a.st[g * a.ldst + tile] = s;
+      }
+    } else if (c0 + threadIdx.x < a.k) {
+      a.st[tile * a.ldst + c0 + threadIdx.x] = s;
+    }
+  }
+  __syncthreads();
+  E4m3Inverse inv[8];
+  if (a.blocks) {
+    inv[0] = e4m3_inverse(scale[0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) inv[j] = inv[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) inv[j] = e4m3_inverse(scale[8 * l16 + j]);
+  }
+  uint32_t pack[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) pack[j] = 0u;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    uint32_t w[2];
+    e4m3_codes<8>(w, [&](int i) { return v[r][i]; }, [&](int i) { return (double)v[r][i]; },
+                  [&](int i) { return inv[i]; });
+    if (a.blocks && a.q != nullptr && row + r < a.m)
+      *reinterpret_cast<uint2*>(a.q + (row + r) * a.ldq + col) = uint2{w[0], w[1]};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) pack[j] |= ((w[j >> 2] >> (8 * (j & 3))) & 0xffu) << (8 * r);
+  }
+  if (a.qt == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cols[(8 * l16 + j) * Q_PITCH + set] = pack[j];
+  __syncthreads();
+  // eight lanes a column, 16 codes each
+  for (int c = threadIdx.x >> 3; c < 128; c += 64) {
+    const uint32_t* p = cols + c * Q_PITCH + 4 * (threadIdx.x & 7);
+    if (c0 + c < a.k)
+      *reinterpret_cast<u32x4_t*>(a.qt + (c0 + c) * a.ldqt + r0 + 16 * (threadIdx.x & 7)) =
+          u32x4_t{p[0], p[1], p[2], p[3]};
+  }
+}
+
+// ------------------------------------------------------------ rotated values
+// A set of 16 lanes holds a 256-group of a row as 16 fp64 values each; after the
+// transform register i of lane l is column 128 (l / 8) + l % 8 + 8 i of the
+// group (row_sets.hpp), so a set's lanes 0 .. 7 hold its first block of 128.
+namespace {
+
+constexpr int Q_SET_BYTES = 16 * 18 * 8;
+
+__device__ __forceinline__ int turned_col(int l16, int i) { return 128 * (l16 >> 3) + (l16 & 7) + 8 * i; }
+
+template <typename TX>
+__device__ __forceinline__ void rotated(const Runs<TX>& raw, double (&v)[16], uint8_t* buf, int l16) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = (double)raw.get(i) * 0.0625;
+  fwht16_regs(v);
+  transpose16(v, reinterpret_cast<double*>(buf), l16);
+  fwht16_regs(v);
+}
+
+// Largest magnitude of the lane's block of 128.
+__device__ __forceinline__ double half_set_max(double v) {
+  v = fmax(v, swz_xor<1>(v));
+  v = fmax(v, swz_xor<2>(v));
+  v = fmax(v, swz_xor<4>(v));
+  return v;
+}
+
+// The lane's 16 codes into the order of memory: 16 bytes of the group's row.
+__device__ __forceinline__ u32x4_t straight(const uint32_t (&w)[4], uint8_t* buf, int l16) {
+  wave_lds_sync();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) buf[turned_col(l16, i)] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+  wave_lds_sync();
+  return *reinterpret_cast<const u32x4_t*>(buf + 16 * l16);
 }
 
 }  // namespace
 
-template <typename TX, bool ROT>
-__global__ __launch_bounds__(512) void k_quant_fp8(QuantFp8Args a, int64_t tiles_k, int rows_per_block) {
-  constexpr int SET_BYTES = 16 * 18 * 8;
-  __shared__ __align__(16) uint8_t turn[ROT ? Q_SETS * SET_BYTES : 16];
-  __shared__ double part[8][Q_COLS];
-  __shared__ float scale[Q_COLS];
-  __shared__ double inverse[Q_COLS];
-  __shared__ uint32_t cols[Q_COLS * Q_PITCH];
-  const int l16 = threadIdx.x & 15, set = threadIdx.x >> 4, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t tile_m = blockIdx.x / tiles_k, tile_k = blockIdx.x - tile_m * tiles_k;
-  const int64_t r0 = tile_m * rows_per_block, c0 = tile_k * Q_COLS;
-  const int64_t kp = (a.k + 127) / 128 * 128;
-  const int per_set = rows_per_block / Q_SETS;
-  uint8_t* bbuf = turn + (ROT ? set * SET_BYTES : 0);
+template <typename TX>
+__global__ __launch_bounds__(256) void k_fp8_rows_rotated(QuantFp8Args a, uint32_t groups) {
+  __shared__ __align__(16) uint8_t turn[16 * Q_SET_BYTES];
+  const int l16 = threadIdx.x & 15, set = threadIdx.x >> 4;
+  const uint32_t tile = blockIdx.x / groups, g = blockIdx.x - tile * groups;
+  const int64_t row = (int64_t)tile * 16 + set, c0 = (int64_t)g * 256;
+  uint8_t* buf = turn + set * Q_SET_BYTES;
+  Runs<TX> raw;
+  if (row < a.m)
+    raw.load((const TX*)a.x + row * a.ldx + c0 + 8 * l16);
+  else
+    raw.zero();
   double v[16];
+  rotated(raw, v, buf, l16);
+  const float s = e4m3_scale(half_set_max(absmax16(v)));
+  const E4m3Inverse inv = e4m3_inverse(s);
+  uint32_t w[4];
+  e4m3_codes<16>(w, [&](int i) { return (float)v[i]; }, [&](int i) { return v[i]; }, [&](int) { return inv; });
+  const u32x4_t w4 = straight(w, buf, l16);
+  if (row < a.m) {
+    *reinterpret_cast<u32x4_t*>(a.q + row * a.ldq + c0 + 16 * l16) = w4;
+    if ((l16 & 7) == 0) a.s[(2 * g + (l16 >> 3)) * a.lds + row] = s;
+  }
+}
 
-  auto fetch = [&](int64_t row) {
-    float f[16];
-    if (row < a.m) {
-      load_tail((const TX*)a.x + row * a.ldx + c0 + 8 * l16, a.k - c0 - 8 * l16, f);
-    } else {
+// A tile of 128 rows and 256 columns, as k_fp8_tile; the four rows of a lane stay
+// in registers as fp64 (two waves a SIMD).
+template <typename TX>
+__global__ __launch_bounds__(512, 2) void k_fp8_tile_rotated(QuantFp8Args a, uint32_t groups) {
+  __shared__ __align__(16) uint8_t turn[32 * Q_SET_BYTES];
+  __shared__ float scale[256];
+  double(*part)[256] = reinterpret_cast<double(*)[256]>(turn);      // [8][256], after the transforms
+  uint32_t* cols = reinterpret_cast<uint32_t*>(turn + 8 * 256 * 8);  // [256][Q_PITCH]
+  static_assert(32 * Q_SET_BYTES >= 8 * 256 * 8 + 256 * Q_PITCH * 4, "the tile turns in the transforms' LDS");
+  const int l16 = threadIdx.x & 15, set = threadIdx.x >> 4, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t tile = blockIdx.x / groups, g = blockIdx.x - tile * groups;
+  const int64_t r0 = (int64_t)tile * Q_ROWS, row = r0 + 4 * set, c0 = (int64_t)g * 256;
+  uint8_t* buf = turn + set * Q_SET_BYTES;
+  Runs<TX> raw[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = 0.f;
-    }
+  for (int r = 0; r < 4; ++r)
+    if (row + r < a.m)
+      raw[r].load((const TX*)a.x + (row + r) * a.ldx + c0 + 8 * l16);
+    else
+      raw[r].zero();
+  double v[4][16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = (double)f[i];
-    if constexpr (ROT) {
-      fwht16_regs(v);
-      transpose16(v, reinterpret_cast<double*>(bbuf), l16);
-      fwht16_regs(v);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] *= 0.0625;
-    }
-  };
-  // The codes of a row as they lie in memory.
-  auto store_row = [&](int64_t row, const uint32_t (&w)[4]) {
-    uint8_t* q = a.q + row * a.ldq + c0;
-    if constexpr (ROT) {
-      wave_lds_sync();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) bbuf[col_of<true>(l16, i)] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
-      wave_lds_sync();
-      const u32x4_t w4 = *reinterpret_cast<const u32x4_t*>(bbuf + 16 * l16);
-      if (row < a.m) *reinterpret_cast<u32x4_t*>(q + 16 * l16) = w4;
-    } else if (row < a.m) {
-      if (c0 < kp) *reinterpret_cast<uint2*>(q + 8 * l16) = uint2{w[0], w[1]};
-      if (c0 + 128 < kp) *reinterpret_cast<uint2*>(q + 128 + 8 * l16) = uint2{w[2], w[3]};
-    }
-  };
+  for (int r = 0; r < 4; ++r) rotated(raw[r], v[r], buf, l16);
 
-  const bool by_row = !a.blocks && a.q != nullptr, by_col = !a.blocks && a.qt != nullptr;
-  double cm[16], bm[2] = {0.0, 0.0};
+  if (!a.blocks && a.q != nullptr) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) cm[i] = 0.0;
-#pragma unroll 1
-  for (int it = 0; it < per_set; ++it) {
-    const int64_t row = r0 + set * per_set + it;
-    fetch(row);
-    if (by_col) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) cm[i] = absmax2(cm[i], v[i]);
-    }
-    if (by_row || a.blocks) {
-      double am[2];
-      if constexpr (ROT) {  // lanes 0 .. 7 hold the first 128 columns
-        am[0] = absmax16(v);
-        am[0] = fmax(am[0], swz_xor<1>(am[0]));
-        am[0] = fmax(am[0], swz_xor<2>(am[0]));
-        am[0] = fmax(am[0], swz_xor<4>(am[0]));
-        am[1] = am[0];
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          am[h] = 0.0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) am[h] = absmax2(am[h], v[8 * h + j]);
-          am[h] = set_max(am[h]);
-        }
-      }
-      bm[0] = fmax(bm[0], am[0]);
-      bm[1] = fmax(bm[1], am[1]);
-      if (by_row) {
-        const float s[2] = {e4m3_scale(am[0]), e4m3_scale(am[1])};
-        const double inv[2] = {s[0] > 0.f ? 1.0 / (double)s[0] : 0.0, s[1] > 0.f ? 1.0 / (double)s[1] : 0.0};
-        uint32_t w[4];
-        e4m3_codes<16>(w, [&](int i) { return v[i]; }, [&](int i) { return s[i >> 3]; },
-                       [&](int i) { return inv[i >> 3]; });
-        store_row(row, w);
-        const int h = ROT ? l16 >> 3 : l16 & 1;
-        if (row < a.m && l16 == (ROT ? 8 * h : h) && c0 + 128 * h < kp)
-          a.s[(c0 / 128 + h) * a.lds + row] = ROT ? s[0] : (h ? s[1] : s[0]);
+    for (int r = 0; r < 4; ++r) {
+      const float s = e4m3_scale(half_set_max(absmax16(v[r])));
+      const E4m3Inverse inv = e4m3_inverse(s);
+      uint32_t w[4];
+      e4m3_codes<16>(w, [&](int i) { return (float)v[r][i]; }, [&](int i) { return v[r][i]; }, [&](int) { return inv; });
+      const u32x4_t w4 = straight(w, buf, l16);
+      if (row + r < a.m) {
+        *reinterpret_cast<u32x4_t*>(a.q + (row + r) * a.ldq + c0 + 16 * l16) = w4;
+        if ((l16 & 7) == 0) a.s[(2 * g + (l16 >> 3)) * a.lds + row + r] = s;
       }
     }
   }
-  if (!a.blocks && !by_col) return;
-
-  // the tile's scales
+  __syncthreads();  // the transforms' LDS is free
+  double m[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m[i] = absmax2(absmax2(v[0][i], v[1][i]), absmax2(v[2][i], v[3][i]));
   if (a.blocks) {
-    if constexpr (ROT) {
-      const double o = swz_xor<8>(bm[0]);
-      bm[1] = (l16 & 8) ? bm[0] : o;
-      bm[0] = (l16 & 8) ? o : bm[0];
-    }
+    const double one = half_set_max(absmax16(m));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      bm[h] = fmax(bm[h], swz_xor<16>(bm[h]));
-      bm[h] = fmax(bm[h], __shfl_xor(bm[h], 32));
-      if (lane == 0) part[wave][h] = bm[h];
-    }
-  } else {
+    for (int i = 0; i < 16; ++i) m[i] = one;
+  }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      cm[i] = fmax(cm[i], swz_xor<16>(cm[i]));
-      cm[i] = fmax(cm[i], __shfl_xor(cm[i], 32));
-      if (lane < 16) part[wave][col_of<ROT>(l16, i)] = cm[i];
-    }
+  for (int i = 0; i < 16; ++i) {
+    m[i] = fmax(m[i], swz_xor<16>(m[i]));
+    m[i] = fmax(m[i], __shfl_xor(m[i], 32));
+    if (lane < 16) part[wave][turned_col(l16, i)] = m[i];
   }
   __syncthreads();
-  if (threadIdx.x < Q_COLS) {
-    const int at = a.blocks ? threadIdx.x >> 7 : threadIdx.x;
-    double m = part[0][at];
+  if (threadIdx.x < 256) {
+    double t = part[0][threadIdx.x];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) m = fmax(m, part[w][at]);
-    const float s = e4m3_scale(m);
+    for (int w = 1; w < 8; ++w) t = fmax(t, part[w][threadIdx.x]);
+    const float s = e4m3_scale(t);
     scale[threadIdx.x] = s;
-    inverse[threadIdx.x] = s > 0.f ? 1.0 / (double)s : 0.0;
-    const int64_t col = c0 + threadIdx.x;
     if (a.blocks) {
-      if ((threadIdx.x & 127) == 0 && col < kp) {
-        if (a.q != nullptr) a.s[tile_m * a.lds + col / 128] = s;
-        if (a.qt != nullptr) a.st[col / 128 * a.ldst + tile_m] = s;
+      if ((threadIdx.x & 127) == 0) {
+        const int64_t b = 2 * (int64_t)g + (threadIdx.x >> 7);
+        if (a.q != nullptr) a.s[tile * a.lds + b] = s;
+        if (a.qt != nullptr) a.st[b * a.ldst + tile] = s;
       }
-    } else if (col < a.k) {
-      a.st[tile_m * a.ldst + col] = s;
+    } else {
+      a.st[tile * a.ldst + c0 + threadIdx.x] = s;
     }
   }
   __syncthreads();
-
   uint32_t pack[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) pack[i] = 0u;
-#pragma unroll 1
-  for (int it = 0; it < per_set; ++it) {
-    const int64_t row = r0 + set * per_set + it;
-    fetch(row);
-    uint32_t w[4];
-    e4m3_codes<16>(w, [&](int i) { return v[i]; }, [&](int i) { return scale[col_of<ROT>(l16, i)]; },
-                   [&](int i) { return inverse[col_of<ROT>(l16, i)]; });
-    if (a.blocks && a.q != nullptr) store_row(row, w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) pack[i] |= ((w[i >> 2] >> (8 * (i & 3))) & 0xffu) << (8 * it);
+  for (int r = 0; r < 4; ++r) {
+    uint32_t w[4];
+    e4m3_codes<16>(w, [&](int i) { return (float)v[r][i]; }, [&](int i) { return v[r][i]; },
+                   [&](int i) { return e4m3_inverse(scale[turned_col(l16, i)]); });
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pack[i] |= ((w[i >> 2] >> (8 * (i & 3))) & 0xffu) << (8 * r);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) cols[turned_col(l16, i) * Q_PITCH + set] = pack[i];
+  __syncthreads();
+  if (a.blocks && a.q != nullptr) {  // byte r of a column's dword is row 4 set + r
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t c = (cols[(16 * l16 + i) * Q_PITCH + set] >> (8 * r)) & 0xffu;
+        w[i >> 2] = (i & 3) == 0 ? c : w[i >> 2] | (c << (8 * (i & 3)));
+      }
+      if (row + r < a.m)
+        *reinterpret_cast<u32x4_t*>(a.q + (row + r) * a.ldq + c0 + 16 * l16) = u32x4_t{w[0], w[1], w[2], w[3]};
+    }
   }
   if (a.qt == nullptr) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) cols[col_of<ROT>(l16, i) * Q_PITCH + set] = pack[i];
-  __syncthreads();
-  // eight lanes a column, 16 codes each
-  for (int c = threadIdx.x >> 3; c < Q_COLS; c += 64) {
-    const int64_t col = c0 + c;
+  for (int c = threadIdx.x >> 3; c < 256; c += 64) {
     const uint32_t* p = cols + c * Q_PITCH + 4 * (threadIdx.x & 7);
-    const u32x4_t w = {p[0], p[1], p[2], p[3]};
-    if (col < a.k) *reinterpret_cast<u32x4_t*>(a.qt + col * a.ldqt + r0 + 16 * (threadIdx.x & 7)) = w;
+    *reinterpret_cast<u32x4_t*>(a.qt + (c0 + c) * a.ldqt + r0 + 16 * (threadIdx.x & 7)) = u32x4_t{p[0], p[1], p[2], p[3]};
   }
 }
 
@@ -222,14 +345,21 @@ namespace {
 
 template <typename TX>
 hipError_t quant_launch(const QuantFp8Args& a, hipStream_t stream) {
-  // rows alone need no tile of 128 of them: a row a set
-  const int rows = a.blocks || a.qt != nullptr ? Q_ROWS : Q_SETS;
-  const int64_t tiles_k = (a.k + Q_COLS - 1) / Q_COLS, tiles_m = (a.m + rows - 1) / rows;
-  const dim3 grid((unsigned)(tiles_m * tiles_k));
-  if (a.rotate)
-    hipLaunchKernelGGL((k_quant_fp8<TX, true>), grid, dim3(512), 0, stream, a, tiles_k, rows);
-  else
-    hipLaunchKernelGGL((k_quant_fp8<TX, false>), grid, dim3(512), 0, stream, a, tiles_k, rows);
+  const bool tiles = a.blocks || a.qt != nullptr;
+  const int64_t wide = a.rotate ? 256 : 128, high = tiles ? Q_ROWS : 16;
+  const uint32_t bk = (uint32_t)((a.k + wide - 1) / wide);
+  const dim3 grid((unsigned)((a.m + high - 1) / high * bk)), block(tiles ? 512 : 256);
+  if (a.rotate) {
+    if (tiles)
+      hipLaunchKernelGGL((k_fp8_tile_rotated<TX>), grid, block, 0, stream, a, bk);
+    else
+      hipLaunchKernelGGL((k_fp8_rows_rotated<TX>), grid, block, 0, stream, a, bk);
+  } else {
+    if (tiles)
+      hipLaunchKernelGGL((k_fp8_tile<TX>), grid, block, 0, stream, a, bk);
+    else
+      hipLaunchKernelGGL((k_fp8_rows<TX>), grid, block, 0, stream, a, bk);
+  }
   return hipGetLastError();
 }
 

@@ -118,21 +118,32 @@ __device__ __forceinline__ void store_cols(T* p, int left, bool vec, const float
 
 }  // namespace
 
-template <int BM, int BN, int WM, int WN>
+// Schedule. Two stages of one block of k (128 bytes a row, and the scales) in LDS:
+// direct loads fill one while the other is worked on, one barrier a step. The
+// scales come the same way: a load to registers would have to be waited for, and
+// with it, in order, every direct load before it (256 x 256 tiles, 4096 x 12288
+// x 4096: 258 us with the scale of b loaded so, 200 through LDS). A wave reads
+// its fragments of b once a step and each of a one ahead of its use, and issues a
+// matrix instruction with the vector work of the previous fragment in its shadow.
+template <int BM, int BN, int WM, int WN, int NS>
 struct F8Cfg {
   static constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, NT = 64 * NW;
   static constexpr int FM = WM / 16, FN = WN / 16;
-  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-  static constexpr int STAGE = A_BYTES + B_BYTES + 4 * (BM + BN);  // operands, then their scales
-  static constexpr int LOADS = (BM + BN) / 8, LPW = LOADS / NW;    // direct loads of 1 KB
+  static constexpr int A_BYTES = BM * 128, AB_BYTES = (BM + BN) * 128;
+  static constexpr int STAGE = AB_BYTES + 4 * (BM + BN);  // operands, then their scales
+  static constexpr int LOADS = (BM + BN) / 8, LPW = LOADS / NW;  // direct loads of 1 KB
+  static constexpr int LDS_BYTES = NS * STAGE;
   static_assert(LOADS % NW == 0 && BM % 64 == 0 && BN % 64 == 0 && 128 % WN == 0, "whole loads, one block of b a wave");
+  static_assert((BM + BN) / 64 <= NW && LDS_BYTES <= 160 * 1024, "a load of scales a wave");
+  static_assert((NS & (NS - 1)) == 0 && (NS - 2) * (LPW + 1) < 64, "ring and vmcnt");
+  static_assert(BN % 128 == 0, "tiles begin with a block of b");
 };
 
 // PARTIAL: the steps [blockIdx.y * sps, ..) of k, raw sums to part.
-template <int BM, int BN, int WM, int WN, bool BROWS, bool OUT_BF16, bool PARTIAL>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void k_qgemm_fp8(GemmFp8Args g, int tiles_m, int tiles_n,
+template <int BM, int BN, int WM, int WN, int NS, bool BROWS, bool OUT_BF16, bool PARTIAL>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void k_qgemm_fp8(GemmFp8Args g, int tiles_m, int tiles_n,
                                                                             int gm, int sps, int64_t ldp) {
-  using Cfg = F8Cfg<BM, BN, WM, WN>;
+  using Cfg = F8Cfg<BM, BN, WM, WN, NS>;
   constexpr int FM = Cfg::FM, FN = Cfg::FN, LPW = Cfg::LPW;
   extern __shared__ __align__(1024) uint8_t ring[];
   int tm, tn;
@@ -148,39 +159,58 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void k_qgemm_fp8(Gem
   const int KB = (int)(g.k >> 7);
   const int ks0 = PARTIAL ? blockIdx.y * sps : 0;
   const int KS = PARTIAL ? min(sps, KB - ks0) : KB;
-  const uint8_t* src[LPW];
-  int dst[LPW];
+  // Direct loads: a uniform base and a 32-bit offset a lane (row pitches below
+  // 2^24). Past the last stage they fetch it again, to a buffer nobody reads: no
+  // branch in the loop.
+  const uint8_t* sbase[LPW];
+  uint32_t soff[LPW];
 #pragma unroll
   for (int i = 0; i < LPW; ++i) {
     const int L = wave * LPW + i;
     if (L < BM / 8) {
       const int row = L * 8 + (lane >> 3), c = (lane & 7) ^ swz_a(row);
-      src[i] = g.a + (int64_t)min(m0 + row, M - 1) * g.lda + c * 16;
+      sbase[i] = g.a + (int64_t)m0 * g.lda + (int64_t)ks0 * 128;
+      soff[i] = (uint32_t)min(row, M - 1 - m0) * (uint32_t)g.lda + c * 16;
     } else {
       const int row = (L - BM / 8) * 8 + (lane >> 3), c = (lane & 7) ^ swz_b(row);
-      src[i] = g.b + (int64_t)min(n0 + row, N - 1) * g.ldb + c * 16;
+      sbase[i] = g.b + (int64_t)n0 * g.ldb + (int64_t)ks0 * 128;
+      soff[i] = (uint32_t)min(row, N - 1 - n0) * (uint32_t)g.ldb + c * 16;
     }
-    src[i] += (int64_t)ks0 * 128;
-    dst[i] = L * 1024;
   }
-  const float* ssrc[2] = {nullptr, nullptr};  // scales: 64 to a load
-  if (wave < BM / 64) ssrc[0] = g.sa + (int64_t)ks0 * g.ldsa + min(m0 + wave * 64 + lane, M - 1);
-  if (BROWS && wave < BN / 64) ssrc[1] = g.sb + (int64_t)ks0 * g.ldsb + min(n0 + wave * 64 + lane, N - 1);
+  // Scales, 64 to a load, one load a wave: those of a, then those of b's rows, or
+  // of its blocks of 128 rows (surplus waves repeat one: the same bytes to the
+  // same place).
+  const int sl = wave < BM / 64 + (BROWS ? BN / 64 : 1) ? wave : wave % (BM / 64);
+  const float* scbase = g.sa + (int64_t)ks0 * g.ldsa + m0;
+  int64_t scoff = min(sl * 64 + lane, M - 1 - m0), scstep = g.ldsa;
+  if (sl >= BM / 64) {
+    scbase = BROWS ? g.sb + (int64_t)ks0 * g.ldsb + n0 : g.sb + (int64_t)(n0 >> 7) * g.ldsb + ks0;
+    scoff = BROWS ? min((sl - BM / 64) * 64 + lane, N - 1 - n0)
+                  : min(lane, min((BN - 1) >> 7, ((N - 1) >> 7) - (n0 >> 7))) * g.ldsb;
+    scstep = BROWS ? g.ldsb : 1;
+  }
   auto issue = [&](int ks) {
-    uint8_t* base = ring + (ks & 1) * Cfg::STAGE;
+    uint8_t* const stage = ring + (ks & (NS - 1)) * Cfg::STAGE;
+    const int at = min(ks, KS - 1);
 #pragma unroll
     for (int i = 0; i < LPW; ++i)
-      __builtin_amdgcn_global_load_lds((const void*)(src[i] + (int64_t)ks * 128), (lds_void_t*)(base + dst[i]), 16, 0, 0);
-    uint8_t* sbase = base + Cfg::A_BYTES + Cfg::B_BYTES;
-    if (wave < BM / 64)
-      __builtin_amdgcn_global_load_lds((const void*)(ssrc[0] + (int64_t)ks * g.ldsa), (lds_void_t*)(sbase + wave * 256),
-                                       4, 0, 0);
-    if (BROWS && wave < BN / 64)
-      __builtin_amdgcn_global_load_lds((const void*)(ssrc[1] + (int64_t)ks * g.ldsb),
-                                       (lds_void_t*)(sbase + 4 * BM + wave * 256), 4, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(sbase[i] + (int64_t)at * 128 + soff[i]),
+                                       (lds_void_t*)(stage + (wave * LPW + i) * 1024), 16, 0, 0);
+    __builtin_amdgcn_global_load_lds((const void*)(scbase + (int64_t)at * scstep + scoff),
+                                     (lds_void_t*)(stage + Cfg::AB_BYTES + sl * 256), 4, 0, 0);
   };
-  // the scale of b that the whole wave shares
-  const float* sbp = BROWS ? nullptr : g.sb + (int64_t)(min(n0 + wn0, N - 1) >> 7) * g.ldsb + ks0;
+  // Fragment addresses: the two granules of a lane differ by one bit.
+  const int arow = wm0 + r16, brow = wn0 + 4 * FN * (r16 >> 2) + (r16 & 3);
+  const int aoff = arow * 128 + (((2 * g4) ^ swz_a(arow)) << 4);  // (16 rows on: the same swizzle)
+  const int boff = Cfg::A_BYTES + brow * 128 + (((2 * g4) ^ swz_b(brow)) << 4);  // (4 rows on: the same)
+  auto read_a = [&](const uint8_t* st, int i) {
+    const uint8_t* p = st + i * 2048;
+    return join8(*reinterpret_cast<const u32x4_t*>(p + aoff), *reinterpret_cast<const u32x4_t*>(p + (aoff ^ 16)));
+  };
+  auto read_b = [&](const uint8_t* st, int j) {
+    const uint8_t* p = st + j * 512;
+    return join8(*reinterpret_cast<const u32x4_t*>(p + boff), *reinterpret_cast<const u32x4_t*>(p + (boff ^ 16)));
+  };
 
   f32x4_t acc[FM][FN];
 #pragma unroll
@@ -188,51 +218,60 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void k_qgemm_fp8(Gem
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  issue(0);
-  __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE(0));
+  constexpr int MFMAS = FN * (OUT_BF16 ? 1 : 4);
+  constexpr int VALUS = (FN * (BROWS ? 8 : 4) + (OUT_BF16 ? 0 : 16) + MFMAS - 1) / MFMAS;
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) issue(s);
+  __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE((NS - 2) * (LPW + 1)));
   barrier_only();
   for (int ks = 0; ks < KS; ++ks) {
-    if (ks + 1 < KS) issue(ks + 1);
-    const uint8_t* as = ring + (ks & 1) * Cfg::STAGE;
-    const uint8_t* bs = as + Cfg::A_BYTES;
-    const float* ss = reinterpret_cast<const float*>(bs + Cfg::B_BYTES);
-    const float sw = BROWS ? 1.f : sbp[ks];
-    Frag<!OUT_BF16> fb[FN], fa;
+    issue(ks + NS - 1);
+    const uint8_t* st = ring + (ks & (NS - 1)) * Cfg::STAGE;
+    const float* ss = reinterpret_cast<const float*>(st + Cfg::AB_BYTES);
+    Frag<!OUT_BF16> wb[FN], wa;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int row = wn0 + 4 * FN * (r16 >> 2) + 4 * j + (r16 & 3);
-      const uint8_t* p = bs + row * 128;
-      fb[j].set(join8(*reinterpret_cast<const u32x4_t*>(p + (((2 * g4) ^ swz_b(row)) << 4)),
-                      *reinterpret_cast<const u32x4_t*>(p + (((2 * g4 + 1) ^ swz_b(row)) << 4))));
-    }
+    for (int j = 0; j < FN; ++j) wb[j].set(read_b(st, j));
+    i32x8_t fa = read_a(st, 0);
+    const float sw = BROWS ? 1.f : ss[BM + (wn0 >> 7)];
+    float sc[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sc[i] = ss[arow + 16 * i];
     f32x4_t sbv[BROWS ? FN : 1];
     if constexpr (BROWS) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) sbv[j] = *reinterpret_cast<const f32x4_t*>(ss + BM + wn0 + 4 * FN * g4 + 4 * j);
     }
     f32x4_t p[2][FN];
-    float sc[2];
     auto fold = [&](int i) {
+      const float s = sc[i] * sw;
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+      for (int j = 0; j < FN; ++j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = fmaf(p[i & 1][j][e], BROWS ? sc[i & 1] * sbv[BROWS ? j : 0][e] : sc[i & 1], acc[i][j][e]);
+          acc[i][j][e] = fmaf(p[i & 1][j][e], BROWS ? s * sbv[BROWS ? j : 0][e] : s, acc[i][j][e]);
+        asm volatile("" : "+v"(acc[i][j]));  // here, not behind the barrier
+      }
     };
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int row = wm0 + i * 16 + r16;
-      const uint8_t* q = as + row * 128;
-      fa.set(join8(*reinterpret_cast<const u32x4_t*>(q + (((2 * g4) ^ swz_a(row)) << 4)),
-                   *reinterpret_cast<const u32x4_t*>(q + (((2 * g4 + 1) ^ swz_a(row)) << 4))));
-      sc[i & 1] = ss[row] * sw;
-      block_sums(fb, fa, p[i & 1]);
+      wa.set(fa);
+      if (i + 1 < FM) fa = read_a(st, i + 1);
+      block_sums(wb, wa, p[i & 1]);
       if (i > 0) fold(i - 1);
+#pragma unroll
+      for (int t = 0; t < MFMAS; ++t) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, VALUS, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
     fold(FM - 1);
-    __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE(0) & LGKMCNT0_ENCODE);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE((NS - 2) * (LPW + 1)) & LGKMCNT0_ENCODE);  // the next stage has landed
     barrier_only();
   }
+  __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE(0));  // no load to LDS outlives the block
 
   const int nb = n0 + wn0 + 4 * FN * g4;
   if constexpr (PARTIAL) {
@@ -280,10 +319,10 @@ __global__ __launch_bounds__(256) void k_qgemm_fp8_join(GemmFp8Args g, int split
 }
 
 // Few rows: bound by the bytes of b, which go straight to registers (and are
-// summed the exact way whatever C's type). A block
-// takes 16 FN rows of b; its eight waves deal the steps of k among themselves
-// and join their sums through LDS in wave order.
-template <int FM, int FN, bool BROWS, bool OUT_BF16>
+// summed the exact way whatever C's type). A block takes 16 FN rows of b; its
+// eight waves deal the steps of k among themselves, U of them in flight each, and
+// join their sums through LDS in wave order.
+template <int FM, int FN, int U, bool BROWS, bool OUT_BF16>
 __global__ __launch_bounds__(512, 1) void k_qgemm_fp8_few(GemmFp8Args g) {
   constexpr int NW = 8;
   __shared__ f32x4_t sums[NW][FM * FN][64];
@@ -309,33 +348,48 @@ __global__ __launch_bounds__(512, 1) void k_qgemm_fp8_few(GemmFp8Args g) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int ks = wave; ks < KB; ks += NW) {
-    Frag<true> fb[FN], fa[FM];
+  for (int ks0 = wave; ks0 < KB; ks0 += NW * U) {
+    i32x8_t rb[U][FN], ra[U][FM];
+    float sc[U][FM];
+    f32x4_t sbv[U][FN];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(bp[j] + (int64_t)ks * 128);
-      fb[j].set(join8(p[0], p[1]));
-    }
-    float sc[FM];
+    for (int u = 0; u < U; ++u) {
+      // (past the last step: the last one again, with scales of zero)
+      const int ks = ks0 + NW * u, at = min(ks, KB - 1);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(ap[i] + (int64_t)ks * 128);
-      fa[i].set(join8(p[0], p[1]));
-      sc[i] = sp[i][(int64_t)ks * g.ldsa];
-    }
-    f32x4_t sbv[FN];
+      for (int j = 0; j < FN; ++j) {
+        const u32x4_t* p = reinterpret_cast<const u32x4_t*>(bp[j] + (int64_t)at * 128);
+        rb[u][j] = join8(p[0], p[1]);
+      }
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sbv[j][e] = BROWS ? sbp[(int64_t)ks * g.ldsb + min(nb + 4 * j + e, N - 1)] : sbp[ks];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      f32x4_t p[FN];
-      block_sums(fb, fa[i], p);
+      for (int i = 0; i < FM; ++i) {
+        const u32x4_t* p = reinterpret_cast<const u32x4_t*>(ap[i] + (int64_t)at * 128);
+        ra[u][i] = join8(p[0], p[1]);
+        sc[u][i] = ks < KB ? sp[i][(int64_t)at * g.ldsa] : 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[j][e], sc[i] * sbv[j][e], acc[i][j][e]);
+        for (int e = 0; e < 4; ++e)
+          sbv[u][j][e] = BROWS ? sbp[(int64_t)at * g.ldsb + min(nb + 4 * j + e, N - 1)] : sbp[at];
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all loads of the batch go out first
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u > 0 && ks0 + NW * u >= KB) break;
+      Frag<true> fb[FN], fa;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j].set(rb[u][j]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        fa.set(ra[u][i]);
+        f32x4_t p[FN];
+        block_sums(fb, fa, p);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[j][e], sc[u][i] * sbv[u][j][e], acc[i][j][e]);
+      }
     }
   }
 #pragma unroll
@@ -361,10 +415,9 @@ __global__ __launch_bounds__(512, 1) void k_qgemm_fp8_few(GemmFp8Args g) {
 // ---------------------------------------------------------------- launchers
 namespace {
 
-constexpr int64_t FEW_ROWS = 64;
 constexpr int64_t F8_CUS = 256;
 
-enum F8Tile { F8_FEW, F8_256x256, F8_128x128 };
+enum F8Tile { F8_FEW, F8_256x256, F8_128x128, F8_64x128 };
 struct F8Plan {
   F8Tile tile;
   int splits, sps;
@@ -372,79 +425,107 @@ struct F8Plan {
 
 int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
 
-F8Plan plan_of(int64_t m, int64_t n, int64_t k) {
+// The tile and the splits of k that take the least time by these measured times
+// of a step of k (bf16 C, fp32 C):
+//   64 x 128    four stages, a block a compute unit: 0.42, 0.8 us
+//   128 x 128   two stages, two blocks a compute unit: 1.13, 2.8 us for both of
+//               them, 0.72, 1.4 for one that is alone
+//   256 x 256   two stages, a block a compute unit, bf16 C only (the widened
+//               fragments do not fit beside its sums): 2.05 us
+// and of a split product's join, 3 us and a write and a read of the partial sums
+// at 3 TB/s. Measured: 2000 x 4096, k 4096, bf16, 128 x 128 39 us, 256 x 256 57;
+// 4096 x 12288 the same way 232 and 200; 300 x 4096, 64 x 128 15.5 us, 128 x 128
+// 24; 64 x 4096, k 12288, 64 x 128 37 us unsplit, 15.6 in 6 splits.
+// Few rows: one block row of 16 takes their bytes of b once more each, so up to
+// 16 rows always, up to 64 where 16-row blocks times n k stay below 2^25 (32 x
+// 4096 x 4096 9.1 against 11.4 us, 64 x 4096 x 4096 14.4 against 11.4).
+F8Plan plan_of(int64_t m, int64_t n, int64_t k, bool c_bf16) {
   const int64_t kb = k / 128;
-  if (m <= FEW_ROWS) return F8Plan{F8_FEW, 1, 0};
-  if (tiles_of(m, n, 256, 256) >= F8_CUS / 2) return F8Plan{F8_256x256, 1, 0};
-  const int64_t tiles = tiles_of(m, n, 128, 128);
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(F8_CUS / tiles, kb / 4));
-  const int64_t sps = (kb + splits - 1) / splits;
-  return F8Plan{F8_128x128, (int)((kb + sps - 1) / sps), (int)sps};
+  if (m <= 16 || (m <= 64 && (m + 15) / 16 * n * k <= ((int64_t)1 << 25))) return F8Plan{F8_FEW, 1, 0};
+  const double step64 = c_bf16 ? 0.42 : 0.8, one128 = c_bf16 ? 0.72 : 1.4, two128 = c_bf16 ? 1.13 : 2.8;
+  auto rounds = [](int64_t tiles) { return (tiles + F8_CUS - 1) / F8_CUS; };
+  const int64_t t64 = tiles_of(m, n, 64, 128), r128 = rounds(tiles_of(m, n, 128, 128));
+  F8Plan best{F8_128x128, 1, (int)kb};
+  double least = ((double)(r128 / 2) * two128 + (double)(r128 & 1) * one128) * (double)kb;
+  const double big = (double)rounds(tiles_of(m, n, 256, 256)) * 2.05 * (double)kb;
+  if (c_bf16 && big < least) {
+    best = F8Plan{F8_256x256, 1, (int)kb};
+    least = big;
+  }
+  for (int64_t s = 1; s <= kb && s <= 16 && (s == 1 || (t64 * s <= F8_CUS)); ++s) {
+    const int64_t sps = (kb + s - 1) / s, splits = (kb + sps - 1) / sps;
+    const double join = splits == 1 ? 0.0 : 3.0 + (double)(splits * m * n) * 8.0 / 3e6;
+    const double t = (double)rounds(t64 * splits) * (double)sps * step64 + join;
+    if (t < least) {
+      best = F8Plan{F8_64x128, (int)splits, (int)sps};
+      least = t;
+    }
+  }
+  return best;
 }
 
 int64_t pitch_of(int64_t n) { return (n + 3) / 4 * 4; }
 
-template <int BM, int BN, int WM, int WN, bool BROWS>
-hipError_t tile_launch(const GemmFp8Args& g, const F8Plan& p, hipStream_t stream) {
-  using Cfg = F8Cfg<BM, BN, WM, WN>;
+// gm: tile rows that an XCD walks together (pp_map_tile).
+template <int BM, int BN, int WM, int WN, int NS, bool BROWS, bool OUT_BF16>
+hipError_t tile_launch(const GemmFp8Args& g, const F8Plan& p, int gm, hipStream_t stream) {
+  using Cfg = F8Cfg<BM, BN, WM, WN, NS>;
   const int tiles_m = (int)((g.m + BM - 1) / BM), tiles_n = (int)((g.n + BN - 1) / BN);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)p.splits), block(Cfg::NT);
-  const size_t lds = 2 * Cfg::STAGE;
   const int64_t ldp = pitch_of(g.n);
-  // (OUT_BF16 of partial sums: the way a block is summed)
-#define TP_LAUNCH_F8(OB, PA) \
-  hipLaunchKernelGGL((k_qgemm_fp8<BM, BN, WM, WN, BROWS, OB, PA>), grid, block, lds, stream, g, tiles_m, tiles_n, 8, p.sps, ldp)
   if (p.splits == 1) {
-    if (g.c_bf16) TP_LAUNCH_F8(true, false); else TP_LAUNCH_F8(false, false);
+    hipLaunchKernelGGL((k_qgemm_fp8<BM, BN, WM, WN, NS, BROWS, OUT_BF16, false>), grid, block, Cfg::LDS_BYTES, stream, g,
+                       tiles_m, tiles_n, gm, p.sps, ldp);
     return hipGetLastError();
   }
   if (g.part == nullptr) return hipErrorInvalidValue;
-  if (g.c_bf16) TP_LAUNCH_F8(true, true); else TP_LAUNCH_F8(false, true);
-#undef TP_LAUNCH_F8
+  hipLaunchKernelGGL((k_qgemm_fp8<BM, BN, WM, WN, NS, BROWS, OUT_BF16, true>), grid, block, Cfg::LDS_BYTES, stream, g, tiles_m,
+                     tiles_n, gm, p.sps, ldp);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t blocks = std::min<int64_t>((g.m * (ldp / 4) + 255) / 256, 65536);
-  if (g.c_bf16)
-    hipLaunchKernelGGL((k_qgemm_fp8_join<true>), dim3((unsigned)blocks), dim3(256), 0, stream, g, p.splits, ldp);
-  else
-    hipLaunchKernelGGL((k_qgemm_fp8_join<false>), dim3((unsigned)blocks), dim3(256), 0, stream, g, p.splits, ldp);
+  hipLaunchKernelGGL((k_qgemm_fp8_join<OUT_BF16>), dim3((unsigned)blocks), dim3(256), 0, stream, g, p.splits, ldp);
   return hipGetLastError();
 }
 
-template <int FM, bool BROWS>
+template <int FM, int U, bool BROWS>
 hipError_t few_launch(const GemmFp8Args& g, hipStream_t stream) {
   constexpr int FN = 1;
   const dim3 grid((unsigned)((g.n + 16 * FN - 1) / (16 * FN))), block(512);
   if (g.c_bf16)
-    hipLaunchKernelGGL((k_qgemm_fp8_few<FM, FN, BROWS, true>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((k_qgemm_fp8_few<FM, FN, U, BROWS, true>), grid, block, 0, stream, g);
   else
-    hipLaunchKernelGGL((k_qgemm_fp8_few<FM, FN, BROWS, false>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((k_qgemm_fp8_few<FM, FN, U, BROWS, false>), grid, block, 0, stream, g);
   return hipGetLastError();
 }
 
-template <bool BROWS>
-hipError_t gemm_launch(const GemmFp8Args& g, hipStream_t stream) {
-  const F8Plan p = plan_of(g.m, g.n, g.k);
+template <bool BROWS, bool OUT_BF16>
+hipError_t plan_launch(const GemmFp8Args& g, const F8Plan& p, hipStream_t stream) {
   switch (p.tile) {
     case F8_FEW:
-      if (g.m <= 16) return few_launch<1, BROWS>(g, stream);
-      if (g.m <= 32) return few_launch<2, BROWS>(g, stream);
-      return few_launch<4, BROWS>(g, stream);
-    case F8_256x256: return tile_launch<256, 256, 128, 64, BROWS>(g, p, stream);
-    case F8_128x128: return tile_launch<128, 128, 64, 32, BROWS>(g, p, stream);
+      if (g.m <= 16) return few_launch<1, 4, BROWS>(g, stream);
+      if (g.m <= 32) return few_launch<2, 2, BROWS>(g, stream);
+      return few_launch<4, 2, BROWS>(g, stream);
+    case F8_256x256:
+      if constexpr (OUT_BF16) return tile_launch<256, 256, 128, 64, 2, BROWS, true>(g, p, 8, stream);
+      break;
+    case F8_128x128: return tile_launch<128, 128, 64, 64, 2, BROWS, OUT_BF16>(g, p, 8, stream);
+    case F8_64x128: return tile_launch<64, 128, 32, 32, 4, BROWS, OUT_BF16>(g, p, 8, stream);
   }
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-int64_t qgemm_fp8_partial_bytes(int64_t m, int64_t n, int64_t k) {
-  const F8Plan p = plan_of(m, n, k);
+int64_t qgemm_fp8_partial_bytes(int64_t m, int64_t n, int64_t k, bool c_bf16) {
+  const F8Plan p = plan_of(m, n, k, c_bf16);
   return p.splits == 1 ? 0 : (int64_t)p.splits * m * pitch_of(n) * 4;
 }
 
 hipError_t launch_qgemm_fp8(const GemmFp8Args& g, hipStream_t stream) {
-  return g.b_rows ? gemm_launch<true>(g, stream) : gemm_launch<false>(g, stream);
+  const F8Plan p = plan_of(g.m, g.n, g.k, g.c_bf16);
+  if (g.b_rows) return g.c_bf16 ? plan_launch<true, true>(g, p, stream) : plan_launch<true, false>(g, p, stream);
+  return g.c_bf16 ? plan_launch<false, true>(g, p, stream) : plan_launch<false, false>(g, p, stream);
 }
 
 }  // namespace tp

@@ -8,6 +8,7 @@
 // The row sits in the registers of its sets of lanes (row_sets.hpp), so the
 // mean comes first and the squares are those of the deviations: no digits are
 // lost in rows far off zero, and every element is read once.
+#include <algorithm>
 #include <type_traits>
 
 #include "block_ops.hpp"
@@ -19,33 +20,53 @@ namespace tp {
 
 enum { LN_OUT_I8 = 0, LN_OUT_BF16 = 1, LN_OUT_FP8 = 2 };
 
-// Sum (or maximum) over the threads of a row: all threads of the block call it
-// with the same red, which the next join but one may use again.
-template <bool MAX>
-__device__ __forceinline__ double row_join(double v, const Place& pl, int groups, double* red) {
-  v = MAX ? set_max(v) : set_sum(v);
+// Sums (or maxima) of N values over the threads of a row: all threads of the block
+// call it, with red [N][sets] of its own for each join of a row.
+template <int N, bool MAX>
+__device__ __forceinline__ void row_join(double (&v)[N], const Place& pl, int groups, double* red) {
+  const int sets = blockDim.x >> 4;
   int first = pl.slot * groups, count = pl.active ? groups : 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = MAX ? set_max(v[i]) : set_sum(v[i]);
   if (pl.wide) {  // sets past the row hold zeros
-    const double o = swz_xor<16>(v);
-    v = MAX ? fmax(v, o) : v + o;
-    const double p = __shfl_xor(v, 32);
-    v = MAX ? fmax(v, p) : v + p;
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const double o = swz_xor<16>(v[i]);
+      v[i] = MAX ? fmax(v[i], o) : v[i] + o;
+      const double p = __shfl_xor(v[i], 32);
+      v[i] = MAX ? fmax(v[i], p) : v[i] + p;
+      if ((threadIdx.x & 63) == 0) red[i * sets + (threadIdx.x >> 6)] = v[i];
+    }
     first = 0;
     count = pl.active ? (int)(blockDim.x >> 6) : 0;
   } else if (pl.l16 == 0) {
-    red[pl.set] = v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[i * sets + pl.set] = v[i];
   }
   __syncthreads();
-  double s = 0.0;
-  for (int w = 0; w < count; ++w) s = MAX ? fmax(s, red[first + w]) : s + red[first + w];
-  return s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.0;
+  for (int w = 0; w < count; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const double o = red[i * sets + first + w];
+      v[i] = MAX ? fmax(v[i], o) : v[i] + o;
+    }
+}
+
+// What is read again after a join is widened again: not kept in twice the
+// registers across it.
+template <int N>
+__device__ __forceinline__ void afresh(float (&t)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(t[i]));
 }
 
 // ------------------------------------------------------------------ forward
 // Codes: fp64 throughout, so they are those of exact arithmetic on the normed
 // row. bf16 rows: the deviations and the row factor in fp64, what follows in
-// fp32, one rounding.
+// fp32, one rounding. gamma and beta are fetched with the row, for codes behind
+// the first join, where few registers are taken.
 template <typename TX, typename TS, bool RES, int OUT, int NT>
 __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_per_block) {
   typedef typename std::conditional<OUT == LN_OUT_BF16, float, double>::type T;
@@ -59,22 +80,6 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
   const int64_t col = (int64_t)pl.grp * 256 + pl.l16 * 8;
   const int64_t k = (int64_t)a.groups * 256;
   const double inv_k = 1.0 / (double)k;
-  PhiloxKey key{};
-  if (RES && a.drop.rng != nullptr) key = philox_key(a.drop.rng);
-
-  float gm[16], bt[16];
-  if (pl.active) {
-    load_vec16(a.gamma, col, gm);
-    if (a.beta.p != nullptr) load_vec16(a.beta, col, bt);
-  }
-  if (!pl.active || a.beta.p == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) bt[i] = 0.f;
-  }
-  if (!pl.active) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) gm[i] = 0.f;
-  }
   const int64_t step = (int64_t)gridDim.x * pl.rows;
   for (int64_t base = (int64_t)blockIdx.x * pl.rows; base < a.m; base += step) {
     const int64_t row = base + pl.slot;
@@ -90,6 +95,7 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
     }
     float t[16];
     if (RES && a.drop.rng != nullptr) {
+      const PhiloxKey key = philox_key(a.drop.rng);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const u32x4_t w = philox4x32_10(key, (uint64_t)(row * k + col + 128 * h) >> 3);
@@ -106,18 +112,39 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
       if (live) store16((TS*)a.sum + row * a.ldsum + col, t);
     }
 
-    double s = 0.0;
+    float gm[16], bt[16];
+    auto weights = [&]() {
+      if (pl.active) {
+        load_vec16(a.gamma, col, gm);
+        if (a.beta.p != nullptr) load_vec16(a.beta, col, bt);
+      }
+      if (!pl.active || a.beta.p == nullptr) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += (double)t[i];
-    const double mu = row_join<false>(s, pl, a.groups, red) * inv_k;
-    s = 0.0;
+        for (int i = 0; i < 16; ++i) bt[i] = 0.f;
+      }
+      if (!pl.active) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) gm[i] = 0.f;
+      }
+    };
+    if (OUT == LN_OUT_BF16) weights();
+    double s[1] = {0.0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[0] += (double)t[i];
+    row_join<1, false>(s, pl, a.groups, red);
+    const double mu = s[0] * inv_k;
+    afresh(t);
+    if (OUT != LN_OUT_BF16) weights();
+    s[0] = 0.0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const double d = (double)t[i] - mu;
-      s = fma(d, d, s);
+      s[0] = fma(d, d, s[0]);
     }
-    if (!pl.active) s = 0.0;
-    const double r = 1.0 / sqrt(row_join<false>(s, pl, a.groups, red + sets) * inv_k + a.eps);
+    if (!pl.active) s[0] = 0.0;
+    row_join<1, false>(s, pl, a.groups, red + sets);
+    const double r = 1.0 / sqrt(s[0] * inv_k + a.eps);
+    afresh(t);
 
     T v[16];
 #pragma unroll
@@ -127,6 +154,7 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
         v[i] = fmaf((float)n, gm[i], bt[i]);
       else
         v[i] = fma(n, (double)gm[i], (double)bt[i]);
+      if ((i & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four at a time: fewer registers
     }
     if (a.rotate) {
 #pragma unroll
@@ -134,16 +162,18 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
       fwht16_regs(v);
       transpose16(v, tbuf, pl.l16);
       fwht16_regs(v);
+    } else if (OUT == LN_OUT_I8) {
+      transpose16(v, tbuf, pl.l16);  // the same output order either way
     }
+    // after the transpose register q is element l16 of lane q's two runs
+    const int at = 128 * (pl.l16 >> 3) + (pl.l16 & 7);
 
     if constexpr (OUT == LN_OUT_BF16) {
       if (a.rotate) transpose16_back(v, tbuf, pl.l16);
       if (live) store16((uint16_t*)a.y + row * a.ldy + col, v);
     } else if constexpr (OUT == LN_OUT_FP8) {
-      // A set holds two blocks of 128. After the transform its lanes 0 .. 7 hold
-      // the first one, register q being element l16 of lane q's two runs;
-      // without it the first run of every lane is the first one's.
-      uint32_t w[4];
+      // A set holds two blocks of 128: after the transform its lanes 0 .. 7 hold
+      // the first one, without it the first run of every lane is the first one's.
       uint8_t* yrow = (uint8_t*)a.y + row * a.ldy + (int64_t)pl.grp * 256;
       if (a.rotate) {
         double am = absmax16(v);
@@ -151,9 +181,9 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
         am = fmax(am, swz_xor<2>(am));
         am = fmax(am, swz_xor<4>(am));
         const float sc = e4m3_scale(am);
-        const double inv = sc > 0.f ? 1.0 / (double)sc : 0.0;
-        e4m3_codes<16>(w, [&](int i) { return v[i]; }, [&](int) { return sc; }, [&](int) { return inv; });
-        const int at = 128 * (pl.l16 >> 3) + (pl.l16 & 7);
+        const E4m3Inverse inv = e4m3_inverse(sc);
+        uint32_t w[4];
+        e4m3_codes<16>(w, [&](int i) { return (float)v[i]; }, [&](int i) { return v[i]; }, [&](int) { return inv; });
         wave_lds_sync();
 #pragma unroll
         for (int q = 0; q < 16; ++q) bbuf[at + 8 * q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
@@ -166,18 +196,14 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          double x[8];
           double am = 0.0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[j] = v[8 * h + j];
-            am = absmax2(am, x[j]);
-          }
-          am = set_max(am);
-          const float sc = e4m3_scale(am);
+          for (int j = 0; j < 8; ++j) am = absmax2(am, v[8 * h + j]);
+          const float sc = e4m3_scale(set_max(am));
+          const E4m3Inverse inv = e4m3_inverse(sc);
           uint32_t w2[2];
-          const double inv = sc > 0.f ? 1.0 / (double)sc : 0.0;
-          e4m3_codes<8>(w2, [&](int i) { return x[i]; }, [&](int) { return sc; }, [&](int) { return inv; });
+          e4m3_codes<8>(w2, [&](int i) { return (float)v[8 * h + i]; }, [&](int i) { return v[8 * h + i]; },
+                        [&](int) { return inv; });
           if (live) {
             *reinterpret_cast<uint2*>(yrow + 128 * h + 8 * pl.l16) = uint2{w2[0], w2[1]};
             if (pl.l16 == 0) a.scales[(2 * pl.grp + h) * a.ldscales + row] = sc;
@@ -185,28 +211,39 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
         }
       }
     } else {
-      const double amax = row_join<true>(absmax16(v), pl, a.groups, red + 2 * sets);
-      const float s32 = (float)(amax / 127.0);
-      const double s64 = (double)s32, inv = s32 > 0.f ? 1.0 / s64 : 0.0;
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      double am[1] = {absmax16(v)};
+      row_join<1, true>(am, pl, a.groups, red + 2 * sets);
+      const float s32 = (float)(am[0] / 127.0);
+      const double s64 = (double)s32, inv64 = s32 > 0.f ? 1.0 / s64 : 0.0;
+      constexpr double MAGIC = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer (RNE)
+      // The product with 1 / s decides the code unless it is within 1e-9 of a tie;
+      // rows with a subnormal scale take the division.
+      const bool direct = s32 == 0.f || s32 >= 0x1p-126f;
+      wave_lds_sync();
+      bool tie = false;
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        w[q >> 2] |= ((uint32_t)quant_code(v[q], s64, inv, 127.0) & 0xffu) << (8 * (q & 3));
-      if (a.rotate) {
-        const int at = 128 * (pl.l16 >> 3) + (pl.l16 & 7);
-        wave_lds_sync();
-#pragma unroll
-        for (int q = 0; q < 16; ++q) bbuf[at + 8 * q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
-        wave_lds_sync();
-        const u32x4_t w4 = *reinterpret_cast<const u32x4_t*>(bbuf + 16 * pl.l16);
-        if (live)
-          *reinterpret_cast<u32x4_t*>((uint8_t*)a.y + row * a.ldy + (int64_t)pl.grp * 256 + 16 * pl.l16) = w4;
-      } else if (live) {
-        uint8_t* yp = (uint8_t*)a.y + row * a.ldy + col;
-        *reinterpret_cast<uint2*>(yp) = uint2{w[0], w[1]};
-        *reinterpret_cast<uint2*>(yp + 128) = uint2{w[2], w[3]};
+      for (int q = 0; q < 16; ++q) {
+        const double f = fma(v[q], inv64, MAGIC);
+        const double d = fma(v[q], inv64, MAGIC - f);
+        tie |= !(fabs(d) < 0.5 - 1e-9);
+        bbuf[at + 8 * q] = (uint8_t)__builtin_bit_cast(uint64_t, f);
+        if ((q & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four codes at a time: fewer registers
       }
-      if (live && pl.grp == 0 && pl.l16 == 0) a.scales[row] = s32;
+      if (__ballot((tie || !direct) && live)) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const double f = fma(v[q], inv64, MAGIC);
+          const double d = fma(v[q], inv64, MAGIC - f);
+          if (!direct || !(fabs(d) < 0.5 - 1e-9)) bbuf[at + 8 * q] = (uint8_t)quant_code(v[q], s64, inv64, 127.0);
+          __builtin_amdgcn_sched_barrier(0);  // one division at a time
+        }
+      }
+      wave_lds_sync();
+      const u32x4_t w4 = *reinterpret_cast<const u32x4_t*>(bbuf + 16 * pl.l16);
+      if (live) {
+        *reinterpret_cast<u32x4_t*>((uint8_t*)a.y + row * a.ldy + (int64_t)pl.grp * 256 + 16 * pl.l16) = w4;
+        if (pl.grp == 0 && pl.l16 == 0) a.scales[row] = s32;
+      }
     }
   }
 }
@@ -216,11 +253,24 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
 //   n = (t - mu) r;  w = gamma g
 //   dt = r (w - mean(w) - n mean(w n)) + dsum;   dbranch = drop(dt)
 //   dgamma = sum over rows of g n;               dbeta = sum over rows of g
-// fp32, the row's sums, the deviations and n's product in fp64. A thread keeps
-// its 16 columns of dgamma and dbeta over the rows of its block; the blocks'
-// sums are joined by k_colsum in a fixed order.
-template <typename TG, typename TT, typename TD, int NT>
-__global__ __launch_bounds__(NT, 1) void k_layernorm_bwd(LayerNormBwdArgs a, int rows_per_block) {
+// fp32, the row's sums, the deviations and n's product in fp64.
+//
+// SUMS: a thread keeps its 16 columns of dgamma and dbeta over the rows of its
+// block; the blocks' sums are joined by k_colsum in a fixed order. Wide rows
+// (more than 16 groups) have no registers for that, and as many blocks as rows:
+// their kernel leaves mu and r of each row, and k_layernorm_dw takes the sums.
+template <typename T>
+__device__ __forceinline__ void rotate_back(float (&g)[16], const Runs<T>& raw, float* buf, int l16) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) g[i] = raw.get(i) * 0.0625f;
+  fwht16_regs(g);
+  transpose16(g, buf, l16);
+  fwht16_regs(g);
+  transpose16_back(g, buf, l16);
+}
+
+template <typename TG, typename TT, typename TD, int NT, bool SUMS>
+__global__ __launch_bounds__(NT, SUMS ? 3 : 4) void k_layernorm_bwd(LayerNormBwdArgs a, int rows_per_block) {
   constexpr int SET_BYTES = 16 * (16 + 4) * 4;
   extern __shared__ __align__(16) uint8_t lds[];
   const Place pl = place_of(a.groups, rows_per_block);
@@ -230,8 +280,6 @@ __global__ __launch_bounds__(NT, 1) void k_layernorm_bwd(LayerNormBwdArgs a, int
   const int64_t col = (int64_t)pl.grp * 256 + pl.l16 * 8;
   const int64_t k = (int64_t)a.groups * 256;
   const double inv_k = 1.0 / (double)k;
-  PhiloxKey key{};
-  if (a.drop.rng != nullptr) key = philox_key(a.drop.rng);
 
   float gm[16], dg[16], db[16];
   if (pl.active) {
@@ -251,66 +299,75 @@ __global__ __launch_bounds__(NT, 1) void k_layernorm_bwd(LayerNormBwdArgs a, int
     Runs<TD> rd;
     rd.zero();
     if (live) {
-      rg.load((const TG*)a.dy + row * a.lddy + col);
       rt.load((const TT*)a.t + row * a.ldt + col);
+      rg.load((const TG*)a.dy + row * a.lddy + col);
       if (a.dsum != nullptr) rd.load((const TD*)a.dsum + row * a.ldds + col);
     } else {
       rg.zero();
       rt.zero();
     }
-    double c0 = 0.0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) c0 += (double)rt.get(i);
-    float g[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) g[i] = rg.get(i);
-    if (a.rotate) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) g[i] *= 0.0625f;
-      fwht16_regs(g);
-      transpose16(g, tbuf, pl.l16);
-      fwht16_regs(g);
-      transpose16_back(g, tbuf, pl.l16);
-    }
-    const double mu = row_join<false>(c0, pl, a.groups, red) * inv_k;
-    double c1 = 0.0, c2 = 0.0, c3 = 0.0;
+    double c[3] = {0.0, 0.0, 0.0}, mean[1] = {0.0};
+    float t[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const double d = (double)rt.get(i) - mu, w = (double)(g[i] * gm[i]);
-      c1 += w;
-      c2 = fma(w, d, c2);
-      c3 = fma(d, d, c3);
+      t[i] = rt.get(i);
+      mean[0] += (double)t[i];
     }
-    if (!pl.active) c3 = 0.0;
-    c1 = row_join<false>(c1, pl, a.groups, red + sets);
-    c2 = row_join<false>(c2, pl, a.groups, red + 2 * sets);
-    c3 = row_join<false>(c3, pl, a.groups, red + 3 * sets);
-    const double r64 = 1.0 / sqrt(c3 * inv_k + a.eps);
-    const float r = (float)r64, m1 = (float)(c1 * inv_k), m2 = (float)(r64 * (c2 * inv_k));
+    row_join<1, false>(mean, pl, a.groups, red);
+    const double mu = mean[0] * inv_k;
+    float g[16];
+    if (a.rotate) {
+      rotate_back(g, rg, tbuf, pl.l16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) g[i] = rg.get(i);
+    }
+    afresh(t);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const double d = (double)t[i] - mu, w = (double)(g[i] * gm[i]);
+      c[0] += w;
+      c[1] = fma(w, d, c[1]);
+      c[2] = fma(d, d, c[2]);
+      if ((i & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four at a time: fewer registers
+    }
+    if (!pl.active) c[2] = 0.0;
+    row_join<3, false>(c, pl, a.groups, red + sets);
+    const double r64 = 1.0 / sqrt(c[2] * inv_k + a.eps);
+    const float r = (float)r64, m1 = (float)(c[0] * inv_k), m2 = (float)(r64 * (c[1] * inv_k));
+    afresh(t);
     float o[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float n = (float)(((double)rt.get(i) - mu) * r64);
+      const float n = (float)(((double)t[i] - mu) * r64);
       o[i] = fmaf(r, fmaf(-n, m2, g[i] * gm[i] - m1), rd.get(i));
-      if (live) {
-        dg[i] = fmaf(g[i], n, dg[i]);
-        db[i] += g[i];
+      if constexpr (SUMS) {
+        if (live) {
+          dg[i] = fmaf(g[i], n, dg[i]);
+          db[i] += g[i];
+        }
       }
+      if ((i & 3) == 3) __builtin_amdgcn_sched_barrier(0);
     }
     if (live) {
+      if (!SUMS && a.stats != nullptr && pl.grp == 0 && pl.l16 == 0)
+        reinterpret_cast<double2*>(a.stats)[row] = double2{mu, r64};
       store16((TD*)a.dx + row * a.lddx + col, o);
       if (a.dbranch != nullptr) {
+        if (a.drop.rng != nullptr) {
+          const PhiloxKey key = philox_key(a.drop.rng);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4_t w = philox4x32_10(key, (uint64_t)(row * k + col + 128 * h) >> 3);
+          for (int h = 0; h < 2; ++h) {
+            const u32x4_t w = philox4x32_10(key, (uint64_t)(row * k + col + 128 * h) >> 3);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[8 * h + j] = philox_drop(w, j, a.drop, o[8 * h + j]);
+            for (int j = 0; j < 8; ++j) o[8 * h + j] = philox_drop(w, j, a.drop, o[8 * h + j]);
+          }
         }
         store16((TD*)a.dbranch + row * a.lddb + col, o);
       }
     }
   }
-  if (a.dgamma == nullptr && a.dbeta == nullptr) return;
+  if (!SUMS || (a.dgamma == nullptr && a.dbeta == nullptr)) return;
   float* part = a.part + (int64_t)blockIdx.x * (2 * k);
   if (pl.rows == 1) {
     if (pl.active) {
@@ -334,11 +391,58 @@ __global__ __launch_bounds__(NT, 1) void k_layernorm_bwd(LayerNormBwdArgs a, int
   }
 }
 
+// dgamma and dbeta of wide rows: a block takes 256 columns of a share of the
+// rows, its 16 sets a row each in turn; the sets' sums are added in order.
+template <typename TG, typename TT>
+__global__ __launch_bounds__(256) void k_layernorm_dw(LayerNormBwdArgs a, int shares) {
+  constexpr int SET_BYTES = 16 * (16 + 4) * 4;
+  __shared__ __align__(16) uint8_t lds[16 * SET_BYTES];
+  const int l16 = threadIdx.x & 15, set = threadIdx.x >> 4;
+  const int share = blockIdx.x / a.groups, grp = blockIdx.x - share * a.groups;
+  const int64_t col = (int64_t)grp * 256 + l16 * 8, k = (int64_t)a.groups * 256;
+  const int64_t r0 = a.m * share / shares, r1 = a.m * (share + 1) / shares;
+  float dg[16], db[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) dg[i] = db[i] = 0.f;
+  for (int64_t row = r0 + set; row < r1; row += 16) {
+    Runs<TG> rg;
+    Runs<TT> rt;
+    rg.load((const TG*)a.dy + row * a.lddy + col);
+    rt.load((const TT*)a.t + row * a.ldt + col);
+    const double2 st = reinterpret_cast<const double2*>(a.stats)[row];
+    float g[16];
+    if (a.rotate) {
+      rotate_back(g, rg, reinterpret_cast<float*>(lds + set * SET_BYTES), l16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) g[i] = rg.get(i);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      dg[i] = fmaf(g[i], (float)(((double)rt.get(i) - st.x) * st.y), dg[i]);
+      db[i] += g[i];
+    }
+  }
+  float* sums = reinterpret_cast<float*>(lds);  // [16][256]
+  float* part = a.part + (int64_t)share * (2 * k) + (int64_t)grp * 256;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
+    store16(sums + set * 256 + 8 * l16, which ? db : dg);
+    __syncthreads();
+    float s = sums[threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += sums[w * 256 + threadIdx.x];
+    part[which * k + threadIdx.x] = s;
+  }
+}
+
 // ---------------------------------------------------------------- launchers
 namespace {
 
 constexpr int64_t LN_BLOCKS = 65536;    // blocks walk rows beyond that many (threads of a grid in 32 bits)
 constexpr int64_t LN_BWD_BLOCKS = 512;  // partial rows of dgamma and dbeta
+constexpr int LN_WIDE_GROUPS = 16;      // rows of more groups leave their sums to k_layernorm_dw
 
 template <typename TX, typename TS, bool RES, int OUT>
 hipError_t ln_launch(const LayerNormArgs& a, hipStream_t stream) {
@@ -367,8 +471,9 @@ hipError_t ln_x(const LayerNormArgs& a, hipStream_t stream) {
 }
 
 Shape ln_bwd_shape(int64_t m, int groups) {
+  if (groups > LN_WIDE_GROUPS) return shape_of(m, groups, LN_BLOCKS);
   Shape s;
-  int64_t rows = groups <= 16 ? 16 / groups : 1;
+  int64_t rows = 16 / groups;
   while (rows > 1 && (m + rows - 1) / rows < 256) rows = (rows + 1) / 2;
   s.rows = (int)rows;
   s.threads = (s.rows * groups * 16 + 63) / 64 * 64;
@@ -377,21 +482,36 @@ Shape ln_bwd_shape(int64_t m, int groups) {
   return s;
 }
 
+// Shares of the rows of k_layernorm_dw: two blocks a compute unit.
+int dw_shares(int64_t m, int groups) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>((512 + groups - 1) / groups, (m + 15) / 16));
+}
+
 template <typename TG, typename TT, typename TD>
 hipError_t ln_bwd_launch(const LayerNormBwdArgs& a, hipStream_t stream) {
   const Shape s = ln_bwd_shape(a.m, a.groups);
   const size_t lds = (size_t)(s.threads / 16) * (16 * 20 * 4 + 4 * sizeof(double));
   const dim3 grid((unsigned)s.blocks), block((unsigned)s.threads);
-  if (s.threads <= 256)
-    hipLaunchKernelGGL((k_layernorm_bwd<TG, TT, TD, 256>), grid, block, lds, stream, a, s.rows);
-  else
-    hipLaunchKernelGGL((k_layernorm_bwd<TG, TT, TD, 1024>), grid, block, lds, stream, a, s.rows);
+  if (a.groups <= LN_WIDE_GROUPS) {
+    hipLaunchKernelGGL((k_layernorm_bwd<TG, TT, TD, 256, true>), grid, block, lds, stream, a, s.rows);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((k_layernorm_bwd<TG, TT, TD, 1024, false>), grid, block, lds, stream, a, s.rows);
   return hipGetLastError();
 }
 
 template <typename TG, typename TT>
 hipError_t ln_bwd_dx(const LayerNormBwdArgs& a, hipStream_t stream) {
-  return a.dx_bf16 ? ln_bwd_launch<TG, TT, uint16_t>(a, stream) : ln_bwd_launch<TG, TT, float>(a, stream);
+  const hipError_t e =
+      a.dx_bf16 ? ln_bwd_launch<TG, TT, uint16_t>(a, stream) : ln_bwd_launch<TG, TT, float>(a, stream);
+  if (e != hipSuccess || a.stats == nullptr) return e;
+  const int shares = dw_shares(a.m, a.groups);
+  hipLaunchKernelGGL((k_layernorm_dw<TG, TT>), dim3((unsigned)(shares * a.groups)), dim3(256), 0, stream, a, shares);
+  return hipGetLastError();
+}
+
+int64_t partial_rows(int64_t m, int groups) {
+  return groups > LN_WIDE_GROUPS ? dw_shares(m, groups) : ln_bwd_shape(m, groups).blocks;
 }
 
 }  // namespace
@@ -400,9 +520,18 @@ hipError_t launch_layernorm(const LayerNormArgs& a, hipStream_t stream) {
   return a.x_bf16 ? ln_x<uint16_t>(a, stream) : ln_x<float>(a, stream);
 }
 
-int64_t layernorm_bwd_partial_rows(int64_t m, int groups) { return ln_bwd_shape(m, groups).blocks; }
+// Partial rows of dgamma and dbeta, then mu and r of each wide row.
+int64_t layernorm_bwd_workspace_bytes(int64_t m, int groups) {
+  const int64_t part = partial_rows(m, groups) * 2 * groups * 256 * 4;
+  return part + (groups > LN_WIDE_GROUPS ? m * 16 : 0);
+}
 
-hipError_t launch_layernorm_bwd(const LayerNormBwdArgs& a, hipStream_t stream) {
+hipError_t launch_layernorm_bwd(const LayerNormBwdArgs& args, hipStream_t stream) {
+  LayerNormBwdArgs a = args;
+  const int64_t k = (int64_t)a.groups * 256;
+  const bool sums = a.dgamma != nullptr || a.dbeta != nullptr;
+  const int64_t rows = a.m > 0 ? partial_rows(a.m, a.groups) : 0;  // m == 0: none, so the sums are zero
+  a.stats = sums && a.groups > LN_WIDE_GROUPS ? (double*)(a.part + rows * 2 * k) : nullptr;
   if (a.m > 0) {
     hipError_t e;
     if (a.dy_bf16)
@@ -411,11 +540,7 @@ hipError_t launch_layernorm_bwd(const LayerNormBwdArgs& a, hipStream_t stream) {
       e = a.t_bf16 ? ln_bwd_dx<float, uint16_t>(a, stream) : ln_bwd_dx<float, float>(a, stream);
     if (e != hipSuccess) return e;
   }
-  if (a.dgamma == nullptr && a.dbeta == nullptr) return hipSuccess;
-  // m == 0: no partial rows, so the sums are zero
-  const int64_t k = (int64_t)a.groups * 256;
-  return launch_colsum(a.part, a.m > 0 ? layernorm_bwd_partial_rows(a.m, a.groups) : 0, 2 * k, a.dgamma, k, a.dbeta,
-                       stream);
+  return sums ? launch_colsum(a.part, rows, 2 * k, a.dgamma, k, a.dbeta, stream) : hipSuccess;
 }
 
 }  // namespace tp
