@@ -9,8 +9,12 @@ namespace tp {
 
 constexpr double E4M3_MAX = 448.0;
 
-// The scale of a block: fp32(amax / 448), 0 for a block of zeros.
+// The scale of a block: fp32(amax / 448), 0 for a block of zeros. For an fp32
+// amax the fp64 product with 1 / 448 rounds to the same: amax / 448 = amax / 7 /
+// 64 is no nearer than 2^-28 of itself to the middle of two fp32 numbers, unless
+// it is an fp32 number.
 __device__ __forceinline__ float e4m3_scale(double amax) { return (float)(amax / E4M3_MAX); }
+__device__ __forceinline__ float e4m3_scale(float amax) { return (float)((double)amax * (1.0 / E4M3_MAX)); }
 
 // The code of q. With e the exponent of |q| (at least -6, where the subnormal
 // codes begin), |q| 2^(3 - e) is below 16 and its nearest integer n is the
@@ -29,45 +33,43 @@ __device__ __forceinline__ uint32_t e4m3_code(double q) {
 }
 
 // What the quick way of codes needs of a scale: 1 / s from below and from above.
-// s below fp32's normal range has no such bounds (quick false: every code is
-// decided by the division).
+// s below fp32's normal range has no such bounds (slow: every code is decided by
+// the division).
 struct E4m3Inverse {
   float s, lo, hi;
-  bool quick;
+  __device__ __forceinline__ bool slow() const { return s > 0.f && s < 0x1p-126f; }
 };
 
 __device__ __forceinline__ E4m3Inverse e4m3_inverse(float s) {
-  const bool quick = s >= 0x1p-126f;
-  const float inv = quick ? 1.f / s : 0.f;
-  return E4m3Inverse{s, inv * (1.f - 0x1p-21f), inv * (1.f + 0x1p-21f), quick};
+  const float inv = s >= 0x1p-126f ? __builtin_amdgcn_rcpf(s) : 0.f;
+  return E4m3Inverse{s, inv * (1.f - 0x1p-21f), inv * (1.f + 0x1p-21f)};
 }
 
 // The codes of N values, four to a dword: x(i) in fp32, exact(i) the value itself
-// in fp64 (x(i) is it, or it rounded), of(i) its scale. Rounding is monotone: the
-// products with 1 / s from below and from above enclose x / s (the roundings of
-// x, 1 / s, the factor and the product are below 2^-22 together), so where both
-// round to one code it is that of x / s. Where they do not (one value in 10^5,
-// one wave in a hundred) the fp64 division decides.
+// in fp64 (x(i) is it, or it rounded), of(i) its scale, slow whether any of those
+// is. Rounding is monotone: the products with 1 / s from below and from above
+// enclose x / s (the roundings of x, of the factor and of the product, 2^-24 each,
+// and 1 / s, 2^-23, stay below 2^-21 together), so where both round to one code it
+// is that of x / s. Where they do not (one value in 10^5, one wave in a hundred)
+// the fp64 division decides.
 template <int N, typename X, typename D, typename S>
-__device__ __forceinline__ void e4m3_codes(uint32_t (&w)[N / 4], X x, D exact, S of) {
+__device__ __forceinline__ void e4m3_codes(uint32_t (&w)[N / 4], X x, D exact, S of, bool slow) {
   uint32_t up[N / 4];
-  bool open = false;
+  bool open = slow;
 #pragma unroll
   for (int q = 0; q < N / 4; ++q) {
     int lo = 0, hi = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 4 * q + 2 * h;
-      const E4m3Inverse a = of(i), b = of(i + 1);
-      const float u = x(i), v = x(i + 1);
-      if (h == 0) {
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.lo, v * b.lo, lo, false);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.hi, v * b.hi, hi, false);
-      } else {
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.lo, v * b.lo, lo, true);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.hi, v * b.hi, hi, true);
-      }
-      open |= (!a.quick && a.s > 0.f) || (!b.quick && b.s > 0.f);
+    {
+      const E4m3Inverse a = of(4 * q), b = of(4 * q + 1);
+      const float u = x(4 * q), v = x(4 * q + 1);
+      lo = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.lo, v * b.lo, lo, false);
+      hi = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.hi, v * b.hi, hi, false);
+    }
+    {
+      const E4m3Inverse a = of(4 * q + 2), b = of(4 * q + 3);
+      const float u = x(4 * q + 2), v = x(4 * q + 3);
+      lo = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.lo, v * b.lo, lo, true);
+      hi = __builtin_amdgcn_cvt_pk_fp8_f32(u * a.hi, v * b.hi, hi, true);
     }
     w[q] = (uint32_t)lo;
     up[q] = (uint32_t)hi;
@@ -78,7 +80,7 @@ __device__ __forceinline__ void e4m3_codes(uint32_t (&w)[N / 4], X x, D exact, S
     for (int i = 0; i < N; ++i) {
       const E4m3Inverse a = of(i);
       const uint32_t mask = 0xffu << (8 * (i & 3));
-      if (((w[i >> 2] ^ up[i >> 2]) & mask) != 0 || (!a.quick && a.s > 0.f))
+      if (((w[i >> 2] ^ up[i >> 2]) & mask) != 0 || a.slow())
         w[i >> 2] = (w[i >> 2] & ~mask) | (e4m3_code(exact(i) / (double)a.s) << (8 * (i & 3)));
       __builtin_amdgcn_sched_barrier(0);  // one division at a time
     }

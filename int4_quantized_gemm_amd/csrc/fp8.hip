@@ -10,6 +10,7 @@
 // from stays in registers until its codes are made.
 #include "block_ops.hpp"
 #include "e4m3.hpp"
+#include "lanes.hpp"
 #include "row_sets.hpp"
 
 namespace tp {
@@ -37,19 +38,33 @@ __device__ __forceinline__ float max8(const float (&v)[8]) {
   return m;
 }
 
-__device__ __forceinline__ float set_max(float v) {
-  v = fmaxf(v, swz_xor<1>(v));
-  v = fmaxf(v, swz_xor<2>(v));
-  v = fmaxf(v, swz_xor<4>(v));
-  v = fmaxf(v, swz_xor<8>(v));
-  return v;
-}
+// What the codes need of a column's scale, made once for a tile.
+struct Inverses {
+  float s[256], lo[256], hi[256];
+  __device__ __forceinline__ void put(int c, const E4m3Inverse& v) {
+    s[c] = v.s;
+    lo[c] = v.lo;
+    hi[c] = v.hi;
+  }
+  __device__ __forceinline__ E4m3Inverse get(int c) const { return E4m3Inverse{s[c], lo[c], hi[c]}; }
+};
 
 // The codes of eight values of one block.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const E4m3Inverse& s) {
   uint32_t w[2];
-  e4m3_codes<8>(w, [&](int i) { return v[i]; }, [&](int i) { return (double)v[i]; }, [&](int) { return s; });
+  e4m3_codes<8>(w, [&](int i) { return v[i]; }, [&](int i) { return (double)v[i]; }, [&](int) { return s; },
+                s.slow());
   return uint2{w[0], w[1]};
+}
+
+// Four rows of four codes each as four columns.
+__device__ __forceinline__ void turn4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&t)[4]) {
+  const uint32_t p = __builtin_amdgcn_perm(b, a, 0x05010400u), q = __builtin_amdgcn_perm(d, c, 0x05010400u);
+  const uint32_t r = __builtin_amdgcn_perm(b, a, 0x07030602u), s = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  t[0] = __builtin_amdgcn_perm(q, p, 0x05040100u);
+  t[1] = __builtin_amdgcn_perm(q, p, 0x07060302u);
+  t[2] = __builtin_amdgcn_perm(s, r, 0x05040100u);
+  t[3] = __builtin_amdgcn_perm(s, r, 0x07060302u);
 }
 
 constexpr int Q_ROWS = 128;  // rows of a tile whose columns or blocks are quantized
@@ -66,7 +81,7 @@ __global__ __launch_bounds__(256) void k_fp8_rows(QuantFp8Args a, uint32_t block
   if (row >= a.m) return;
   float v[8];
   load_left((const TX*)a.x + row * a.ldx + col, a.k - col, v);
-  const float s = set_max(max8(v)) / (float)E4M3_MAX;
+  const float s = e4m3_scale(row_all<true>(max8(v)));
   *reinterpret_cast<uint2*>(a.q + row * a.ldq + col) = codes8(v, e4m3_inverse(s));
   if (l16 == 0) a.s[g * a.lds + row] = s;
 }
@@ -77,7 +92,7 @@ __global__ __launch_bounds__(256) void k_fp8_rows(QuantFp8Args a, uint32_t block
 template <typename TX>
 __global__ __launch_bounds__(512) void k_fp8_tile(QuantFp8Args a, uint32_t blocks_k) {
   __shared__ float part[8][128];
-  __shared__ float scale[128];
+  __shared__ Inverses inverses;
   __shared__ uint32_t cols[128 * Q_PITCH];
   const int l16 = threadIdx.x & 15, set = threadIdx.x >> 4, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const uint32_t tile = blockIdx.x / blocks_k, g = blockIdx.x - tile * blocks_k;
@@ -95,7 +110,7 @@ __global__ __launch_bounds__(512) void k_fp8_tile(QuantFp8Args a, uint32_t block
   if (!a.blocks && a.q != nullptr) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float s = set_max(max8(v[r])) / (float)E4M3_MAX;
+      const float s = e4m3_scale(row_all<true>(max8(v[r])));
       const uint2 w = codes8(v[r], e4m3_inverse(s));
       if (row + r < a.m) {
         *reinterpret_cast<uint2*>(a.q + (row + r) * a.ldq + col) = w;
@@ -109,11 +124,10 @@ __global__ __launch_bounds__(512) void k_fp8_tile(QuantFp8Args a, uint32_t block
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     m[j] = fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])), fmaxf(fabsf(v[2][j]), fabsf(v[3][j])));
-    m[j] = fmaxf(m[j], swz_xor<16>(m[j]));
-    m[j] = fmaxf(m[j], __shfl_xor(m[j], 32));
+    m[j] = rows_all<true>(m[j]);
   }
   if (a.blocks) {
-    const float one = set_max(max8(m));
+    const float one = row_all<true>(max8(m));
 #pragma unroll
     for (int j = 0; j < 8; ++j) m[j] = one;
   }
@@ -126,8 +140,8 @@ __global__ __launch_bounds__(512) void k_fp8_tile(QuantFp8Args a, uint32_t block
     float t = part[0][threadIdx.x];
 #pragma unroll
     for (int w = 1; w < 8; ++w) t = fmaxf(t, part[w][threadIdx.x]);
-    const float s = t / (float)E4M3_MAX;
-    scale[threadIdx.x] = s;
+    const float s = e4m3_scale(t);
+    inverses.put(threadIdx.x, e4m3_inverse(s));
     if (a.blocks) {
       if (threadIdx.x == 0) {
         if (a.q != nullptr) a.s[tile * a.lds + g] = s;
@@ -139,30 +153,28 @@ __global__ __launch_bounds__(512) void k_fp8_tile(QuantFp8Args a, uint32_t block
   }
   __syncthreads();
   E4m3Inverse inv[8];
-  if (a.blocks) {
-    inv[0] = e4m3_inverse(scale[0]);
+  bool slow = false;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) inv[j] = inv[0];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) inv[j] = e4m3_inverse(scale[8 * l16 + j]);
+  for (int j = 0; j < 8; ++j) {
+    inv[j] = inverses.get(8 * l16 + j);
+    slow |= inv[j].slow();
   }
-  uint32_t pack[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) pack[j] = 0u;
+  uint32_t w[4][2];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    uint32_t w[2];
-    e4m3_codes<8>(w, [&](int i) { return v[r][i]; }, [&](int i) { return (double)v[r][i]; },
-                  [&](int i) { return inv[i]; });
+    e4m3_codes<8>(w[r], [&](int i) { return v[r][i]; }, [&](int i) { return (double)v[r][i]; },
+                  [&](int i) { return inv[i]; }, slow);
     if (a.blocks && a.q != nullptr && row + r < a.m)
-      *reinterpret_cast<uint2*>(a.q + (row + r) * a.ldq + col) = uint2{w[0], w[1]};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) pack[j] |= ((w[j >> 2] >> (8 * (j & 3))) & 0xffu) << (8 * r);
+      *reinterpret_cast<uint2*>(a.q + (row + r) * a.ldq + col) = uint2{w[r][0], w[r][1]};
   }
   if (a.qt == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cols[(8 * l16 + j) * Q_PITCH + set] = pack[j];
+  for (int h = 0; h < 2; ++h) {
+    uint32_t t[4];
+    turn4(w[0][h], w[1][h], w[2][h], w[3][h], t);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cols[(8 * l16 + 4 * h + j) * Q_PITCH + set] = t[j];
+  }
   __syncthreads();
   // eight lanes a column, 16 codes each
   for (int c = threadIdx.x >> 3; c < 128; c += 64) {
@@ -228,7 +240,8 @@ __global__ __launch_bounds__(256) void k_fp8_rows_rotated(QuantFp8Args a, uint32
   const float s = e4m3_scale(half_set_max(absmax16(v)));
   const E4m3Inverse inv = e4m3_inverse(s);
   uint32_t w[4];
-  e4m3_codes<16>(w, [&](int i) { return (float)v[i]; }, [&](int i) { return v[i]; }, [&](int) { return inv; });
+  e4m3_codes<16>(w, [&](int i) { return (float)v[i]; }, [&](int i) { return v[i]; }, [&](int) { return inv; },
+                 inv.slow());
   const u32x4_t w4 = straight(w, buf, l16);
   if (row < a.m) {
     *reinterpret_cast<u32x4_t*>(a.q + row * a.ldq + c0 + 16 * l16) = w4;
@@ -241,7 +254,7 @@ __global__ __launch_bounds__(256) void k_fp8_rows_rotated(QuantFp8Args a, uint32
 template <typename TX>
 __global__ __launch_bounds__(512, 2) void k_fp8_tile_rotated(QuantFp8Args a, uint32_t groups) {
   __shared__ __align__(16) uint8_t turn[32 * Q_SET_BYTES];
-  __shared__ float scale[256];
+  __shared__ Inverses inverses;
   double(*part)[256] = reinterpret_cast<double(*)[256]>(turn);      // [8][256], after the transforms
   uint32_t* cols = reinterpret_cast<uint32_t*>(turn + 8 * 256 * 8);  // [256][Q_PITCH]
   static_assert(32 * Q_SET_BYTES >= 8 * 256 * 8 + 256 * Q_PITCH * 4, "the tile turns in the transforms' LDS");
@@ -266,7 +279,8 @@ __global__ __launch_bounds__(512, 2) void k_fp8_tile_rotated(QuantFp8Args a, uin
       const float s = e4m3_scale(half_set_max(absmax16(v[r])));
       const E4m3Inverse inv = e4m3_inverse(s);
       uint32_t w[4];
-      e4m3_codes<16>(w, [&](int i) { return (float)v[r][i]; }, [&](int i) { return v[r][i]; }, [&](int) { return inv; });
+      e4m3_codes<16>(w, [&](int i) { return (float)v[r][i]; }, [&](int i) { return v[r][i]; }, [&](int) { return inv; },
+                     inv.slow());
       const u32x4_t w4 = straight(w, buf, l16);
       if (row + r < a.m) {
         *reinterpret_cast<u32x4_t*>(a.q + (row + r) * a.ldq + c0 + 16 * l16) = w4;
@@ -285,8 +299,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_tile_rotated(QuantFp8Args a, uin
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    m[i] = fmax(m[i], swz_xor<16>(m[i]));
-    m[i] = fmax(m[i], __shfl_xor(m[i], 32));
+    m[i] = rows_all<true>(m[i]);
     if (lane < 16) part[wave][turned_col(l16, i)] = m[i];
   }
   __syncthreads();
@@ -295,7 +308,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_tile_rotated(QuantFp8Args a, uin
 #pragma unroll
     for (int w = 1; w < 8; ++w) t = fmax(t, part[w][threadIdx.x]);
     const float s = e4m3_scale(t);
-    scale[threadIdx.x] = s;
+    inverses.put(threadIdx.x, e4m3_inverse(s));
     if (a.blocks) {
       if ((threadIdx.x & 127) == 0) {
         const int64_t b = 2 * (int64_t)g + (threadIdx.x >> 7);
@@ -307,19 +320,21 @@ __global__ __launch_bounds__(512, 2) void k_fp8_tile_rotated(QuantFp8Args a, uin
     }
   }
   __syncthreads();
-  uint32_t pack[16];
+  bool slow = false;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) pack[i] = 0u;
+  for (int i = 0; i < 16; ++i) slow |= inverses.get(turned_col(l16, i)).slow();
+  uint32_t w[4][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    uint32_t w[4];
-    e4m3_codes<16>(w, [&](int i) { return (float)v[r][i]; }, [&](int i) { return v[r][i]; },
-                   [&](int i) { return e4m3_inverse(scale[turned_col(l16, i)]); });
+  for (int r = 0; r < 4; ++r)
+    e4m3_codes<16>(w[r], [&](int i) { return (float)v[r][i]; }, [&](int i) { return v[r][i]; },
+                   [&](int i) { return inverses.get(turned_col(l16, i)); }, slow);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) pack[i] |= ((w[i >> 2] >> (8 * (i & 3))) & 0xffu) << (8 * r);
+  for (int h = 0; h < 4; ++h) {
+    uint32_t t[4];
+    turn4(w[0][h], w[1][h], w[2][h], w[3][h], t);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cols[turned_col(l16, 4 * h + j) * Q_PITCH + set] = t[j];
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) cols[turned_col(l16, i) * Q_PITCH + set] = pack[i];
   __syncthreads();
   if (a.blocks && a.q != nullptr) {  // byte r of a column's dword is row 4 set + r
 #pragma unroll

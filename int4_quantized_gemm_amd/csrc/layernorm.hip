@@ -13,6 +13,7 @@
 
 #include "block_ops.hpp"
 #include "e4m3.hpp"
+#include "lanes.hpp"
 #include "philox.hpp"
 #include "row_sets.hpp"
 
@@ -21,38 +22,66 @@ namespace tp {
 enum { LN_OUT_I8 = 0, LN_OUT_BF16 = 1, LN_OUT_FP8 = 2 };
 
 // Sums (or maxima) of N values over the threads of a row: all threads of the block
-// call it, with red [N][sets] of its own for each join of a row.
-template <int N, bool MAX>
+// call it, with red [N][JOIN] of its own for each join of a row. Where a block
+// has one wide row its waves' results are met all at once (red holds zeros past
+// the last wave); short rows have at most three sets.
+constexpr int JOIN = 16;  // results of a join: the most waves, and the most sets of short rows
+
+template <int N, bool MAX, int WAVES>
 __device__ __forceinline__ void row_join(double (&v)[N], const Place& pl, int groups, double* red) {
-  const int sets = blockDim.x >> 4;
-  int first = pl.slot * groups, count = pl.active ? groups : 0;
+  __builtin_amdgcn_sched_barrier(0);  // nothing of the next phase before this one: registers
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = MAX ? set_max(v[i]) : set_sum(v[i]);
-  if (pl.wide) {  // sets past the row hold zeros
+  for (int i = 0; i < N; ++i) v[i] = row_all<MAX>(v[i]);
+  if (WAVES > 4 || pl.wide) {  // sets past the row hold zeros
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const double o = swz_xor<16>(v[i]);
-      v[i] = MAX ? fmax(v[i], o) : v[i] + o;
-      const double p = __shfl_xor(v[i], 32);
-      v[i] = MAX ? fmax(v[i], p) : v[i] + p;
-      if ((threadIdx.x & 63) == 0) red[i * sets + (threadIdx.x >> 6)] = v[i];
+      v[i] = rows_all<MAX>(v[i]);
+      if ((threadIdx.x & 63) == 0) red[i * JOIN + (threadIdx.x >> 6)] = v[i];
     }
-    first = 0;
-    count = pl.active ? (int)(blockDim.x >> 6) : 0;
-  } else if (pl.l16 == 0) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[i * sets + pl.set] = v[i];
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.0;
+#pragma unroll
+      for (int q = 0; q < WAVES; q += 4) {  // four at a time: fewer registers
+        const double2 e = *reinterpret_cast<const double2*>(red + i * JOIN + q);
+        const double2 f = *reinterpret_cast<const double2*>(red + i * JOIN + q + 2);
+        v[i] = meet<MAX>(v[i], meet<MAX>(meet<MAX>(e.x, e.y), meet<MAX>(f.x, f.y)));
+        asm volatile("" : "+v"(v[i]));  // summed here
+      }
+    }
+  } else {  // (16 sets at most)
+    if (pl.l16 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[i * JOIN + pl.set] = v[i];
+    }
+    __syncthreads();
+    const int first = pl.slot * groups, count = pl.active ? groups : 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.0;
+      for (int w = 0; w < count; ++w) v[i] = meet<MAX>(v[i], red[i * JOIN + first + w]);
+    }
   }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.0;
-  for (int w = 0; w < count; ++w)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const double o = red[i * sets + first + w];
-      v[i] = MAX ? fmax(v[i], o) : v[i] + o;
-    }
+  __builtin_amdgcn_sched_barrier(0);
 }
+
+// The eight dwords of a lane's 16 bf16 weights; fp32 ones are fetched where they
+// are used.
+struct Weights16 {
+  u32x4_t w[2];
+  __device__ __forceinline__ void fetch(const VecArg& g, bool bf16, int64_t c, uint32_t none) {
+    w[0] = w[1] = u32x4_t{none, none, none, none};
+    if (g.p != nullptr && bf16) {
+      w[0] = *reinterpret_cast<const u32x4_t*>((const uint16_t*)g.p + c);
+      w[1] = *reinterpret_cast<const u32x4_t*>((const uint16_t*)g.p + c + 128);
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t v = w[i >> 3][(i >> 1) & 3];
+    return (i & 1) ? bf16_hi(v) : bf16_lo(v);
+  }
+};
 
 // What is read again after a join is widened again: not kept in twice the
 // registers across it.
@@ -65,185 +94,197 @@ __device__ __forceinline__ void afresh(float (&t)[N]) {
 // ------------------------------------------------------------------ forward
 // Codes: fp64 throughout, so they are those of exact arithmetic on the normed
 // row. bf16 rows: the deviations and the row factor in fp64, what follows in
-// fp32, one rounding. gamma and beta are fetched with the row, for codes behind
-// the first join, where few registers are taken.
+// fp32, one rounding (a deviation is the difference from the mean's two fp32
+// parts: as exact as t allows). bf16 weights are fetched with the row.
 template <typename TX, typename TS, bool RES, int OUT, int NT>
-__global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_per_block) {
+__global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_per_block, int64_t row0) {
   typedef typename std::conditional<OUT == LN_OUT_BF16, float, double>::type T;
   constexpr int SET_BYTES = 16 * (16 + (sizeof(T) == 4 ? 4 : 2)) * (int)sizeof(T);
   extern __shared__ __align__(16) uint8_t lds[];
   const Place pl = place_of(a.groups, rows_per_block);
   uint8_t* bbuf = lds + pl.set * SET_BYTES;
   T* tbuf = reinterpret_cast<T*>(bbuf);
-  const int sets = blockDim.x >> 4;
-  double* red = reinterpret_cast<double*>(lds + sets * SET_BYTES);  // [3][sets]
-  const int64_t col = (int64_t)pl.grp * 256 + pl.l16 * 8;
+  constexpr int WAVES = NT / 64;
+  double* red = reinterpret_cast<double*>(lds + (blockDim.x >> 4) * SET_BYTES);  // [3][JOIN]
+  const uint32_t col = pl.grp * 256 + pl.l16 * 8;
   const int64_t k = (int64_t)a.groups * 256;
   const double inv_k = 1.0 / (double)k;
-  const int64_t step = (int64_t)gridDim.x * pl.rows;
-  for (int64_t base = (int64_t)blockIdx.x * pl.rows; base < a.m; base += step) {
-    const int64_t row = base + pl.slot;
-    const bool live = pl.active && row < a.m;
-    Runs<TX> rx;
-    Runs<TS> rr;
-    if (live) {
-      rx.load((const TX*)a.x + row * a.ldx + col);
-      if constexpr (RES) rr.load((const TS*)a.res + row * a.ldr + col);
-    } else {
-      rx.zero();
-      if constexpr (RES) rr.zero();
+  const bool wb = a.gamma.p != nullptr ? a.gamma.bf16 : a.beta.bf16;
+  if (threadIdx.x < 3 * JOIN) red[threadIdx.x] = 0.0;
+  __syncthreads();
+  // (a wide row is the whole block's: its addresses take no registers of the lanes)
+  const int64_t row = row0 + (NT > 256 ? blockIdx.x : blockIdx.x * (int64_t)pl.rows + pl.slot);
+  const bool live = pl.active && row < a.m;
+  Runs<TX> rx;
+  Runs<TS> rr;
+  Weights16 gw, bw;
+  gw.fetch(a.gamma, pl.active && wb, col, 0x3f803f80u);
+  bw.fetch(a.beta, pl.active && wb, col, 0u);
+  if (live) {
+    rx.load((const TX*)a.x + row * a.ldx + col);
+    if constexpr (RES) rr.load((const TS*)a.res + row * a.ldr + col);
+  } else {
+    rx.zero();
+    if constexpr (RES) rr.zero();
+  }
+  float t[16];
+  if (RES && a.drop.rng != nullptr) {
+    const PhiloxKey key = philox_key(a.drop.rng);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4_t w = philox4x32_10(key, (uint64_t)(row * k + col + 128 * h) >> 3);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[8 * h + j] = philox_drop(w, j, a.drop, rx.get(8 * h + j));
     }
-    float t[16];
-    if (RES && a.drop.rng != nullptr) {
-      const PhiloxKey key = philox_key(a.drop.rng);
+  } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4_t w = philox4x32_10(key, (uint64_t)(row * k + col + 128 * h) >> 3);
+    for (int i = 0; i < 16; ++i) t[i] = rx.get(i);
+  }
+  if constexpr (RES) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[8 * h + j] = philox_drop(w, j, a.drop, rx.get(8 * h + j));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = rx.get(i);
-    }
-    if constexpr (RES) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = as_stream<TS>(t[i] + rr.get(i));
-      if (live) store16((TS*)a.sum + row * a.ldsum + col, t);
-    }
+    for (int i = 0; i < 16; ++i) t[i] = as_stream<TS>(t[i] + rr.get(i));
+    if (live) store16((TS*)a.sum + row * a.ldsum + col, t);
+  }
 
-    float gm[16], bt[16];
-    auto weights = [&]() {
-      if (pl.active) {
-        load_vec16(a.gamma, col, gm);
-        if (a.beta.p != nullptr) load_vec16(a.beta, col, bt);
-      }
-      if (!pl.active || a.beta.p == nullptr) {
+  double s[1] = {0.0};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) bt[i] = 0.f;
-      }
-      if (!pl.active) {
+  for (int i = 0; i < 16; ++i) s[0] += (double)t[i];
+  row_join<1, false, WAVES>(s, pl, a.groups, red);
+  const double mu = s[0] * inv_k;
+  const float mu_hi = (float)mu, mu_lo = (float)(mu - (double)mu_hi);
+  if (OUT != LN_OUT_BF16) afresh(t);
+  s[0] = 0.0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) gm[i] = 0.f;
-      }
-    };
-    if (OUT == LN_OUT_BF16) weights();
-    double s[1] = {0.0};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[0] += (double)t[i];
-    row_join<1, false>(s, pl, a.groups, red);
-    const double mu = s[0] * inv_k;
-    afresh(t);
-    if (OUT != LN_OUT_BF16) weights();
-    s[0] = 0.0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 16; ++i) {
+    if constexpr (OUT == LN_OUT_BF16) {
+      t[i] = (t[i] - mu_hi) - mu_lo;
+      s[0] = fma((double)t[i], (double)t[i], s[0]);
+    } else {
       const double d = (double)t[i] - mu;
       s[0] = fma(d, d, s[0]);
     }
-    if (!pl.active) s[0] = 0.0;
-    row_join<1, false>(s, pl, a.groups, red + sets);
-    const double r = 1.0 / sqrt(s[0] * inv_k + a.eps);
-    afresh(t);
+  }
+  if (!pl.active) s[0] = 0.0;
+  row_join<1, false, WAVES>(s, pl, a.groups, red + JOIN);
+  const double r = 1.0 / sqrt(s[0] * inv_k + a.eps);
+  if (OUT != LN_OUT_BF16) afresh(t);
 
-    T v[16];
+  T v[16];
+  auto apply = [&](int i, float gm, float bt) {
+    if constexpr (OUT == LN_OUT_BF16)
+      v[i] = fmaf(t[i] * (float)r, gm, bt);
+    else
+      v[i] = fma(((double)t[i] - mu) * r, (double)gm, (double)bt);
+  };
+  if (wb || (a.gamma.p == nullptr && a.beta.p == nullptr)) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const double n = ((double)t[i] - mu) * r;
-      if constexpr (OUT == LN_OUT_BF16)
-        v[i] = fmaf((float)n, gm[i], bt[i]);
-      else
-        v[i] = fma(n, (double)gm[i], (double)bt[i]);
-      if ((i & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four at a time: fewer registers
+      apply(i, gw.get(i), bw.get(i));
+      if (OUT != LN_OUT_BF16 && (i & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four at a time: fewer registers
     }
-    if (a.rotate) {
+  } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] *= (T)0.0625;
-      fwht16_regs(v);
-      transpose16(v, tbuf, pl.l16);
-      fwht16_regs(v);
-    } else if (OUT == LN_OUT_I8) {
-      transpose16(v, tbuf, pl.l16);  // the same output order either way
+    for (int h = 0; h < 4; ++h) {
+      f32x4_t gm = {1.f, 1.f, 1.f, 1.f}, bt = {0.f, 0.f, 0.f, 0.f};
+      const int64_t c = col + 128 * (h >> 1) + 4 * (h & 1);
+      if (pl.active && a.gamma.p != nullptr) gm = *reinterpret_cast<const f32x4_t*>((const float*)a.gamma.p + c);
+      if (pl.active && a.beta.p != nullptr) bt = *reinterpret_cast<const f32x4_t*>((const float*)a.beta.p + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) apply(4 * h + e, gm[e], bt[e]);
     }
-    // after the transpose register q is element l16 of lane q's two runs
-    const int at = 128 * (pl.l16 >> 3) + (pl.l16 & 7);
+  }
+  if (!pl.active) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0;
+  }
+  if (a.rotate) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= (T)0.0625;
+    fwht16_regs(v);
+    transpose16(v, tbuf, pl.l16);
+    fwht16_regs(v);
+  } else if (OUT == LN_OUT_I8) {
+    transpose16(v, tbuf, pl.l16);  // the same output order either way
+  }
+  // after the transpose register q is element l16 of lane q's two runs
+  const int at = 128 * (pl.l16 >> 3) + (pl.l16 & 7);
 
-    if constexpr (OUT == LN_OUT_BF16) {
-      if (a.rotate) transpose16_back(v, tbuf, pl.l16);
-      if (live) store16((uint16_t*)a.y + row * a.ldy + col, v);
-    } else if constexpr (OUT == LN_OUT_FP8) {
-      // A set holds two blocks of 128: after the transform its lanes 0 .. 7 hold
-      // the first one, without it the first run of every lane is the first one's.
-      uint8_t* yrow = (uint8_t*)a.y + row * a.ldy + (int64_t)pl.grp * 256;
-      if (a.rotate) {
-        double am = absmax16(v);
-        am = fmax(am, swz_xor<1>(am));
-        am = fmax(am, swz_xor<2>(am));
-        am = fmax(am, swz_xor<4>(am));
-        const float sc = e4m3_scale(am);
-        const E4m3Inverse inv = e4m3_inverse(sc);
-        uint32_t w[4];
-        e4m3_codes<16>(w, [&](int i) { return (float)v[i]; }, [&](int i) { return v[i]; }, [&](int) { return inv; });
-        wave_lds_sync();
+  if constexpr (OUT == LN_OUT_BF16) {
+    if (a.rotate) transpose16_back(v, tbuf, pl.l16);
+    if (live) store16((uint16_t*)a.y + row * a.ldy + col, v);
+  } else if constexpr (OUT == LN_OUT_FP8) {
+    // A set holds two blocks of 128: after the transform its lanes 0 .. 7 hold
+    // the first one, without it the first run of every lane is the first one's.
+    uint8_t* yrow = (uint8_t*)a.y + row * a.ldy + (int64_t)pl.grp * 256;
+    if (a.rotate) {
+      double am = absmax16(v);
+      am = fmax(am, swz_xor<1>(am));
+      am = fmax(am, swz_xor<2>(am));
+      am = fmax(am, swz_xor<4>(am));
+      const float sc = e4m3_scale(am);
+      const E4m3Inverse inv = e4m3_inverse(sc);
+      uint32_t w[4];
+      e4m3_codes<16>(w, [&](int i) { return (float)v[i]; }, [&](int i) { return v[i]; }, [&](int) { return inv; },
+                       inv.slow());
+      wave_lds_sync();
 #pragma unroll
-        for (int q = 0; q < 16; ++q) bbuf[at + 8 * q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
-        wave_lds_sync();
-        const u32x4_t w4 = *reinterpret_cast<const u32x4_t*>(bbuf + 16 * pl.l16);
-        if (live) {
-          *reinterpret_cast<u32x4_t*>(yrow + 16 * pl.l16) = w4;
-          if ((pl.l16 & 7) == 0) a.scales[(2 * pl.grp + (pl.l16 >> 3)) * a.ldscales + row] = sc;
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          double am = 0.0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) am = absmax2(am, v[8 * h + j]);
-          const float sc = e4m3_scale(set_max(am));
-          const E4m3Inverse inv = e4m3_inverse(sc);
-          uint32_t w2[2];
-          e4m3_codes<8>(w2, [&](int i) { return (float)v[8 * h + i]; }, [&](int i) { return v[8 * h + i]; },
-                        [&](int) { return inv; });
-          if (live) {
-            *reinterpret_cast<uint2*>(yrow + 128 * h + 8 * pl.l16) = uint2{w2[0], w2[1]};
-            if (pl.l16 == 0) a.scales[(2 * pl.grp + h) * a.ldscales + row] = sc;
-          }
-        }
+      for (int q = 0; q < 16; ++q) bbuf[at + 8 * q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
+      wave_lds_sync();
+      const u32x4_t w4 = *reinterpret_cast<const u32x4_t*>(bbuf + 16 * pl.l16);
+      if (live) {
+        *reinterpret_cast<u32x4_t*>(yrow + 16 * pl.l16) = w4;
+        if ((pl.l16 & 7) == 0) a.scales[(2 * pl.grp + (pl.l16 >> 3)) * a.ldscales + row] = sc;
       }
     } else {
-      double am[1] = {absmax16(v)};
-      row_join<1, true>(am, pl, a.groups, red + 2 * sets);
-      const float s32 = (float)(am[0] / 127.0);
-      const double s64 = (double)s32, inv64 = s32 > 0.f ? 1.0 / s64 : 0.0;
-      constexpr double MAGIC = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer (RNE)
-      // The product with 1 / s decides the code unless it is within 1e-9 of a tie;
-      // rows with a subnormal scale take the division.
-      const bool direct = s32 == 0.f || s32 >= 0x1p-126f;
-      wave_lds_sync();
-      bool tie = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        double am = 0.0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) am = absmax2(am, v[8 * h + j]);
+        const float sc = e4m3_scale(row_all<true>(am));
+        const E4m3Inverse inv = e4m3_inverse(sc);
+        uint32_t w2[2];
+        e4m3_codes<8>(w2, [&](int i) { return (float)v[8 * h + i]; }, [&](int i) { return v[8 * h + i]; },
+                      [&](int) { return inv; }, inv.slow());
+        if (live) {
+          *reinterpret_cast<uint2*>(yrow + 128 * h + 8 * pl.l16) = uint2{w2[0], w2[1]};
+          if (pl.l16 == 0) a.scales[(2 * pl.grp + h) * a.ldscales + row] = sc;
+        }
+      }
+    }
+  } else {
+    double am[1] = {absmax16(v)};
+    row_join<1, true, WAVES>(am, pl, a.groups, red + 2 * JOIN);
+    const float s32 = (float)(am[0] / 127.0);
+    const double s64 = (double)s32, inv64 = s32 > 0.f ? 1.0 / s64 : 0.0;
+    constexpr double MAGIC = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer (RNE)
+    // The product with 1 / s decides the code unless it is within 1e-9 of a tie;
+    // rows with a subnormal scale take the division.
+    const bool direct = s32 == 0.f || s32 >= 0x1p-126f;
+    wave_lds_sync();
+    bool tie = false;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const double f = fma(v[q], inv64, MAGIC);
+      const double d = fma(v[q], inv64, MAGIC - f);
+      tie |= !(fabs(d) < 0.5 - 1e-9);
+      bbuf[at + 8 * q] = (uint8_t)__builtin_bit_cast(uint64_t, f);
+      if ((q & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four codes at a time: fewer registers
+    }
+    if (__ballot((tie || !direct) && live)) {
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         const double f = fma(v[q], inv64, MAGIC);
         const double d = fma(v[q], inv64, MAGIC - f);
-        tie |= !(fabs(d) < 0.5 - 1e-9);
-        bbuf[at + 8 * q] = (uint8_t)__builtin_bit_cast(uint64_t, f);
-        if ((q & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four codes at a time: fewer registers
+        if (!direct || !(fabs(d) < 0.5 - 1e-9)) bbuf[at + 8 * q] = (uint8_t)quant_code(v[q], s64, inv64, 127.0);
+        __builtin_amdgcn_sched_barrier(0);  // one division at a time
       }
-      if (__ballot((tie || !direct) && live)) {
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const double f = fma(v[q], inv64, MAGIC);
-          const double d = fma(v[q], inv64, MAGIC - f);
-          if (!direct || !(fabs(d) < 0.5 - 1e-9)) bbuf[at + 8 * q] = (uint8_t)quant_code(v[q], s64, inv64, 127.0);
-          __builtin_amdgcn_sched_barrier(0);  // one division at a time
-        }
-      }
-      wave_lds_sync();
-      const u32x4_t w4 = *reinterpret_cast<const u32x4_t*>(bbuf + 16 * pl.l16);
-      if (live) {
-        *reinterpret_cast<u32x4_t*>((uint8_t*)a.y + row * a.ldy + (int64_t)pl.grp * 256 + 16 * pl.l16) = w4;
-        if (pl.grp == 0 && pl.l16 == 0) a.scales[row] = s32;
-      }
+    }
+    wave_lds_sync();
+    const u32x4_t w4 = *reinterpret_cast<const u32x4_t*>(bbuf + 16 * pl.l16);
+    if (live) {
+      *reinterpret_cast<u32x4_t*>((uint8_t*)a.y + row * a.ldy + (int64_t)pl.grp * 256 + 16 * pl.l16) = w4;
+      if (pl.grp == 0 && pl.l16 == 0) a.scales[row] = s32;
     }
   }
 }
@@ -253,7 +294,8 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
 //   n = (t - mu) r;  w = gamma g
 //   dt = r (w - mean(w) - n mean(w n)) + dsum;   dbranch = drop(dt)
 //   dgamma = sum over rows of g n;               dbeta = sum over rows of g
-// fp32, the row's sums, the deviations and n's product in fp64.
+// fp32, the row's sums in fp64; a deviation is the difference from the mean's two
+// fp32 parts.
 //
 // SUMS: a thread keeps its 16 columns of dgamma and dbeta over the rows of its
 // block; the blocks' sums are joined by k_colsum in a fixed order. Wide rows
@@ -269,30 +311,36 @@ __device__ __forceinline__ void rotate_back(float (&g)[16], const Runs<T>& raw, 
   transpose16_back(g, buf, l16);
 }
 
-template <typename TG, typename TT, typename TD, int NT, bool SUMS>
-__global__ __launch_bounds__(NT, SUMS ? 3 : 4) void k_layernorm_bwd(LayerNormBwdArgs a, int rows_per_block) {
+template <typename TG, typename TT, typename TD, bool WB, int NT, bool SUMS>
+__global__ __launch_bounds__(NT, SUMS ? 3 : 6) void k_layernorm_bwd(LayerNormBwdArgs a, int rows_per_block, int64_t row0) {
   constexpr int SET_BYTES = 16 * (16 + 4) * 4;
   extern __shared__ __align__(16) uint8_t lds[];
   const Place pl = place_of(a.groups, rows_per_block);
   float* tbuf = reinterpret_cast<float*>(lds + pl.set * SET_BYTES);
-  const int sets = blockDim.x >> 4;
-  double* red = reinterpret_cast<double*>(lds + sets * SET_BYTES);  // [4][sets]
-  const int64_t col = (int64_t)pl.grp * 256 + pl.l16 * 8;
+  constexpr int WAVES = NT / 64;
+  double* red = reinterpret_cast<double*>(lds + (blockDim.x >> 4) * SET_BYTES);  // [4][JOIN]
+  if (threadIdx.x < 4 * JOIN) red[threadIdx.x] = 0.0;
+  __syncthreads();
+  const uint32_t col = pl.grp * 256 + pl.l16 * 8;
   const int64_t k = (int64_t)a.groups * 256;
   const double inv_k = 1.0 / (double)k;
 
-  float gm[16], dg[16], db[16];
-  if (pl.active) {
-    load_vec16(a.gamma, col, gm);
+  // gamma: bf16 (or ones) as it lies in memory, or fp32
+  Weights16 gw;
+  float gf[WB ? 1 : 16], dg[16], db[16];
+  if constexpr (WB) {
+    gw.fetch(a.gamma, pl.active, col, pl.active ? 0x3f803f80u : 0u);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) gm[i] = 0.f;
+    for (int i = 0; i < 16; ++i) gf[i] = 0.f;
+    if (pl.active) load_vec16(a.gamma, col, gf);
   }
+  auto gm = [&](int i) { return WB ? gw.get(i) : gf[WB ? 0 : i]; };
 #pragma unroll
   for (int i = 0; i < 16; ++i) dg[i] = db[i] = 0.f;
   const int64_t step = (int64_t)gridDim.x * pl.rows;
-  for (int64_t base = (int64_t)blockIdx.x * pl.rows; base < a.m; base += step) {
-    const int64_t row = base + pl.slot;
+  for (int64_t base = row0 + (int64_t)blockIdx.x * pl.rows; base < a.m; base += step) {
+    const int64_t row = SUMS ? base + pl.slot : base;
     const bool live = pl.active && row < a.m;
     Runs<TG> rg;
     Runs<TT> rt;
@@ -306,6 +354,7 @@ __global__ __launch_bounds__(NT, SUMS ? 3 : 4) void k_layernorm_bwd(LayerNormBwd
       rg.zero();
       rt.zero();
     }
+    __builtin_amdgcn_sched_barrier(0);
     double c[3] = {0.0, 0.0, 0.0}, mean[1] = {0.0};
     float t[16];
 #pragma unroll
@@ -313,8 +362,10 @@ __global__ __launch_bounds__(NT, SUMS ? 3 : 4) void k_layernorm_bwd(LayerNormBwd
       t[i] = rt.get(i);
       mean[0] += (double)t[i];
     }
-    row_join<1, false>(mean, pl, a.groups, red);
+    row_join<1, false, WAVES>(mean, pl, a.groups, red);
+    __builtin_amdgcn_sched_barrier(0);
     const double mu = mean[0] * inv_k;
+    const float mu_hi = (float)mu, mu_lo = (float)(mu - (double)mu_hi);
     float g[16];
     if (a.rotate) {
       rotate_back(g, rg, tbuf, pl.l16);
@@ -322,25 +373,27 @@ __global__ __launch_bounds__(NT, SUMS ? 3 : 4) void k_layernorm_bwd(LayerNormBwd
 #pragma unroll
       for (int i = 0; i < 16; ++i) g[i] = rg.get(i);
     }
-    afresh(t);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const double d = (double)t[i] - mu, w = (double)(g[i] * gm[i]);
+      t[i] = (t[i] - mu_hi) - mu_lo;  // the deviation
+      if (!SUMS) g[i] *= gm(i);  // (g itself is not used again)
+      const double d = (double)t[i], w = (double)(SUMS ? g[i] * gm(i) : g[i]);
       c[0] += w;
       c[1] = fma(w, d, c[1]);
       c[2] = fma(d, d, c[2]);
       if ((i & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four at a time: fewer registers
     }
+    __builtin_amdgcn_sched_barrier(0);
     if (!pl.active) c[2] = 0.0;
-    row_join<3, false>(c, pl, a.groups, red + sets);
+    row_join<3, false, WAVES>(c, pl, a.groups, red + JOIN);
     const double r64 = 1.0 / sqrt(c[2] * inv_k + a.eps);
     const float r = (float)r64, m1 = (float)(c[0] * inv_k), m2 = (float)(r64 * (c[1] * inv_k));
-    afresh(t);
     float o[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float n = (float)(((double)t[i] - mu) * r64);
-      o[i] = fmaf(r, fmaf(-n, m2, g[i] * gm[i] - m1), rd.get(i));
+      const float n = t[i] * r;
+      o[i] = fmaf(r, fmaf(-n, m2, (SUMS ? g[i] * gm(i) : g[i]) - m1), rd.get(i));
       if constexpr (SUMS) {
         if (live) {
           dg[i] = fmaf(g[i], n, dg[i]);
@@ -354,6 +407,7 @@ __global__ __launch_bounds__(NT, SUMS ? 3 : 4) void k_layernorm_bwd(LayerNormBwd
         reinterpret_cast<double2*>(a.stats)[row] = double2{mu, r64};
       store16((TD*)a.dx + row * a.lddx + col, o);
       if (a.dbranch != nullptr) {
+        __builtin_amdgcn_sched_barrier(0);  // the generator's registers come last
         if (a.drop.rng != nullptr) {
           const PhiloxKey key = philox_key(a.drop.rng);
 #pragma unroll
@@ -366,6 +420,7 @@ __global__ __launch_bounds__(NT, SUMS ? 3 : 4) void k_layernorm_bwd(LayerNormBwd
         store16((TD*)a.dbranch + row * a.lddb + col, o);
       }
     }
+    if (!SUMS) return;  // (one row a block)
   }
   if (!SUMS || (a.dgamma == nullptr && a.dbeta == nullptr)) return;
   float* part = a.part + (int64_t)blockIdx.x * (2 * k);
@@ -410,6 +465,7 @@ __global__ __launch_bounds__(256) void k_layernorm_dw(LayerNormBwdArgs a, int sh
     rg.load((const TG*)a.dy + row * a.lddy + col);
     rt.load((const TT*)a.t + row * a.ldt + col);
     const double2 st = reinterpret_cast<const double2*>(a.stats)[row];
+    const float mu_hi = (float)st.x, mu_lo = (float)(st.x - (double)mu_hi), r = (float)st.y;
     float g[16];
     if (a.rotate) {
       rotate_back(g, rg, reinterpret_cast<float*>(lds + set * SET_BYTES), l16);
@@ -419,7 +475,7 @@ __global__ __launch_bounds__(256) void k_layernorm_dw(LayerNormBwdArgs a, int sh
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      dg[i] = fmaf(g[i], (float)(((double)rt.get(i) - st.x) * st.y), dg[i]);
+      dg[i] = fmaf(g[i], ((rt.get(i) - mu_hi) - mu_lo) * r, dg[i]);
       db[i] += g[i];
     }
   }
@@ -440,7 +496,7 @@ __global__ __launch_bounds__(256) void k_layernorm_dw(LayerNormBwdArgs a, int sh
 // ---------------------------------------------------------------- launchers
 namespace {
 
-constexpr int64_t LN_BLOCKS = 65536;    // blocks walk rows beyond that many (threads of a grid in 32 bits)
+constexpr int64_t LN_BLOCKS = 1 << 21;  // of a launch, whose threads are counted in 32 bits
 constexpr int64_t LN_BWD_BLOCKS = 512;  // partial rows of dgamma and dbeta
 constexpr int LN_WIDE_GROUPS = 16;      // rows of more groups leave their sums to k_layernorm_dw
 
@@ -448,13 +504,18 @@ template <typename TX, typename TS, bool RES, int OUT>
 hipError_t ln_launch(const LayerNormArgs& a, hipStream_t stream) {
   const Shape s = shape_of(a.m, a.groups, LN_BLOCKS);
   const int set_bytes = OUT == LN_OUT_BF16 ? 16 * 20 * 4 : 16 * 18 * 8;
-  const size_t lds = (size_t)(s.threads / 16) * (set_bytes + 3 * sizeof(double));
-  const dim3 grid((unsigned)s.blocks), block((unsigned)s.threads);
-  if (s.threads <= 256)
-    hipLaunchKernelGGL((k_layernorm<TX, TS, RES, OUT, 256>), grid, block, lds, stream, a, s.rows);
-  else
-    hipLaunchKernelGGL((k_layernorm<TX, TS, RES, OUT, 1024>), grid, block, lds, stream, a, s.rows);
-  return hipGetLastError();
+  const size_t lds = (size_t)(s.threads / 16) * set_bytes + 3 * JOIN * sizeof(double);
+  for (int64_t row0 = 0; row0 < a.m; row0 += s.blocks * s.rows) {
+    const int64_t blocks = std::min(s.blocks, (a.m - row0 + s.rows - 1) / s.rows);
+    const dim3 grid((unsigned)blocks), block((unsigned)s.threads);
+    if (s.threads <= 256)
+      hipLaunchKernelGGL((k_layernorm<TX, TS, RES, OUT, 256>), grid, block, lds, stream, a, s.rows, row0);
+    else
+      hipLaunchKernelGGL((k_layernorm<TX, TS, RES, OUT, 1024>), grid, block, lds, stream, a, s.rows, row0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename TX, typename TS, bool RES>
@@ -487,23 +548,34 @@ int dw_shares(int64_t m, int groups) {
   return (int)std::max<int64_t>(1, std::min<int64_t>((512 + groups - 1) / groups, (m + 15) / 16));
 }
 
-template <typename TG, typename TT, typename TD>
+template <typename TG, typename TT, typename TD, bool WB>
 hipError_t ln_bwd_launch(const LayerNormBwdArgs& a, hipStream_t stream) {
   const Shape s = ln_bwd_shape(a.m, a.groups);
-  const size_t lds = (size_t)(s.threads / 16) * (16 * 20 * 4 + 4 * sizeof(double));
+  const size_t lds = (size_t)(s.threads / 16) * (16 * 20 * 4) + 4 * JOIN * sizeof(double);
   const dim3 grid((unsigned)s.blocks), block((unsigned)s.threads);
   if (a.groups <= LN_WIDE_GROUPS) {
-    hipLaunchKernelGGL((k_layernorm_bwd<TG, TT, TD, 256, true>), grid, block, lds, stream, a, s.rows);
+    hipLaunchKernelGGL((k_layernorm_bwd<TG, TT, TD, WB, 256, true>), grid, block, lds, stream, a, s.rows, (int64_t)0);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((k_layernorm_bwd<TG, TT, TD, 1024, false>), grid, block, lds, stream, a, s.rows);
-  return hipGetLastError();
+  for (int64_t row0 = 0; row0 < a.m; row0 += s.blocks) {
+    const dim3 some((unsigned)std::min(s.blocks, a.m - row0));
+    hipLaunchKernelGGL((k_layernorm_bwd<TG, TT, TD, WB, 1024, false>), some, block, lds, stream, a, s.rows, row0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename TG, typename TT, typename TD>
+hipError_t ln_bwd_weight(const LayerNormBwdArgs& a, hipStream_t stream) {
+  return a.gamma.p == nullptr || a.gamma.bf16 ? ln_bwd_launch<TG, TT, TD, true>(a, stream)
+                                              : ln_bwd_launch<TG, TT, TD, false>(a, stream);
 }
 
 template <typename TG, typename TT>
 hipError_t ln_bwd_dx(const LayerNormBwdArgs& a, hipStream_t stream) {
   const hipError_t e =
-      a.dx_bf16 ? ln_bwd_launch<TG, TT, uint16_t>(a, stream) : ln_bwd_launch<TG, TT, float>(a, stream);
+      a.dx_bf16 ? ln_bwd_weight<TG, TT, uint16_t>(a, stream) : ln_bwd_weight<TG, TT, float>(a, stream);
   if (e != hipSuccess || a.stats == nullptr) return e;
   const int shares = dw_shares(a.m, a.groups);
   hipLaunchKernelGGL((k_layernorm_dw<TG, TT>), dim3((unsigned)(shares * a.groups)), dim3(256), 0, stream, a, shares);
