@@ -748,8 +748,9 @@ tp_status tp_layernorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, cons
  *             reaches the residual stream from behind.
  *   drop_p, rng  the forward's. dbranch NULL: not wanted (without a dropout it
  *             would be dx).
- *   dx        [m, k], dx_dtype, row pitch lddx; may be dsum or dy itself (same
- *             pointer, type and pitch); any other overlap is refused.
+ *   dx        [m, k], dx_dtype, row pitch lddx; may be dsum itself (same pointer,
+ *             type and pitch), and dy itself where neither dgamma nor dbeta is
+ *             wanted; any other overlap is refused.
  *   dbranch   [m, k], dx_dtype, row pitch lddb; overlaps nothing.
  *   dgamma, dbeta  fp32 [k], each NULL where it is not wanted. m == 0 gives zeros.
  *   workspace tp_layernorm_backward_workspace_size(m, k) bytes, 16-byte aligned,

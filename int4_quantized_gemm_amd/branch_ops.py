@@ -145,7 +145,7 @@ def tp_layernorm_rotate_backward(dy, t, gamma=None, eps=1e-5, dsum=None, drop_p=
     forward's. Returns (dx, dbranch, dgamma, dbeta): the residual's gradient,
     x's (drop(dx); None where drop_p is 0: it is dx), and the weights' (None
     where they are not wanted). dx (default dtype: dsum's, else t's) may be dsum
-    or dy itself."""
+    itself, or dy itself where neither weight's gradient is wanted."""
     index = _device(dy, "t gamma dsum rng dx dbranch dgamma dbeta workspace",
                     (t, gamma, dsum, rng, dx, dbranch, dgamma, dbeta, workspace))
     scope = _elsewhere(index, stream)

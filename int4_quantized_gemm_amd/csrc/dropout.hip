@@ -47,7 +47,8 @@ __device__ __forceinline__ void store_run(T* p, int n, const float (&v)[8]) {
 template <typename TX, typename TY, bool RES>
 __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a) {
   const int64_t runs = (a.k + 7) >> 3, total = a.m * runs;
-  const PhiloxKey key = philox_key(a.drop.rng);
+  const bool drops = a.drop.rng != nullptr;  // NULL: a threshold of 0, which drops nothing and may have no seed
+  const PhiloxKey key = drops ? philox_key(a.drop.rng) : PhiloxKey{};
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t run = (int64_t)blockIdx.x * 256 + threadIdx.x; run < total; run += step) {
     int64_t row;
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a) {
     float x[8], r[8];
     load_run((const TX*)a.x + row * a.ldx + c, n, x);
     if constexpr (RES) load_run((const TY*)a.res + row * a.ldr + c, n, r);
-    const u32x4_t w = philox4x32_10(key, (uint64_t)run);
+    const u32x4_t w = drops ? philox4x32_10(key, (uint64_t)run) : u32x4_t{};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       x[j] = philox_drop(w, j, a.drop, x[j]);

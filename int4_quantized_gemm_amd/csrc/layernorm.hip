@@ -83,6 +83,13 @@ struct Weights16 {
   }
 };
 
+// sum / k with its remainder taken back: the mean of equal values is that value,
+// so a constant row has deviations of zero.
+__device__ __forceinline__ double row_mean(double sum, double k, double inv_k) {
+  const double q = sum * inv_k;
+  return fma(fma(-q, k, sum), inv_k, q);
+}
+
 // What is read again after a join is widened again: not kept in twice the
 // registers across it.
 template <int N>
@@ -93,9 +100,9 @@ __device__ __forceinline__ void afresh(float (&t)[N]) {
 
 // ------------------------------------------------------------------ forward
 // Codes: fp64 throughout, so they are those of exact arithmetic on the normed
-// row. bf16 rows: the deviations and the row factor in fp64, what follows in
-// fp32, one rounding (a deviation is the difference from the mean's two fp32
-// parts: as exact as t allows). bf16 weights are fetched with the row.
+// row. bf16 rows: the row's sums in fp64, the rest in fp32, one rounding; a
+// deviation is the difference from the mean's two fp32 parts, as exact as t
+// allows. bf16 weights are fetched with the row.
 template <typename TX, typename TS, bool RES, int OUT, int NT>
 __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_per_block, int64_t row0) {
   typedef typename std::conditional<OUT == LN_OUT_BF16, float, double>::type T;
@@ -150,7 +157,7 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[0] += (double)t[i];
   row_join<1, false, WAVES>(s, pl, a.groups, red);
-  const double mu = s[0] * inv_k;
+  const double mu = row_mean(s[0], (double)k, inv_k);
   const float mu_hi = (float)mu, mu_lo = (float)(mu - (double)mu_hi);
   if (OUT != LN_OUT_BF16) afresh(t);
   s[0] = 0.0;
@@ -364,7 +371,7 @@ __global__ __launch_bounds__(NT, SUMS ? 3 : 6) void k_layernorm_bwd(LayerNormBwd
     }
     row_join<1, false, WAVES>(mean, pl, a.groups, red);
     __builtin_amdgcn_sched_barrier(0);
-    const double mu = mean[0] * inv_k;
+    const double mu = row_mean(mean[0], (double)k, inv_k);
     const float mu_hi = (float)mu, mu_lo = (float)(mu - (double)mu_hi);
     float g[16];
     if (a.rotate) {

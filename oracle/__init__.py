@@ -80,6 +80,9 @@ from .loader import dequantize, dequantize_unrotate, requantize
 from .lora import lora_delta, lora_add, lora_down_codes, lora_grad_codes
 from .norm import stream_sum, rmsnorm, rmsnorm_backward
 from .rope import norm_rope, norm_rope_backward
+from .branch import (
+    layernorm, layernorm_backward, philox4x32_10, drop_threshold, drop_factor, drop_keep, dropped, dropout, e4m3_value,
+    e4m3_code, quantize_fp8_rows, quantize_fp8_cols, quantize_fp8_blocks, qgemm_fp8)
 
 __all__ = [
     "GROUP",
@@ -115,4 +118,18 @@ __all__ = [
     "qgemm_w4",
     "qgemm_w8a8",
     "int_accumulate",
+    "layernorm",
+    "layernorm_backward",
+    "philox4x32_10",
+    "drop_threshold",
+    "drop_factor",
+    "drop_keep",
+    "dropped",
+    "dropout",
+    "e4m3_value",
+    "e4m3_code",
+    "quantize_fp8_rows",
+    "quantize_fp8_cols",
+    "quantize_fp8_blocks",
+    "qgemm_fp8",
 ]
