@@ -1238,7 +1238,7 @@ tp_status tp_layernorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, cons
       return fail(TP_ERR_NULL_POINTER, "residual and sum_out are given together or not at all");
     TP_TRY(check_matrix("residual", residual, m, k * ss, ldr, ss, &er));
     TP_TRY(check_matrix("sum_out", sum_out, m, k * ss, ldsum, ss, &esum));
-  } else if (drop_p != 0.0) {
+  } else if (drop_p != 0.0 && m > 0) {  // (no rows: empty tensors have no address)
     return fail(TP_ERR_NULL_POINTER, "drop_p=%g needs a residual and sum_out", drop_p);
   }
   TP_TRY(check_weight("gamma", gamma, g_dtype, k, &eg));

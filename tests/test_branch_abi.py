@@ -84,6 +84,7 @@ def test_layernorm_refusals(lib, kw, status):
 def test_layernorm_empty_and_optional(lib):
     assert ln(lib, m=0) == 0
     assert ln(lib, m=0, x=0, res=B, y=0, sc=0) == 0
+    assert ln(lib, m=0, x=0, res=0, sm=0, y=0, sc=0) == 0  # with a dropout
     assert ln(lib, m=0, res=0, sm=0, g=0, b=0, gdt=9, sdt=9, p=0.0, rng=0) == 0
     assert ln(lib, m=0, kind=1, sc=0, ldsc=0) == 0
     assert ln(lib, m=0, kind=0, ldsc=0) == 0
