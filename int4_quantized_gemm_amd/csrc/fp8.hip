@@ -72,7 +72,11 @@ constexpr int Q_PITCH = 33;  // dwords of a column's 128 codes in LDS
 
 }  // namespace
 
-// Row codes: a set of 16 lanes takes 128 columns of a row, a block 16 rows.
+// Row codes: a set of 16 lanes takes 128 columns of a row, a block 16 rows. 4096 x
+// 4096 bf16 13.9 us (50 MB, 3.6 TB/s: half of it the vector unit's work, the two
+// roundings an element), fp32 13.3 us (6.3 TB/s). Two or four rows of a set in
+// flight: 15.3 and 17.6 us, 2000 x 4096 9.9 and 10.6 against 8.9; ahead only from
+// some 10^8 elements on (16384 x 12288 136 and 134 against 144).
 template <typename TX>
 __global__ __launch_bounds__(256) void k_fp8_rows(QuantFp8Args a, uint32_t blocks_k) {
   const int l16 = threadIdx.x & 15;
@@ -88,7 +92,10 @@ __global__ __launch_bounds__(256) void k_fp8_rows(QuantFp8Args a, uint32_t block
 
 // A tile of 128 rows and 128 columns: 32 sets of 16 lanes, four consecutive rows
 // each, so that a lane holds the codes of four rows of a column as one dword
-// when it turns the tile through LDS.
+// when it turns the tile through LDS. Bound by the vector unit (four roundings an
+// element where rows and columns are wanted) and the tile's two barriers: 2000 x
+// 4096 bf16 by columns 11.7 us, both ways 18.0; blocks of 12288 x 4096 fp32 both
+// ways 54 us (302 MB, 5.6 TB/s).
 template <typename TX>
 __global__ __launch_bounds__(512) void k_fp8_tile(QuantFp8Args a, uint32_t blocks_k) {
   __shared__ float part[8][128];
@@ -223,6 +230,7 @@ __device__ __forceinline__ u32x4_t straight(const uint32_t (&w)[4], uint8_t* buf
 
 }  // namespace
 
+// (4096 x 4096 bf16 16.5 us: fp64 on the vector unit.)
 template <typename TX>
 __global__ __launch_bounds__(256) void k_fp8_rows_rotated(QuantFp8Args a, uint32_t groups) {
   __shared__ __align__(16) uint8_t turn[16 * Q_SET_BYTES];
@@ -250,7 +258,7 @@ __global__ __launch_bounds__(256) void k_fp8_rows_rotated(QuantFp8Args a, uint32
 }
 
 // A tile of 128 rows and 256 columns, as k_fp8_tile; the four rows of a lane stay
-// in registers as fp64 (two waves a SIMD).
+// in registers as fp64 (two waves a SIMD; 2000 x 4096 bf16 by columns 14.2 us).
 template <typename TX>
 __global__ __launch_bounds__(512, 2) void k_fp8_tile_rotated(QuantFp8Args a, uint32_t groups) {
   __shared__ __align__(16) uint8_t turn[32 * Q_SET_BYTES];

@@ -103,6 +103,13 @@ __device__ __forceinline__ void afresh(float (&t)[N]) {
 // row. bf16 rows: the row's sums in fp64, the rest in fp32, one rounding; a
 // deviation is the difference from the mean's two fp32 parts, as exact as t
 // allows. bf16 weights are fetched with the row.
+//
+// A block has one row (or a few short ones) and walks none: a loop's addresses
+// and the weights kept for it cost 32 registers, one wave a SIMD of four or five
+// (4096 x 4096, bf16 and its stream, dropout, rotated bf16 rows: 33.5 -> 26.5 us).
+// bf16 rows are bound by HBM (those 26.5 us: 5.1 TB/s), codes by fp64 beside it
+// (e4m3 codes of 2000 x 8192, fp32 in, bf16 stream: 33.2 us, 4.5 TB/s), one row of
+// 4096 by its chain of three joins (4.4 us).
 template <typename TX, typename TS, bool RES, int OUT, int NT>
 __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_per_block, int64_t row0) {
   typedef typename std::conditional<OUT == LN_OUT_BF16, float, double>::type T;
@@ -308,6 +315,11 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
 // block; the blocks' sums are joined by k_colsum in a fixed order. Wide rows
 // (more than 16 groups) have no registers for that, and as many blocks as rows:
 // their kernel leaves mu and r of each row, and k_layernorm_dw takes the sums.
+// Measured: 4096 x 4096, fp32 dy, bf16 t, dsum and dx, with the dropout 46.1 us
+// (HBM: 201 MB, 4.4 TB/s, three waves a SIMD: four spilled and were slower) and
+// 4.9 for the join of 512 partial rows; 333 x 12288 fp32 16.6 us (1.3 rows a
+// compute unit, each a chain of two joins), 8.1 for the sums' kernel (HBM: dy and t
+// again, from the last-level cache) and 4.0.
 template <typename T>
 __device__ __forceinline__ void rotate_back(float (&g)[16], const Runs<T>& raw, float* buf, int l16) {
 #pragma unroll
@@ -504,8 +516,15 @@ __global__ __launch_bounds__(256) void k_layernorm_dw(LayerNormBwdArgs a, int sh
 namespace {
 
 constexpr int64_t LN_BLOCKS = 1 << 21;  // of a launch, whose threads are counted in 32 bits
-constexpr int64_t LN_BWD_BLOCKS = 512;  // partial rows of dgamma and dbeta
-constexpr int LN_WIDE_GROUPS = 16;      // rows of more groups leave their sums to k_layernorm_dw
+// Partial rows of dgamma and dbeta, a pass at 512, 256 and 1024 blocks: 4096 x 4096,
+// fp32 dy and dropout 55.4, 68.5 and 58.5 us; 16384 x 1024 bf16 37.7, 51.9 and 40.5;
+// 4096 x 2048 bf16 25.6, 32.2 and 28.6.
+constexpr int64_t LN_BWD_BLOCKS = 512;
+// Rows of more groups leave their sums to k_layernorm_dw (a thread of 16 groups'
+// block keeps its 32 sums). A pass of 16 groups with the sums kept and left: 4096 x
+// 4096, fp32 dy and dropout 55.4 and 69.5 us, bf16 38.6 and 40.0; 300 x 4096 fp32
+// 15.5 and 19.2.
+constexpr int LN_WIDE_GROUPS = 16;
 
 template <typename TX, typename TS, bool RES, int OUT>
 hipError_t ln_launch(const LayerNormArgs& a, hipStream_t stream) {
@@ -538,6 +557,9 @@ hipError_t ln_x(const LayerNormArgs& a, hipStream_t stream) {
   return a.s_bf16 ? ln_out<TX, uint16_t, true>(a, stream) : ln_out<TX, float, true>(a, stream);
 }
 
+// Rows that keep their sums share a block of 16 sets, as long as 256 blocks have
+// work (one row a block from four groups on: 16384 x 1024 69.5 against 37.7 us,
+// 4096 x 2048 31.2 against 25.6).
 Shape ln_bwd_shape(int64_t m, int groups) {
   if (groups > LN_WIDE_GROUPS) return shape_of(m, groups, LN_BLOCKS);
   Shape s;
@@ -550,7 +572,8 @@ Shape ln_bwd_shape(int64_t m, int groups) {
   return s;
 }
 
-// Shares of the rows of k_layernorm_dw: two blocks a compute unit.
+// Shares of the rows of k_layernorm_dw: two blocks a compute unit (2048 x 8192, the
+// whole pass: 45.0 us, one block 49.4, four 45.3).
 int dw_shares(int64_t m, int groups) {
   return (int)std::max<int64_t>(1, std::min<int64_t>((512 + groups - 1) / groups, (m + 15) / 16));
 }
