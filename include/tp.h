@@ -723,7 +723,8 @@ tp_status tp_dropout(const void* x, tp_dtype x_dtype, int64_t ldx, const void* r
  *   gamma, beta  [k], g_dtype, contiguous, 16-byte aligned; NULL: all ones, all
  *             zeros.
  *   The other arguments as in tp_rmsnorm_rotate; ldscales is used for
- *   TP_NORM_OUT_FP8 only. For bf16 rows h has to be within fp32's range.
+ *   TP_NORM_OUT_FP8 only. For bf16 rows t - mean, h and its rotation have to be
+ *   within fp32's range.
  */
 tp_status tp_layernorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, const void* residual, int64_t ldr,
                               void* sum_out, int64_t ldsum, tp_dtype s_dtype, const void* gamma, const void* beta,
@@ -756,8 +757,8 @@ tp_status tp_layernorm_rotate(const void* x, tp_dtype x_dtype, int64_t ldx, cons
  *   workspace tp_layernorm_backward_workspace_size(m, k) bytes, 16-byte aligned,
  *             where dgamma or dbeta is wanted; not used otherwise.
  *   fp32 arithmetic, the sums of a row and the deviations in fp64; dx and dbranch
- *   rounded once, dgamma and dbeta summed in fp32 in a fixed order. gamma g has to
- *   be within fp32's range; from a deviation of 2^126 on the low bits of rr are
+ *   rounded once, dgamma and dbeta summed in fp32 in a fixed order. t - mean and
+ *   gamma g have to be within fp32's range; from a deviation of 2^126 on the low bits of rr are
  *   lost. k at most 16384.
  */
 size_t tp_layernorm_backward_workspace_size(int64_t m, int64_t k);

@@ -33,15 +33,17 @@ __device__ __forceinline__ uint32_t e4m3_code(double q) {
 }
 
 // What the quick way of codes needs of a scale: 1 / s from below and from above.
-// s below fp32's normal range has no such bounds (slow: every code is decided by
-// the division).
+// It takes x in fp32: from s = 2^-100 on, what fp32 holds as a subnormal is below
+// 2^-26 s, so its code is 0 whatever its rounding; up to 2^118, 448 s and a bit is
+// an fp32 number. Beyond, both are 0 and every code is decided by the division
+// (slow).
 struct E4m3Inverse {
   float s, lo, hi;
-  __device__ __forceinline__ bool slow() const { return s > 0.f && s < 0x1p-126f; }
+  __device__ __forceinline__ bool slow() const { return lo == 0.f && s > 0.f; }
 };
 
 __device__ __forceinline__ E4m3Inverse e4m3_inverse(float s) {
-  const float inv = s >= 0x1p-126f ? __builtin_amdgcn_rcpf(s) : 0.f;
+  const float inv = s >= 0x1p-100f && s <= 0x1p118f ? __builtin_amdgcn_rcpf(s) : 0.f;
   return E4m3Inverse{s, inv * (1.f - 0x1p-21f), inv * (1.f + 0x1p-21f)};
 }
 

@@ -104,9 +104,10 @@ __device__ __forceinline__ void afresh(float (&t)[N]) {
 // deviation is the difference from the mean's two fp32 parts, as exact as t
 // allows. bf16 weights are fetched with the row.
 //
-// A block has one row (or a few short ones) and walks none: a loop's addresses
-// and the weights kept for it cost 32 registers, one wave a SIMD of four or five
-// (4096 x 4096, bf16 and its stream, dropout, rotated bf16 rows: 33.5 -> 26.5 us).
+// A block has one row (or a few short ones) and walks none: 72 to 96 registers
+// instead of the 128 of a loop with its addresses and weights (4096 x 4096, bf16 and
+// its stream, dropout, rotated bf16 rows: 33.5 -> 26.5 us, with the sums across lanes
+// on the vector unit).
 // bf16 rows are bound by HBM (those 26.5 us: 5.1 TB/s), codes by fp64 beside it
 // (e4m3 codes of 2000 x 8192, fp32 in, bf16 stream: 33.2 us, 4.5 TB/s), one row of
 // 4096 by its chain of three joins (4.4 us).

@@ -127,8 +127,8 @@ def _check(t64, gamma, beta, eps, rotate, kind, got):
         # max|h|, and the mean by some 2^-52 of max|t|. There +0 and -0 are one
         # code, and a block of nothing else has any scale of that size.
         noise = 2.0 ** -44 * (np.abs(h).max(axis=1) + np.abs(t64).max(axis=1) / np.sqrt(t64.var(axis=1) + eps))
-        lost = 448 * s <= noise
-        assert np.all((448 * gs <= noise)[lost])
+        lost = 448.0 * s.astype(np.float64) <= noise
+        assert np.all((448.0 * gs.astype(np.float64) <= noise)[lost])
         assert np.array_equal(gs[~lost], s[~lost]), f"{int(np.sum(gs != s))} scales differ"
         zero = (np.abs(hr) <= noise[:, None]) & ((gq & 0x7F) == 0) & ((q & 0x7F) == 0)
         bad = (gq != q) & ~zero & ~lost.T.repeat(128, axis=1)
@@ -380,3 +380,47 @@ def test_non_finite_rows_leave_the_others(capsys):
         assert torch.equal(a.view(torch.uint8)[fine], b.view(torch.uint8)[fine]), kind
     a, b = (tp.tp_quantize_fp8(v.to(d))[0].view(torch.uint8) for v in (x, bad))
     assert torch.equal(a[fine], b[fine])
+
+
+# (a, c): rows a, a, c, 0 .. whose rotation has values c / 16 that fp32 rounds across
+# the midpoint of two codes (they are subnormal there), under a normal scale
+CROSSED = [("0x1.4510bep-113", "0x1.8abca4p-127"), ("0x1.0a7d3ep-113", "0x1.439b24p-127"), ("0x1.043b28p-113", "0x1.3c01a4p-127"),
+           ("0x1.d0327ap-113", "0x1.19d82ep-126"), ("0x1.9b4c7cp-113", "0x1.f373ep-127"), ("0x1.8b2b02p-113", "0x1.dfdd5cp-127"),
+           ("0x1.ef60e8p-113", "0x1.2cc6d2p-126"), ("0x1.00b378p-113", "0x1.37b854p-127")]
+
+
+def test_rotated_values_beyond_fp32():
+    """Rotated values are fp64: below fp32's normal numbers and above its largest
+    they have codes like any others."""
+    d = dev()
+    announce("tp_quantize_fp8 rotated values beyond fp32")
+    x = np.zeros((16, 256), dtype=np.float32)
+    for i, (a, c) in enumerate(CROSSED):
+        x[i, :3] = float.fromhex(a), float.fromhex(a), float.fromhex(c)
+    rng = np.random.default_rng(4)
+    x[8], x[9] = np.float32(3e38), rng.standard_normal(256) * 1e38
+    x[10] = np.float32(-1e38)
+    x[10, :128] *= np.float32(-2)
+    x[11:] = (rng.standard_normal((5, 256)) * 1e-37).astype(np.float32)
+    xt = torch.from_numpy(x)
+    for rows in (xt, xt[:8], xt[8:11]):
+        _check_quant(rows, rows.shape[0], 256, True, d, rows.to(d))
+
+
+def test_layernorm_codes_beyond_fp32():
+    """The same of normed rows under weights near the ends of fp32: rows of +-1
+    are their own norm (eps far below)."""
+    d = dev()
+    announce("tp_layernorm_rotate weights at the ends of fp32")
+    k = 512
+    rng = np.random.default_rng(6)
+    x = np.where(np.arange(k) % 2, 1.0, -1.0)[None, :].repeat(3, 0)
+    x[1] = -x[1]
+    x[2] = rng.standard_normal(k)
+    for size in (1e38, 1e-37, 4e-36):
+        gamma = np.minimum(size * (1 + np.abs(rng.standard_normal(k))), np.finfo(np.float32).max)
+        gamma = torch.from_numpy(gamma.astype(np.float32))
+        for rotate in (True, False):
+            got = tp.tp_layernorm_rotate(torch.from_numpy(x.astype(np.float32)).to(d), gamma.to(d), eps=1e-30, rotate=rotate,
+                                         out_kind="fp8")
+            _check(x.astype(np.float32).astype(np.float64), gamma, None, 1e-30, rotate, "fp8", got)
