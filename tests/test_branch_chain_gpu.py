@@ -241,6 +241,31 @@ def test_rows_past_2g_elements():
                    np.where(keep, (want[1] + B.U * np.abs(want[0])) * factor, 0), True, "dbranch")
 
 
+@pytest.mark.parametrize("k", [1024, 4352])
+def test_more_rows_than_blocks_of_a_launch(k):
+    """More rows than one launch takes blocks (2^21): the second launch's rows, and
+    the last of the first's."""
+    d = dev()
+    m = 2 ** 21 + 77
+    announce("more rows than blocks", m, k)
+    x = _noise(m, k, d, 3)
+    rows = np.array([0, 2 ** 21 - 1, 2 ** 21, 2 ** 21 + 1, m - 1])
+    at = torch.from_numpy(rows).to(d)
+    x64 = f64(x[at])
+    q, s = tp.tp_layernorm_rotate(x, eps=EPS, out_kind="fp8")
+    wq, ws = oracle.quantize_fp8_rows(oracle.rotate_groups(oracle.layernorm(x64, None, None, EPS)))
+    assert np.array_equal(_codes(q.view(torch.uint8)[at]), wq) and np.array_equal(host(s[:, at]), ws)
+    del q, s
+    dx, _, _, dbeta = tp.tp_layernorm_rotate_backward(x, x, eps=EPS, rotate=False, want_dgamma=False)
+    want = R.layernorm_backward(x64, x64, None, EPS, None, False, 1)
+    B.assert_close(f64(dx[at]), want[0], want[1], True, "dx")
+    total = sum(x[r:r + 65536].double().sum(dim=0) for r in range(0, m, 65536))
+    size = sum(x[r:r + 65536].abs().double().sum(dim=0) for r in range(0, m, 65536))
+    # a thread adds up to m / 512 rows one by one, then 512 partial rows by 16s
+    room = (m / 512 + 80) * B.U * f64(size.float()) * 1.01
+    assert np.all(np.abs(f64(dbeta) - total.cpu().numpy()) <= room)
+
+
 def test_codes_past_2g_elements():
     d = dev()
     m, k = 140001, 16384
