@@ -128,9 +128,11 @@ __device__ __forceinline__ void store_cols(T* p, int left, bool vec, const float
 // Measured: 4096 x 12288 x 4096, bf16 C, 200 us, 2060 TFLOP/s (the instruction alone
 // 3800); 2000 x 4096 x 4096 40 us, 1680. With an fp32 C 4096 x 4096 x 4096 136 us,
 // 1010, and with a scale a row of b and k 2048 86 us, 800 (the bf16 instruction
-// alone 1830): there the widening and the folds, 3 to 4 vector instructions beside
-// each matrix instruction, are the bound; widening each fragment of a beside the
-// products of the one before changed nothing (88 us).
+// alone 1830): there the widening and the folds, 3.5 to 4.5 vector instructions
+// beside each matrix instruction, are the bound (two of them are free, four make a
+// bf16 instruction 11.8 ns instead of 7.9, two waves a SIMD; beside an 8-bit one of
+// 14.3 ns four make 16.3); widening each fragment of a beside the products of the
+// one before changed nothing (88 us).
 template <int BM, int BN, int WM, int WN, int NS>
 struct F8Cfg {
   static constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, NT = 64 * NW;
