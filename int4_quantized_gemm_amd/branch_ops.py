@@ -14,6 +14,8 @@ tensors' device (or on `stream`, whose allocations it then uses). All tensors
 of a call sit on one device.
 """
 
+import functools
+
 import torch
 
 from . import _lib
@@ -23,6 +25,13 @@ from .block_ops import _device, _dt, _elsewhere, _empty, _mat, _raw_stream, _scr
 _F8 = torch.float8_e4m3fn
 _KIND = {"i8": (TP_NORM_OUT_I8, torch.int8), "bf16": (TP_NORM_OUT_BF16, torch.bfloat16), "fp8": (TP_NORM_OUT_FP8, _F8)}
 _BLOCK = 128  # elements that share a scale
+
+
+@functools.lru_cache(maxsize=4096)
+def _size_of(query, *sizes):
+    """A workspace's size, which depends on the call's sizes alone (asked for
+    anew it takes 0.5 us of a call of 8)."""
+    return getattr(_lib.load(), query)(*sizes)
 
 
 def _up(v):
@@ -133,7 +142,7 @@ def tp_layernorm_rotate(x, gamma=None, beta=None, eps=1e-5, residual=None, drop_
 
 def tp_layernorm_backward_workspace_size(m, k):
     """Bytes of workspace tp_layernorm_rotate_backward needs for dgamma and dbeta."""
-    return _lib.load().tp_layernorm_backward_workspace_size(m, k)
+    return _size_of("tp_layernorm_backward_workspace_size", m, k)
 
 
 def tp_layernorm_rotate_backward(dy, t, gamma=None, eps=1e-5, dsum=None, drop_p=0.0, rng=None, rotate=True,
@@ -239,7 +248,7 @@ def tp_quantize_fp8(x, block_rows=1, rotate=False, want="rows", q=None, scales=N
 
 def tp_qgemm_fp8_workspace_size(m, n, k, out_dtype=torch.float32):
     """Bytes of workspace tp_qgemm_fp8 needs (0: none)."""
-    return _lib.load().tp_qgemm_fp8_workspace_size(m, n, k, _lib.TP_BF16 if out_dtype == torch.bfloat16 else _lib.TP_F32)
+    return _size_of("tp_qgemm_fp8_workspace_size", m, n, k, _lib.TP_BF16 if out_dtype == torch.bfloat16 else _lib.TP_F32)
 
 
 def tp_qgemm_fp8(a, a_scales, b, b_scales, b_block_rows=128, out_dtype=torch.float32, out=None, workspace=None,
