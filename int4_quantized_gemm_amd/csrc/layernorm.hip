@@ -331,8 +331,18 @@ __device__ __forceinline__ void rotate_back(float (&g)[16], const Runs<T>& raw, 
   transpose16_back(g, buf, l16);
 }
 
+// Waves of a SIMD that the registers are cut for. Wide rows: six (80 registers)
+// where dx and gamma are bf16, five else, which spilled 7 to 27 of 80 (all fp32,
+// dsum, rotated: 2048 x 8192 101 -> 80 us, 2000 x 4352 62 -> 47; 333 x 12288 with an
+// fp32 gamma 29.5 -> 26.5).
+constexpr int ln_bwd_waves(bool dx_bf16, bool gamma_bf16, bool sums) {
+  return sums ? 3 : dx_bf16 && gamma_bf16 ? 6 : 5;
+}
+
 template <typename TG, typename TT, typename TD, bool WB, int NT, bool SUMS>
-__global__ __launch_bounds__(NT, SUMS ? 3 : 6) void k_layernorm_bwd(LayerNormBwdArgs a, int rows_per_block, int64_t row0) {
+__global__ __launch_bounds__(NT, ln_bwd_waves(sizeof(TD) == 2, WB, SUMS)) void k_layernorm_bwd(LayerNormBwdArgs a,
+                                                                                            int rows_per_block,
+                                                                                            int64_t row0) {
   constexpr int SET_BYTES = 16 * (16 + 4) * 4;
   extern __shared__ __align__(16) uint8_t lds[];
   const Place pl = place_of(a.groups, rows_per_block);
