@@ -316,11 +316,11 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
 // block; the blocks' sums are joined by k_colsum in a fixed order. Wide rows
 // (more than 16 groups) have no registers for that, and as many blocks as rows:
 // their kernel leaves mu and r of each row, and k_layernorm_dw takes the sums.
-// Measured: 4096 x 4096, fp32 dy, bf16 t, dsum and dx, with the dropout 46.1 us
+// Measured: 4096 x 4096, fp32 dy, bf16 t, dsum and dx, with the dropout 45.8 us
 // (HBM: 201 MB, 4.4 TB/s, three waves a SIMD: four spilled and were slower) and
-// 4.9 for the join of 512 partial rows; 333 x 12288 fp32 16.6 us (1.3 rows a
-// compute unit, each a chain of two joins), 8.1 for the sums' kernel (HBM: dy and t
-// again, from the last-level cache) and 4.0.
+// 4.8 for the join of 512 partial rows; 333 x 12288 fp32 16.1 us (1.3 rows a
+// compute unit, each a chain of two joins), 8.3 for the sums' kernel (HBM: dy and t
+// again, from the last-level cache) and 3.8.
 template <typename T>
 __device__ __forceinline__ void rotate_back(float (&g)[16], const Runs<T>& raw, float* buf, int l16) {
 #pragma unroll
