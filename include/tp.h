@@ -823,6 +823,8 @@ tp_status tp_quantize_fp8(const void* x, tp_dtype x_dtype, int64_t ldx, int64_t 
  *   2^-15 of the largest of eight products: 2e-5 of the sums' norm on ordinary
  *   data, a hundredth of bf16's own rounding. Blocks are added in fp32 in a fixed
  *   order. Code bytes 0x7f and 0xff are NaN and reach the outputs that read them.
+ *   Scales are any finite numbers: a product sa sb that fp32 does not hold (it
+ *   overflows, or is subnormal) is taken in fp64 with the block's sum.
  *   k a positive multiple of 128; k, lda and ldb below 2^24, m and n below 2^26,
  *   m n at most 2^36.
  *

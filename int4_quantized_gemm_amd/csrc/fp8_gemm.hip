@@ -87,6 +87,23 @@ __device__ __forceinline__ i32x8_t join8(u32x4_t lo, u32x4_t hi) {
   return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
+// The exponent of a scale and 62: at most MID_SCALES where the scale is within 2^-63 ..
+// 2^62, or 0 (infinity and NaN too, whose products show whatever way they take). The
+// product of two such is 0 because one of them is, or a normal number.
+constexpr uint32_t MID_SCALES = 124;
+__device__ __forceinline__ uint32_t scale_reach(float s) { return (uint32_t)(__builtin_amdgcn_frexp_expf(s) + 62); }
+
+// A block's sum folded into the results where its scales may not be such: a block's
+// sum is 0 or within 2^-18 .. 2^25, so p sa sb is often an ordinary number where fp32
+// holds sa sb as a subnormal, as 0 or as infinity. There fp64 holds all of it. Where
+// the product is a normal number the bits are those of the usual way: a row's
+// results do not depend on its neighbours' scales.
+__device__ __forceinline__ float fold_wide(float p, float sa, float sb, float c) {
+  const float s = sa * sb;
+  if (__builtin_isnormal(s)) return fmaf(p, s, c);
+  return (float)fma((double)p * (double)sa, (double)sb, (double)c);
+}
+
 // N consecutive columns of a row of C, as far as it has them.
 template <int N, typename T>
 __device__ __forceinline__ void store_cols(T* p, int left, bool vec, const float (&v)[N]) {
@@ -221,65 +238,110 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void k_qgemm_fp8(Gem
   };
 
   f32x4_t acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   constexpr int MFMAS = FN * (OUT_BF16 ? 1 : 4);
   constexpr int VALUS = (FN * (BROWS ? 8 : 4) + (OUT_BF16 ? 0 : 16) + MFMAS - 1) / MFMAS;
+  // WIDE: with fold_wide. Otherwise reach says afterwards whether a scale may need it:
+  // one that this wave fetched (FETCHED, a read of LDS a step), or the few that it
+  // uses. 300 x 4096 x 4096 15.0 us without a look at the scales, 15.3 at those it
+  // uses, 15.7 at those it fetched; 128 x 128 at 2000 x 4096 x 4096 36.5, 38.0 and 37.5.
+  constexpr bool FETCHED = BROWS || FM > 2;
+  uint32_t reach = 0;
+  auto walk = [&](auto wide) {
+    constexpr bool WIDE = decltype(wide)::value;
 #pragma unroll
-  for (int s = 0; s < NS - 1; ++s) issue(s);
-  __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE((NS - 2) * (LPW + 1)));
-  barrier_only();
-  for (int ks = 0; ks < KS; ++ks) {
-    issue(ks + NS - 1);
-    const uint8_t* st = ring + (ks & (NS - 1)) * Cfg::STAGE;
-    const float* ss = reinterpret_cast<const float*>(st + Cfg::AB_BYTES);
-    Frag<!OUT_BF16> wb[FN], wa;
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) wb[j].set(read_b(st, j));
-    i32x8_t fa = read_a(st, 0);
-    const float sw = BROWS ? 1.f : ss[BM + (wn0 >> 7)];
-    float sc[FM];
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sc[i] = ss[arow + 16 * i];
-    f32x4_t sbv[BROWS ? FN : 1];
-    if constexpr (BROWS) {
+    for (int s = 0; s < NS - 1; ++s) issue(s);
+    __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE((NS - 2) * (LPW + 1)));
+    barrier_only();
+    for (int ks = 0; ks < KS; ++ks) {
+      issue(ks + NS - 1);
+      const uint8_t* st = ring + (ks & (NS - 1)) * Cfg::STAGE;
+      const float* ss = reinterpret_cast<const float*>(st + Cfg::AB_BYTES);
+      if constexpr (WIDE) {  // one fragment of b at a time: no more registers than the loop below
+        const float sw = BROWS ? 1.f : ss[BM + (wn0 >> 7)];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) sbv[j] = *reinterpret_cast<const f32x4_t*>(ss + BM + wn0 + 4 * FN * g4 + 4 * j);
-    }
-    f32x4_t p[2][FN];
-    auto fold = [&](int i) {
-      const float s = sc[i] * sw;
+        for (int i = 0; i < FM; ++i) {
+          Frag<!OUT_BF16> wb[1], wa;
+          wa.set(read_a(st, i));
+          const float sa = ss[arow + 16 * i];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
+          for (int j = 0; j < FN; ++j) {
+            f32x4_t p[1];
+            wb[0].set(read_b(st, j));
+            block_sums(wb, wa, p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = fmaf(p[i & 1][j][e], BROWS ? s * sbv[BROWS ? j : 0][e] : s, acc[i][j][e]);
-        asm volatile("" : "+v"(acc[i][j]));  // here, not behind the barrier
-      }
-    };
+            for (int e = 0; e < 4; ++e)
+              acc[i][j][e] = fold_wide(p[0][e], sa, BROWS ? ss[BM + wn0 + 4 * FN * g4 + 4 * j + e] : sw, acc[i][j][e]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      } else {
+        Frag<!OUT_BF16> wb[FN], wa;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      wa.set(fa);
-      if (i + 1 < FM) fa = read_a(st, i + 1);
-      block_sums(wb, wa, p[i & 1]);
-      if (i > 0) fold(i - 1);
+        for (int j = 0; j < FN; ++j) wb[j].set(read_b(st, j));
+        i32x8_t fa = read_a(st, 0);
+        const float sw = BROWS ? 1.f : ss[BM + (wn0 >> 7)];
+        float sc[FM];
 #pragma unroll
-      for (int t = 0; t < MFMAS; ++t) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, VALUS, 0);
+        for (int i = 0; i < FM; ++i) sc[i] = ss[arow + 16 * i];
+        f32x4_t sbv[BROWS ? FN : 1];
+        if constexpr (BROWS) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) sbv[j] = *reinterpret_cast<const f32x4_t*>(ss + BM + wn0 + 4 * FN * g4 + 4 * j);
+        }
+        const float own = FETCHED ? ss[sl * 64 + lane] : sw;
+        f32x4_t p[2][FN];
+        auto fold = [&](int i) {
+          const float s = sc[i] * sw;
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[i][j][e] = fmaf(p[i & 1][j][e], BROWS ? s * sbv[BROWS ? j : 0][e] : s, acc[i][j][e]);
+            asm volatile("" : "+v"(acc[i][j]));  // here, not behind the barrier
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          wa.set(fa);
+          if (i + 1 < FM) fa = read_a(st, i + 1);
+          block_sums(wb, wa, p[i & 1]);
+          if (i > 0)
+            fold(i - 1);
+          else
+            reach = max(reach, scale_reach(own));
+          if constexpr (!FETCHED) reach = max(reach, scale_reach(sc[i]));
+#pragma unroll
+          for (int t = 0; t < MFMAS; ++t) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, VALUS, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        fold(FM - 1);
       }
       __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE((NS - 2) * (LPW + 1)) & LGKMCNT0_ENCODE);  // the next stage has landed
+      barrier_only();
     }
-    fold(FM - 1);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE((NS - 2) * (LPW + 1)) & LGKMCNT0_ENCODE);  // the next stage has landed
-    barrier_only();
-  }
-  __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE(0));  // no load to LDS outlives the block
+    __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE(0));  // no load to LDS outlives the block
+  };
+  walk(std::false_type{});
+  // The sums again, with fp64 where it is needed, where a scale of the block is far
+  // from 1 (as a branch in the loop: 258 spilled registers in the largest tile).
+  __shared__ uint32_t far_waves[Cfg::NW];
+  const uint64_t far_lanes = __ballot(reach > MID_SCALES);  // (of all lanes: not inside the branch)
+  if (lane == 0) far_waves[wave] = far_lanes != 0;
+  __syncthreads();
+  uint32_t any = 0;
+#pragma unroll
+  for (int w = 0; w < Cfg::NW; ++w) any |= far_waves[w];
+  if (__builtin_amdgcn_readfirstlane(any) != 0) walk(std::true_type{});
 
   const int nb = n0 + wn0 + 4 * FN * g4;
   if constexpr (PARTIAL) {
@@ -353,54 +415,70 @@ __global__ __launch_bounds__(512, 1) void k_qgemm_fp8_few(GemmFp8Args g) {
   const int nb = n0 + 4 * FN * g4;
   const float* sbp = BROWS ? g.sb : g.sb + (int64_t)(n0 >> 7) * g.ldsb;
   f32x4_t acc[FM][FN];
+  uint32_t reach = 0;  // of the scales that this wave meets, as in k_qgemm_fp8
+  auto walk = [&](auto wide) {
+    constexpr bool WIDE = decltype(wide)::value;
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int ks0 = wave; ks0 < KB; ks0 += NW * U) {
-    i32x8_t rb[U][FN], ra[U][FM];
-    float sc[U][FM];
-    f32x4_t sbv[U][FN];
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int ks0 = wave; ks0 < KB; ks0 += NW * U) {
+      i32x8_t rb[U][FN], ra[U][FM];
+      float sc[U][FM];
+      f32x4_t sbv[U][FN];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // (past the last step: the last one again, with scales of zero)
-      const int ks = ks0 + NW * u, at = min(ks, KB - 1);
+      for (int u = 0; u < U; ++u) {
+        // (past the last step: the last one again, with scales of zero)
+        const int ks = ks0 + NW * u, at = min(ks, KB - 1);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const u32x4_t* p = reinterpret_cast<const u32x4_t*>(bp[j] + (int64_t)at * 128);
-        rb[u][j] = join8(p[0], p[1]);
-      }
+        for (int j = 0; j < FN; ++j) {
+          const u32x4_t* p = reinterpret_cast<const u32x4_t*>(bp[j] + (int64_t)at * 128);
+          rb[u][j] = join8(p[0], p[1]);
+        }
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const u32x4_t* p = reinterpret_cast<const u32x4_t*>(ap[i] + (int64_t)at * 128);
-        ra[u][i] = join8(p[0], p[1]);
-        sc[u][i] = ks < KB ? sp[i][(int64_t)at * g.ldsa] : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sbv[u][j][e] = BROWS ? sbp[(int64_t)at * g.ldsb + min(nb + 4 * j + e, N - 1)] : sbp[at];
-    }
-    __builtin_amdgcn_sched_barrier(0);  // all loads of the batch go out first
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u > 0 && ks0 + NW * u >= KB) break;
-      Frag<true> fb[FN], fa;
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j].set(rb[u][j]);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        fa.set(ra[u][i]);
-        f32x4_t p[FN];
-        block_sums(fb, fa, p);
+        for (int i = 0; i < FM; ++i) {
+          const u32x4_t* p = reinterpret_cast<const u32x4_t*>(ap[i] + (int64_t)at * 128);
+          ra[u][i] = join8(p[0], p[1]);
+          sc[u][i] = ks < KB ? sp[i][(int64_t)at * g.ldsa] : 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[j][e], sc[u][i] * sbv[u][j][e], acc[i][j][e]);
+          for (int e = 0; e < 4; ++e)
+            sbv[u][j][e] = BROWS ? sbp[(int64_t)at * g.ldsb + min(nb + 4 * j + e, N - 1)] : sbp[at];
+      }
+      __builtin_amdgcn_sched_barrier(0);  // all loads of the batch go out first
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u > 0 && ks0 + NW * u >= KB) break;
+        if constexpr (!WIDE) {
+#pragma unroll
+          for (int i = 0; i < FM; ++i) reach = max(reach, scale_reach(sc[u][i]));
+#pragma unroll
+          for (int j = 0; j < (BROWS ? FN : 1); ++j)
+#pragma unroll
+            for (int e = 0; e < (BROWS ? 4 : 1); ++e) reach = max(reach, scale_reach(sbv[u][j][e]));
+        }
+        Frag<true> fb[FN], fa;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j].set(rb[u][j]);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          fa.set(ra[u][i]);
+          f32x4_t p[FN];
+          block_sums(fb, fa, p);
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[i][j][e] = WIDE ? fold_wide(p[j][e], sc[u][i], sbv[u][j][e], acc[i][j][e])
+                                  : fmaf(p[j][e], sc[u][i] * sbv[u][j][e], acc[i][j][e]);
+        }
       }
     }
-  }
+  };
+  walk(std::false_type{});
+  if (__ballot(reach > MID_SCALES) != 0) walk(std::true_type{});
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
