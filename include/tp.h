@@ -777,6 +777,8 @@ tp_status tp_layernorm_rotate_backward(const void* dy, tp_dtype dy_dtype, int64_
  *
  *   s     fp32(amax / 448) over the block, 0 for a block of zeros
  *   code  e4m3(x / s): nearest even, at most 448 in magnitude; 0 where s is 0
+ *   A NaN in x has a NaN code (0x7f or 0xff) and no part in amax; an infinity has
+ *   one too, under an infinite scale. The products that read them show it.
  *
  *   x        [m, k], x_dtype, row pitch ldx; a_flags TP_A_ROTATE: its rows are
  *            rotated first (k a multiple of 256), TP_A_PREROTATED: any k.

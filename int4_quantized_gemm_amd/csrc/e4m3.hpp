@@ -53,7 +53,8 @@ __device__ __forceinline__ E4m3Inverse e4m3_inverse(float s) {
 // enclose x / s (the roundings of x, of the factor and of the product, 2^-24 each,
 // and 1 / s, 2^-23, stay below 2^-21 together), so where both round to one code it
 // is that of x / s. Where they do not (one value in 10^5, one wave in a hundred)
-// the fp64 division decides.
+// the fp64 division decides. NaN, and infinity under its infinite scale, have a NaN
+// code either way.
 template <int N, typename X, typename D, typename S>
 __device__ __forceinline__ void e4m3_codes(uint32_t (&w)[N / 4], X x, D exact, S of, bool slow) {
   uint32_t up[N / 4];
@@ -85,6 +86,11 @@ __device__ __forceinline__ void e4m3_codes(uint32_t (&w)[N / 4], X x, D exact, S
       if (((w[i >> 2] ^ up[i >> 2]) & mask) != 0 || a.slow())
         w[i >> 2] = (w[i >> 2] & ~mask) | (e4m3_code(exact(i) / (double)a.s) << (8 * (i & 3)));
       __builtin_amdgcn_sched_barrier(0);  // one division at a time
+    }
+    if (__ballot(slow)) {  // (apart: in the division's way it took 3% more for every row)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (of(i).slow() && !(fabs(exact(i)) < __builtin_inf())) w[i >> 2] |= 0x7fu << (8 * (i & 3));
     }
   }
 }
