@@ -255,7 +255,8 @@ def tp_qgemm_fp8(a, a_scales, b, b_scales, b_block_rows=128, out_dtype=torch.flo
                  stream=None):
     """C [m, n] = a . b^T of e4m3 codes [m, k] and [n, k] with a scale for each
     block of 128 along k: a_scales [k / 128, m]; b_scales [n / 128 rounded up,
-    k / 128] (a scale for 128 x 128 codes), or with b_block_rows=1 [k / 128, n]."""
+    k / 128] (a scale for 128 x 128 codes), or with b_block_rows=1 [k / 128, n].
+    A new C has rows at multiples of 16 bytes, as the other operators take them."""
     index = _device(a, "a_scales b b_scales out workspace", (a_scales, b, b_scales, out, workspace))
     scope = _elsewhere(index, stream)
     if scope is not None:
@@ -269,7 +270,9 @@ def tp_qgemm_fp8(a, a_scales, b, b_scales, b_block_rows=128, out_dtype=torch.flo
     rows, cols = (kb, n) if b_block_rows == 1 else (_up(n) // _BLOCK, kb)
     ldsb = _mat(b_scales, "b_scales", rows, cols, torch.float32)
     if out is None:
-        out, ldc = _empty((m, n), (n, 1), dtype=out_dtype, device=a.device), n
+        per = 8 if out_dtype == torch.bfloat16 else 4
+        ldc = -(-n // per) * per
+        out = _empty((m, n), (ldc, 1), dtype=out_dtype, device=a.device)
     else:
         ldc = _mat(out, "out", m, n)
     need = tp_qgemm_fp8_workspace_size(m, n, k, out.dtype)
