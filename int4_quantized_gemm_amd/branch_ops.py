@@ -256,7 +256,8 @@ def tp_qgemm_fp8(a, a_scales, b, b_scales, b_block_rows=128, out_dtype=torch.flo
     """C [m, n] = a . b^T of e4m3 codes [m, k] and [n, k] with a scale for each
     block of 128 along k: a_scales [k / 128, m]; b_scales [n / 128 rounded up,
     k / 128] (a scale for 128 x 128 codes), or with b_block_rows=1 [k / 128, n].
-    A new C has rows at multiples of 16 bytes, as the other operators take them."""
+    A new C has rows at multiples of 16 bytes, as the other operators take them.
+    k == 0 (the weight's gradient of no tokens) gives zeros."""
     index = _device(a, "a_scales b b_scales out workspace", (a_scales, b, b_scales, out, workspace))
     scope = _elsewhere(index, stream)
     if scope is not None:
@@ -275,9 +276,12 @@ def tp_qgemm_fp8(a, a_scales, b, b_scales, b_block_rows=128, out_dtype=torch.flo
         out = _empty((m, n), (ldc, 1), dtype=out_dtype, device=a.device)
     else:
         ldc = _mat(out, "out", m, n)
+    out_dt = _dt(out, "out")
+    if k == 0 and b_block_rows in (1, _BLOCK):  # no tokens: the C entry point has no products of nothing
+        return out.zero_()
     need = tp_qgemm_fp8_workspace_size(m, n, k, out.dtype)
     ws_ptr, ws_bytes, ws = (None, 0, None) if workspace is None and not need else _scratch(workspace, need, a.device)
     _lib.check(_lib.load().tp_qgemm_fp8(
         a.data_ptr(), lda, a_scales.data_ptr(), ldsa, b.data_ptr(), ldb, b_scales.data_ptr(), ldsb, b_block_rows, m, n,
-        k, out.data_ptr(), _dt(out, "out"), ldc, ws_ptr, ws_bytes, _raw_stream(index)))
+        k, out.data_ptr(), out_dt, ldc, ws_ptr, ws_bytes, _raw_stream(index)))
     return out
