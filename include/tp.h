@@ -714,7 +714,8 @@ tp_status tp_dropout(const void* x, tp_dtype x_dtype, int64_t ldx, const void* r
  *   h[r, j]   (t[r, j] - mean_j(t)) / sqrt(mean_j((t - mean)^2) + eps) * gamma[j]
  *             + beta[j]
  *   y         a_flags TP_A_ROTATE: h . blockdiag(Q); TP_A_PREROTATED: h.
- *             TP_NORM_OUT_I8 and TP_NORM_OUT_BF16 as in tp_rmsnorm_rotate.
+ *             TP_NORM_OUT_I8 and TP_NORM_OUT_BF16 as in tp_rmsnorm_rotate; an
+ *             int8 row whose h is not finite has an infinite scale.
  *             TP_NORM_OUT_FP8: e4m3 [m, k] (row pitch ldy bytes) and scales fp32
  *             [k / 128, m] (row pitch ldscales elements), the codes and scales
  *             that tp_quantize_fp8 with block_rows 1 defines for these rows.

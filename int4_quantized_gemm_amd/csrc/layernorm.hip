@@ -268,7 +268,14 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
       }
     }
   } else {
-    double am[1] = {absmax16(v)};
+    // Maxima drop NaN: a row that holds one gets an infinite scale, so that what reads
+    // it is not finite either. (A rotated group is NaN everywhere.)
+    uint32_t top = (uint32_t)(__builtin_bit_cast(uint64_t, v[0]) >> 32) & 0x7fffffffu;
+    if (!a.rotate) {
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = max(top, (uint32_t)(__builtin_bit_cast(uint64_t, v[i]) >> 32) & 0x7fffffffu);
+    }
+    double am[1] = {top > 0x7ff00000u ? __builtin_inf() : absmax16(v)};
     row_join<1, true, WAVES>(am, pl, a.groups, red + 2 * JOIN);
     const float s32 = (float)(am[0] / 127.0);
     const double s64 = (double)s32, inv64 = s32 > 0.f ? 1.0 / s64 : 0.0;

@@ -76,3 +76,40 @@ def test_nan_reaches_the_product(size):
         bad = np.zeros(m, dtype=bool)
         bad[[3, 9, 60]] = True
         assert not np.any(np.isfinite(y[bad])) and np.all(np.isfinite(y[~bad]))
+
+
+# rows of one group, rows that share a block, wide rows
+@pytest.mark.parametrize("m,k", [(9, 256), (9, 768), (9, 4096), (9, 12288)])
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("where", ["x", "residual", "gamma", "beta"])
+def test_int8_rows_show_what_is_not_finite(m, k, rotate, where):
+    """A row that is not finite has a scale that is not; the others keep their bytes."""
+    d = dev()
+    announce("tp_layernorm_rotate int8 rows, not finite in", where, m, k, rotate)
+    rng = np.random.default_rng(k)
+    draw = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(d)  # noqa: E731
+    x, res, gamma, beta = draw(m, k), draw(m, k), draw(k), draw(k)
+    call = lambda: tp.tp_layernorm_rotate(x, gamma, beta, residual=res, rotate=rotate, out_kind="i8")  # noqa: E731
+    q0, s0, _ = call()
+    assert torch.all(torch.isfinite(s0))
+    for value, col in ((float("nan"), 0), (float("nan"), k - 1), (float("inf"), 17), (float("nan"), 140)):
+        bad = np.zeros(m, dtype=bool)
+        if where in ("x", "residual"):
+            t = x if where == "x" else res
+            bad[[2, 8]] = True
+            kept = t[[2, 8], col].clone()
+            t[[2, 8], col] = value
+        else:
+            t = gamma if where == "gamma" else beta
+            bad[:] = True
+            kept = t[col].clone()
+            t[col] = value
+        q, s, _ = call()
+        assert not np.any(np.isfinite(host(s)[bad])), (value, col)
+        assert np.abs(host(q).astype(int)).max() <= 127
+        fine = torch.from_numpy(~bad).to(d)
+        assert torch.equal(q[fine], q0[fine]) and torch.equal(s[fine], s0[fine])
+        if where in ("x", "residual"):
+            t[[2, 8], col] = kept
+        else:
+            t[col] = kept
