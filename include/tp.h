@@ -821,10 +821,14 @@ tp_status tp_quantize_fp8(const void* x, tp_dtype x_dtype, int64_t ldx, int64_t 
  *   c        [m, n], c_dtype, row pitch ldc; aligned to the element.
  *   workspace  tp_qgemm_fp8_workspace_size(m, n, k, c_dtype) bytes, 16-byte
  *            aligned (partial sums where k is split; nothing is kept between calls).
- *   Sums: with an fp32 c a block's products are exact and summed in fp32. With a
- *   bf16 c the 8-bit matrix instruction sums them, which drops what is below about
- *   2^-15 of the largest of eight products: 2e-5 of the sums' norm on ordinary
- *   data, a hundredth of bf16's own rounding. Blocks are added in fp32 in a fixed
+ *   Sums: with an fp32 c, and with a bf16 c of few rows (m up to 16, or up to 64
+ *   where ceil(m / 16) n k is at most 2^25), a block's products are exact and summed
+ *   in fp32. With a bf16 c of more rows the 8-bit matrix instruction sums them, which
+ *   drops what is far below the largest of the products it adds: 1.3e-5 of the sums'
+ *   norm on ordinary data, at most 5e-5 with channels up to 100 times the rest, a
+ *   thirtieth of bf16's own rounding (sums that cancel are off by that of their
+ *   terms). So a row's bf16 result may round the other way (1 to 2% of them do) when
+ *   more rows share its call. Blocks are added in fp32 in a fixed
  *   order. Code bytes 0x7f and 0xff are NaN and reach the outputs that read them.
  *   Scales are any finite numbers: a product sa sb that fp32 does not hold (it
  *   overflows, or is subnormal) is taken in fp64 with the block's sum.
