@@ -244,8 +244,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void k_qgemm_fp8(Gem
   constexpr int VALUS = (FN * (BROWS ? 8 : 4) + (OUT_BF16 ? 0 : 16) + MFMAS - 1) / MFMAS;
   // WIDE: with fold_wide. Otherwise reach says afterwards whether a scale may need it:
   // one that this wave fetched (FETCHED, a read of LDS a step), or the few that it
-  // uses. 300 x 4096 x 4096 15.0 us without a look at the scales, 15.3 at those it
-  // uses, 15.7 at those it fetched; 128 x 128 at 2000 x 4096 x 4096 36.5, 38.0 and 37.5.
+  // uses. The look at those it uses takes 2% of 300 x 4096 x 4096 (64 x 128 tiles,
+  // 15.0 us) and 3% of 2000 x 4096 x 4096 (128 x 128, 38 us), at those it fetched 5%
+  // and 1%.
   constexpr bool FETCHED = BROWS || FM > 2;
   uint32_t reach = 0;
   auto walk = [&](auto wide) {
@@ -294,7 +295,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void k_qgemm_fp8(Gem
 #pragma unroll
           for (int j = 0; j < FN; ++j) sbv[j] = *reinterpret_cast<const f32x4_t*>(ss + BM + wn0 + 4 * FN * g4 + 4 * j);
         }
-        const float own = FETCHED ? ss[sl * 64 + lane] : sw;
+        float own = sw;
         f32x4_t p[2][FN];
         auto fold = [&](int i) {
           const float s = sc[i] * sw;
@@ -311,10 +312,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void k_qgemm_fp8(Gem
           wa.set(fa);
           if (i + 1 < FM) fa = read_a(st, i + 1);
           block_sums(wb, wa, p[i & 1]);
-          if (i > 0)
-            fold(i - 1);
-          else
-            reach = max(reach, scale_reach(own));
+          if (FETCHED && i == FM - 2) own = ss[sl * 64 + lane];
+          if (i > 0) fold(i - 1);
+          if (i == (FETCHED ? FM - 1 : 0)) reach = max(reach, scale_reach(own));
           if constexpr (!FETCHED) reach = max(reach, scale_reach(sc[i]));
 #pragma unroll
           for (int t = 0; t < MFMAS; ++t) {
