@@ -190,7 +190,7 @@ struct LayerNormBwdArgs {
   void* dx;
   int dx_bf16;
   int64_t lddx;
-  void* dbranch;  // nullptr: not wanted; needs drop.rng
+  void* dbranch;  // nullptr: not wanted (without drop.rng nothing drops: dx's values)
   int64_t lddb;
   float *dgamma, *dbeta;  // nullptr: not wanted
   float* part;            // layernorm_bwd_workspace_bytes(m, groups) bytes, where one is

@@ -73,8 +73,9 @@ constexpr int Q_PITCH = 33;  // dwords of a column's 128 codes in LDS
 }  // namespace
 
 // Row codes: a set of 16 lanes takes 128 columns of a row, a block 16 rows. 4096 x
-// 4096 bf16 13.9 us (50 MB, 3.6 TB/s: half of it the vector unit's work, the two
-// roundings an element), fp32 13.3 us (6.3 TB/s). Two or four rows of a set in
+// 4096 bf16 14.1 us (50 MB, 3.6 TB/s; the vector unit is busy 65% of the time, two
+// waves in three take the division of some value), fp32 13.3 us (6.3 TB/s; busy 35%,
+// as few divisions as e4m3.hpp says). Two or four rows of a set in
 // flight: 15.3 and 17.6 us, 2000 x 4096 9.9 and 10.6 against 8.9; ahead only from
 // some 10^8 elements on (16384 x 12288 136 and 134 against 144).
 template <typename TX>
@@ -92,10 +93,11 @@ __global__ __launch_bounds__(256) void k_fp8_rows(QuantFp8Args a, uint32_t block
 
 // A tile of 128 rows and 128 columns: 32 sets of 16 lanes, four consecutive rows
 // each, so that a lane holds the codes of four rows of a column as one dword
-// when it turns the tile through LDS. Bound by the vector unit (four roundings an
-// element where rows and columns are wanted) and the tile's two barriers: 2000 x
-// 4096 bf16 by columns 11.7 us, both ways 18.0; blocks of 12288 x 4096 fp32 both
-// ways 54 us (302 MB, 5.6 TB/s).
+// when it turns the tile through LDS. Bound by its phases (load, maxima, barrier,
+// inverses, barrier, codes, turn, barrier, store), which little else covers: two
+// blocks a compute unit, the waves wait for 50 to 60% of their time, the vector unit
+// is busy for 45 to 50% of it. 2000 x 4096 bf16 by columns 12.1 us, both ways 19;
+// blocks of 12288 x 4096 fp32 both ways 54.5 us (302 MB, 5.5 TB/s).
 template <typename TX>
 __global__ __launch_bounds__(512) void k_fp8_tile(QuantFp8Args a, uint32_t blocks_k) {
   __shared__ float part[8][128];
@@ -230,7 +232,7 @@ __device__ __forceinline__ u32x4_t straight(const uint32_t (&w)[4], uint8_t* buf
 
 }  // namespace
 
-// (4096 x 4096 bf16 16.5 us: fp64 on the vector unit.)
+// (4096 x 4096 bf16 16.7 us: fp64 on the vector unit, busy 60% of the time.)
 template <typename TX>
 __global__ __launch_bounds__(256) void k_fp8_rows_rotated(QuantFp8Args a, uint32_t groups) {
   __shared__ __align__(16) uint8_t turn[16 * Q_SET_BYTES];
@@ -258,7 +260,8 @@ __global__ __launch_bounds__(256) void k_fp8_rows_rotated(QuantFp8Args a, uint32
 }
 
 // A tile of 128 rows and 256 columns, as k_fp8_tile; the four rows of a lane stay
-// in registers as fp64 (two waves a SIMD; 2000 x 4096 bf16 by columns 14.2 us).
+// in registers as fp64 (two waves a SIMD; 2000 x 4096 bf16 by columns 15.4 us, the
+// vector unit busy for a third of it: 256 blocks, one a compute unit).
 template <typename TX>
 __global__ __launch_bounds__(512, 2) void k_fp8_tile_rotated(QuantFp8Args a, uint32_t groups) {
   __shared__ __align__(16) uint8_t turn[32 * Q_SET_BYTES];

@@ -143,10 +143,10 @@ __device__ __forceinline__ void store_cols(T* p, int left, bool vec, const float
 // x 4096: 258 us with the scale of b loaded so, 200 through LDS). A wave reads
 // its fragments of b once a step and each of a one ahead of its use, and issues a
 // matrix instruction with the vector work of the previous fragment in its shadow.
-// Measured: 4096 x 12288 x 4096, bf16 C, 200 us, 2060 TFLOP/s (the instruction alone
-// 3800); 2000 x 4096 x 4096 40 us, 1680. With an fp32 C 4096 x 4096 x 4096 136 us,
-// 1010, and with a scale a row of b and k 2048 86 us, 800 (the bf16 instruction
-// alone 1830): there the widening and the folds, 3.5 to 4.5 vector instructions
+// Measured, calls in a row: 4096 x 12288 x 4096, bf16 C, 198 us, 2080 TFLOP/s (the
+// instruction alone 3800; 214 us between other kernels); 2000 x 4096 x 4096 39.5 us,
+// 1700. With an fp32 C 4096 x 4096 x 4096 140 us, 980, and with a scale a row of b
+// and k 2048 89 us, 770 (the bf16 instruction alone 1830): there the widening and the folds, 3.5 to 4.5 vector instructions
 // beside each matrix instruction, are the bound (two of them are free, four make a
 // bf16 instruction 11.8 ns instead of 7.9, two waves a SIMD; beside an 8-bit one of
 // 14.3 ns four make 16.3); widening each fragment of a beside the products of the
@@ -517,7 +517,9 @@ int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm
 // of a step of k (bf16 C, fp32 C):
 //   64 x 128    four stages, a block a compute unit: 0.42, 0.8 us
 //   128 x 128   two stages, two blocks a compute unit: 1.13, 2.8 us for both of
-//               them, 0.72, 1.4 for one that is alone
+//               them, 0.72, 1.4 for one that is alone (2.8 with a scale a row of b;
+//               with its blocks 2.1, which the rule does not tell apart: 1200 x 4096
+//               x 4096 takes 64 x 128 and 76 us, where 2.1 would give 67)
 //   256 x 256   two stages, a block a compute unit, bf16 C only (the widened
 //               fragments do not fit beside its sums): 2.05 us
 // and of a split product's join, 3 us and a write and a read of the partial sums

@@ -24,8 +24,9 @@ enum { LN_OUT_I8 = 0, LN_OUT_BF16 = 1, LN_OUT_FP8 = 2 };
 // Sums (or maxima) of N values over the threads of a row: all threads of the block
 // call it, with red [N][JOIN] of its own for each join of a row. Where a block
 // has one wide row its waves' results are met all at once (red holds zeros past
-// the last wave); short rows have at most three sets.
-constexpr int JOIN = 16;  // results of a join: the most waves, and the most sets of short rows
+// the last wave); rows that share a block (of up to three sets forward, of up to
+// eight in the gradients) are met set by set.
+constexpr int JOIN = 16;  // results of a join: the most waves, and the sets of a block of short rows
 
 template <int N, bool MAX, int WAVES>
 __device__ __forceinline__ void row_join(double (&v)[N], const Place& pl, int groups, double* red) {
@@ -109,8 +110,9 @@ __device__ __forceinline__ void afresh(float (&t)[N]) {
 // its stream, dropout, rotated bf16 rows: 33.5 -> 26.5 us, with the sums across lanes
 // on the vector unit).
 // bf16 rows are bound by HBM (those 26.5 us: 5.1 TB/s), codes by fp64 beside it
-// (e4m3 codes of 2000 x 8192, fp32 in, bf16 stream: 33.2 us, 4.5 TB/s), one row of
-// 4096 by its chain of three joins (4.4 us).
+// (e4m3 codes of 2000 x 8192, fp32 in, bf16 stream: 33.1 us, 4.5 TB/s; int8 codes with
+// their third join 36.7, 4.0 TB/s, rotated 39, and of 4096 x 4096 in bf16 with the
+// dropout, rotated, 38, 3.1 TB/s), one row of 4096 by its chain of three joins (4.3).
 template <typename TX, typename TS, bool RES, int OUT, int NT>
 __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_per_block, int64_t row0) {
   typedef typename std::conditional<OUT == LN_OUT_BF16, float, double>::type T;
@@ -323,11 +325,12 @@ __global__ __launch_bounds__(NT, 4) void k_layernorm(LayerNormArgs a, int rows_p
 // block; the blocks' sums are joined by k_colsum in a fixed order. Wide rows
 // (more than 16 groups) have no registers for that, and as many blocks as rows:
 // their kernel leaves mu and r of each row, and k_layernorm_dw takes the sums.
-// Measured: 4096 x 4096, fp32 dy, bf16 t, dsum and dx, with the dropout 45.8 us
+// Measured: 4096 x 4096, fp32 dy, bf16 t, dsum and dx, with the dropout 45.1 us
 // (HBM: 201 MB, 4.4 TB/s, three waves a SIMD: four spilled and were slower) and
-// 4.8 for the join of 512 partial rows; 333 x 12288 fp32 16.1 us (1.3 rows a
-// compute unit, each a chain of two joins), 8.3 for the sums' kernel (HBM: dy and t
-// again, from the last-level cache) and 3.8.
+// 4.4 for the join of 512 partial rows; 333 x 12288 fp32 15.7 us (1.3 rows a
+// compute unit, each a chain of two joins), 7.0 for the sums' kernel (dy and t
+// again, from the last-level cache) and 1.9 (minima of a trace; 50.8 and 5.1, 16.2,
+// 7.8 and 3.0 at the median).
 template <typename T>
 __device__ __forceinline__ void rotate_back(float (&g)[16], const Runs<T>& raw, float* buf, int l16) {
 #pragma unroll
