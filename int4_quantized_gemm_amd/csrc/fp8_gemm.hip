@@ -88,11 +88,17 @@ __device__ __forceinline__ i32x8_t join8(u32x4_t lo, u32x4_t hi) {
   return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
-// The exponent of a scale and 62: at most MID_SCALES where the scale is within 2^-63 ..
-// 2^62, or 0 (infinity and NaN too, whose products show whatever way they take). The
-// product of two such is 0 because one of them is, or a normal number.
+// The exponent of a scale and its side's bias: at most MID_SCALES for a scale of a
+// within 2^-85 .. 2^40, one of b within 2^-41 .. 2^84, or 0 (infinity and NaN too, whose
+// products show whatever way they take). The product of two such is 0 because one of
+// them is, or a normal number. (a has the room below: in the gradients it is the
+// smaller side. The least and the largest of either side, looked at together, leave
+// more room and took 2 to 5% more, in every product.)
 constexpr uint32_t MID_SCALES = 124;
-__device__ __forceinline__ uint32_t scale_reach(float s) { return (uint32_t)(__builtin_amdgcn_frexp_expf(s) + 62); }
+constexpr int A_BIAS = 84, B_BIAS = 40;
+__device__ __forceinline__ uint32_t scale_reach(float s, int bias) {
+  return (uint32_t)(__builtin_amdgcn_frexp_expf(s) + bias);  // s is 0.5 .. 1 times 2^it
+}
 
 // A block's sum folded into the results where its scales may not be such: a block's
 // sum is 0 or within 2^-18 .. 2^25, so p sa sb is often an ordinary number where fp32
@@ -314,8 +320,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void k_qgemm_fp8(Gem
           block_sums(wb, wa, p[i & 1]);
           if (FETCHED && i == FM - 2) own = ss[sl * 64 + lane];
           if (i > 0) fold(i - 1);
-          if (i == (FETCHED ? FM - 1 : 0)) reach = max(reach, scale_reach(own));
-          if constexpr (!FETCHED) reach = max(reach, scale_reach(sc[i]));
+          if (i == (FETCHED ? FM - 1 : 0)) reach = max(reach, scale_reach(own, FETCHED && sl < BM / 64 ? A_BIAS : B_BIAS));
+          if constexpr (!FETCHED) reach = max(reach, scale_reach(sc[i], A_BIAS));
 #pragma unroll
           for (int t = 0; t < MFMAS; ++t) {
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -333,8 +339,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void k_qgemm_fp8(Gem
     __builtin_amdgcn_s_waitcnt(VMCNT_ENCODE(0));  // no load to LDS outlives the block
   };
   walk(std::false_type{});
-  // The sums again, with fp64 where it is needed, where a scale of the block is far
-  // from 1 (as a branch in the loop: 258 spilled registers in the largest tile).
+  // The sums again, with fp64 where it is needed, where a scale of the block is that
+  // far from 1 (2.5 to 3 times the usual time; as a branch in the loop it spilled 258
+  // registers of the largest tile).
   __shared__ uint32_t far_waves[Cfg::NW];
   const uint64_t far_lanes = __ballot(reach > MID_SCALES);  // (of all lanes: not inside the branch)
   if (lane == 0) far_waves[wave] = far_lanes != 0;
@@ -454,11 +461,11 @@ __global__ __launch_bounds__(512, 1) void k_qgemm_fp8_few(GemmFp8Args g) {
         if (u > 0 && ks0 + NW * u >= KB) break;
         if constexpr (!WIDE) {
 #pragma unroll
-          for (int i = 0; i < FM; ++i) reach = max(reach, scale_reach(sc[u][i]));
+          for (int i = 0; i < FM; ++i) reach = max(reach, scale_reach(sc[u][i], A_BIAS));
 #pragma unroll
           for (int j = 0; j < (BROWS ? FN : 1); ++j)
 #pragma unroll
-            for (int e = 0; e < (BROWS ? 4 : 1); ++e) reach = max(reach, scale_reach(sbv[u][j][e]));
+            for (int e = 0; e < (BROWS ? 4 : 1); ++e) reach = max(reach, scale_reach(sbv[u][j][e], B_BIAS));
         }
         Frag<true> fb[FN], fa;
 #pragma unroll

@@ -77,3 +77,33 @@ def test_scale_products_beyond_fp32(m, n, k, rows, dtype):
     again = _call(a, strange, b, sb, rows, dtype, d)
     assert torch.equal(again[plain], got[plain]), "rows change with their neighbours' scales"
     assert np.all(np.isnan(f64(again)[ka == TINY]))
+
+
+# exponents of scales on either side of where the products change their way, and at the
+# ends of fp32
+A_EDGES = [-149, -127, -126, -125, -87, -86, -85, -84, -41, -1, 0, 39, 40, 41, 42, 100]
+B_EDGES = [-149, -126, -64, -43, -42, -41, -40, -39, 0, 14, 83, 84, 85, 86]
+
+
+@pytest.mark.parametrize("m,n", [(16, 40), (40, 200), (300, 300), (1999, 4093), (4093, 4091)])
+@pytest.mark.parametrize("rows", [128, 1])
+def test_scales_at_the_edges(m, n, rows):
+    """One block of whole numbers p under powers of two: p 2^e rounded once to fp32
+    (subnormal results too), exactly."""
+    d = dev()
+    announce("tp_qgemm_fp8 scales at the edges", m, n, rows)
+    rng = np.random.default_rng(m + n)
+    a, b = rng.integers(-8, 9, (m, 128)).astype(np.float64), rng.integers(-8, 9, (n, 128)).astype(np.float64)
+    ea = np.array(A_EDGES)[rng.integers(0, len(A_EDGES), m)]
+    eb = np.array(B_EDGES)[(np.arange(-(-n // 128)) + m) % len(B_EDGES) if rows == 128 else rng.integers(0, len(B_EDGES), n)]
+    e = ea[:, None] + (np.repeat(eb, 128)[:n] if rows == 128 else eb)[None, :]
+    p = a @ b.T
+    fits = e < 128 - 14  # |p| is at most 2^13
+    want = np.ldexp(np.where(fits, p, 0.0), np.where(fits, e, 0)).astype(np.float32)
+    power = lambda v: np.ldexp(1.0, v).astype(np.float32)  # noqa: E731
+    sa, sb = power(ea)[None, :], power(eb)[:, None] if rows == 128 else power(eb)[None, :]
+    for dtype in (F32, BF16):
+        got = _call(oracle.e4m3_code(a), sa, oracle.e4m3_code(b), sb, rows, dtype, d)
+        ref = torch.from_numpy(want).to(d).to(dtype)
+        bad = (got != ref) & torch.from_numpy(fits).to(d)
+        assert not torch.any(bad), f"{int(bad.sum())} values differ"
