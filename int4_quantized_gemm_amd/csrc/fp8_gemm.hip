@@ -152,11 +152,11 @@ __device__ __forceinline__ void store_cols(T* p, int left, bool vec, const float
 // Measured, calls in a row: 4096 x 12288 x 4096, bf16 C, 198 us, 2080 TFLOP/s (the
 // instruction alone 3800; 214 us between other kernels); 2000 x 4096 x 4096 39.5 us,
 // 1700. With an fp32 C 4096 x 4096 x 4096 140 us, 980, and with a scale a row of b
-// and k 2048 89 us, 770 (the bf16 instruction alone 1830): there the widening and the folds, 3.5 to 4.5 vector instructions
-// beside each matrix instruction, are the bound (two of them are free, four make a
-// bf16 instruction 11.8 ns instead of 7.9, two waves a SIMD; beside an 8-bit one of
-// 14.3 ns four make 16.3); widening each fragment of a beside the products of the
-// one before changed nothing (88 us).
+// and k 2048 89 us, 770 (the bf16 instruction alone 1830): there the widening and the
+// folds, 3.5 to 4.5 vector instructions beside each matrix instruction, are the bound
+// (two of them are free, four make a bf16 instruction 11.8 ns instead of 7.9, two
+// waves a SIMD; beside an 8-bit one of 14.3 ns four make 16.3); widening each fragment
+// of a beside the products of the one before changed nothing (88 us).
 template <int BM, int BN, int WM, int WN, int NS>
 struct F8Cfg {
   static constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, NT = 64 * NW;
